@@ -91,7 +91,8 @@ extern "C" {
 #define KV1B_STATUS_FP16_SATURATED 2  /* a value group's min or scale left the binary16 range */
 #define KV1B_STATUS_TIMEOUT 4         /* an attend kernel's bounded pipeline wait ran out (results invalid) */
 #define KV1B_STATUS_BAD_INDEX 8       /* kv1b_attend_selected_exact met a selected index outside the valid
-                                         tokens; that entry was skipped */
+                                         tokens, or a paged call a page, position or length outside its
+                                         range; that entry was skipped */
 
 /*
  * Cache descriptor.  Filled by kv1b_cache_init; treat as opaque except for reading the fields.
@@ -311,6 +312,123 @@ int kv1b_scores_probe(const kv1b_cache_t* cache, const void* q, int32_t q_dtype,
 int kv1b_attend_wait_probe(const kv1b_cache_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads,
                            float scale, float* out, void* ws, size_t ws_bytes, int32_t wait_tries,
                            int32_t stall_stage, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Paged cache: the same compressed keys and values for a serving batch -- sequences of uneven lengths
+ * whose tokens live in pages of one buffer, named by a page table on the device.  Nothing about the
+ * lengths is read on the host, so a captured CUDA graph replays with lengths, tables and inputs that
+ * change in place.  (The pages the library follows describe no paging, rotary positions, windows or
+ * shared prefixes; these exist for its users.)
+ *
+ * pages: u8 [num_pages][num_kv_heads][page_tokens / 32][3200], 128-byte aligned.  One 3,200-byte block
+ * holds 32 tokens of one kv-head:
+ *   bytes    0   key sign bits, u32 [32][4]: row 8 i + 2 t + e is token 8 t + 2 i + e; bit b of word w
+ *                is 1 iff channel 32 w + b of the rotated key is >= 0
+ *   bytes  512   f32 [32]: N * (1/C) of the token's key (the product of the two scalars)
+ *   bytes  640   f16 [4][32]: value scale per 32-channel group and token
+ *   bytes  896   f16 [4][32]: value min per group and token
+ *   bytes 1152   value codes, u32 [128][4]: nibble p of word w of channel c is the code of token
+ *                8 w + 2 p for p < 4, 8 w + 2 (p - 4) + 1 for p >= 4
+ * Blocks hold whatever the buffer held where no token was appended; no call reads a token at or past
+ * its sequence's length into a result.
+ */
+#define KV1B_PAGED_BLOCK_TOKENS 32
+#define KV1B_PAGED_BLOCK_BYTES 3200
+#define KV1B_PAGED_MAX_PAGE_TOKENS 4096
+#define KV1B_PAGED_MAX_SEQS 1024
+#define KV1B_PAGED_MAX_HEADS 1024
+#define KV1B_ROPE_MAX_AXES 3
+
+typedef struct kv1b_paged {
+  void* pages;
+  const float* signs;     /* f32 [3][128] rotation signs (+-1; 0 in the rounds past the last), 16-byte aligned */
+  int32_t* d_status;      /* i32 [1], OR of KV1B_STATUS_* bits; NULL: not recorded */
+  int32_t num_pages;
+  int32_t num_kv_heads;   /* <= KV1B_PAGED_MAX_HEADS */
+  int32_t page_tokens;    /* power of two, 32 .. KV1B_PAGED_MAX_PAGE_TOKENS */
+  int32_t reserved;
+} kv1b_paged_t;
+
+/* Rotary positions.  Pair i < rot_dim / 2 of a row is turned by the angle whose cos is
+ * cos_sin[pos][i] and whose sin is cos_sin[pos][rot_dim / 2 + i], pos the token's position on the
+ * pair's axis: the first sections[0] pairs take axis 0, the next sections[1] axis 1, the others axis 2
+ * (one axis for text; time, height and width for images and video).  A pair is channels (i, i +
+ * rot_dim / 2), or (2 i, 2 i + 1) when interleaved; channels from rot_dim on pass through:
+ *   a' = fl(fl(a cos) - fl(b sin)),  b' = fl(fl(b cos) + fl(a sin))   in fp32. */
+typedef struct kv1b_rope {
+  const float* cos_sin;   /* device, f32 [num_positions][rot_dim], 16-byte aligned */
+  int32_t num_positions;
+  int32_t rot_dim;        /* multiple of 8, 8 .. 128 */
+  int32_t axes;           /* 1 .. KV1B_ROPE_MAX_AXES */
+  int32_t interleaved;
+  int32_t sections[KV1B_ROPE_MAX_AXES];  /* sum: rot_dim / 2 */
+  int32_t reserved;
+} kv1b_rope_t;
+
+/* Bytes of the page buffer (0 if the shape is unsupported). */
+size_t kv1b_paged_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t head_dim, int32_t page_tokens);
+
+/* Draw the rotation signs (f32 [3][128], as kv1b_cache_init_rounds draws them) and zero the status
+ * word.  Asynchronous on `stream`. */
+int kv1b_paged_signs(float* signs, uint64_t seed, int32_t rounds, int32_t* d_status, void* stream);
+
+/* Encode new tokens of several sequences into their pages, with the rotary position applied to the
+ * keys on the way (fp32, no rounding before the encoder), and turn the same tokens' queries.
+ * k, v: element (t, h, c) at k[t*k_stride_t + h*k_stride_h + c] for token row t < num_tokens, type
+ *   `dtype`; bases 16-byte aligned, strides in elements, multiples of 4 (slices of one projection's
+ *   rows do).  cu_new: i32 [num_seqs + 1], ascending; sequence b appends rows cu_new[b] .. cu_new[b+1]-1
+ *   at its positions start[b], start[b] + 1, ... (start: i32 [num_seqs]; not advanced by the call).
+ *   Rows past cu_new[num_seqs] (padding) are not touched.
+ * page_table: i32, sequence b's page of positions [i page_tokens, (i+1) page_tokens) at
+ *   page_table[b*table_stride + i], i < max_pages.
+ * rope: NULL for none; positions: i32, token row t on axis a at positions[a*pos_stride + t].
+ * q, q_out: NULL, or the queries (element (t, h, c) at q[t*q_stride_t + h*q_stride_h + c], h <
+ *   num_q_heads) and where their turned rows go, in `dtype` (copied when rope is NULL; q_out may be q
+ *   with the same strides).
+ * Encoded as kv1b_encode_append, except that values are first limited to +-65504 (NaN to 0) and a
+ * group's scale is one binary16 step lower where min + 15 scale would pass 65504.
+ * Skipped, with KV1B_STATUS_BAD_INDEX: tokens whose page is outside [0, num_pages) or past max_pages,
+ * tokens with a position outside the rotary table, and all new tokens of a sequence whose cu_new or
+ * start entries are not valid.  KV1B_STATUS_NONFINITE / _FP16_SATURATED as kv1b_encode_append.
+ * Two sequences of one call must not write the same page. */
+int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, int32_t dtype, int32_t num_tokens,
+                      int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h, int32_t num_seqs,
+                      const int32_t* cu_new, const int32_t* start, const int32_t* page_table, int64_t table_stride,
+                      int32_t max_pages, const kv1b_rope_t* rope, const int32_t* positions, int64_t pos_stride,
+                      const void* q, void* q_out, int32_t num_q_heads, int64_t q_stride_t, int64_t q_stride_h,
+                      int64_t qo_stride_t, int64_t qo_stride_h, void* stream);
+
+/* Workspace bytes of kv1b_paged_attend / kv1b_paged_attend_shared (0 on invalid arguments). */
+size_t kv1b_paged_attend_workspace_bytes(const kv1b_paged_t* cache, int32_t num_q_heads);
+size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_seqs, int32_t num_q_heads);
+
+/* Decode attention over a page table: one query token per sequence.
+ * q: [num_seqs][num_q_heads][128] contiguous, KV1B_DTYPE_BF16 or _F16, 16-byte aligned; out: the same
+ *   shape and type.  (An fp32 query is KV1B_ERR_UNSUPPORTED: weights and expanded values enter the
+ *   tensor cores as binary16, which an fp32 output would promise too much for; kv1b_attend takes it.)
+ * lengths: i32 [num_seqs], tokens each sequence holds (the query is the last of them); values below 0
+ *   or past max_pages * page_tokens are limited to that range, with KV1B_STATUS_BAD_INDEX.
+ * window, sinks: window = 0 sees every token; window > 0 sees token t iff t >= length - window or
+ *   t < sinks.
+ * Logits and softmax as kv1b_attend.  Zeros for a sequence of length 0.  Blocks whose page is outside
+ *   [0, num_pages) count as unseen, with KV1B_STATUS_BAD_INDEX.
+ * ws: 256-byte aligned, kv1b_paged_attend_workspace_bytes; written and read within the call only.
+ *   Calls that may overlap on the GPU need workspaces of their own. */
+int kv1b_paged_attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
+                      int32_t num_seqs, const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                      const int32_t* lengths, int32_t window, int32_t sinks, void* out, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Decode attention for a batch whose sequences all begin with the same tokens: sequence b sees the
+ * prefix (prefix_length[0] tokens, a device i32, in pages prefix_pages[0 .. max_prefix_pages)), then
+ * its own lengths[b] tokens in its row of page_table, which starts a page of its own.  Equal to
+ * kv1b_paged_attend over the concatenation, but the prefix is read once for the whole batch.
+ * Arguments otherwise as kv1b_paged_attend; either part may be empty. */
+int kv1b_paged_attend_shared(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
+                             int32_t num_seqs, const int32_t* prefix_pages, int32_t max_prefix_pages,
+                             const int32_t* prefix_length, const int32_t* page_table, int64_t table_stride,
+                             int32_t max_pages, const int32_t* lengths, void* out, void* ws, size_t ws_bytes,
+                             void* stream);
 
 /* Synchronous: waits for `stream`, then copies the cache's status word to *flags (host). */
 int kv1b_read_status(const kv1b_cache_t* cache, int32_t* flags, void* stream);

@@ -25,6 +25,7 @@ PART_ROW = 2 + 128
 STATUS_TIMEOUT = 4
 PROBE_POPC, PROBE_ATTEND, PROBE_TOPP = 0, 1, 2
 STATUS_NONFINITE, STATUS_FP16_SATURATED = 1, 2
+STATUS_BAD_INDEX = 8
 ERRORS = {0: "ok", -1: "invalid argument", -2: "unsupported", -3: "capacity", -4: "misaligned",
           -5: "workspace too small", -6: "CUDA error"}
 
@@ -33,7 +34,9 @@ SYMBOLS = ("kv1b_cache_bytes", "kv1b_cache_init", "kv1b_cache_init_rounds", "kv1
            "kv1b_attend", "kv1b_attend_noalloc", "kv1b_attend_topp", "kv1b_attend_select",
            "kv1b_attend_selected_exact",
            "kv1b_merge_partials", "kv1b_query_prep", "kv1b_scores", "kv1b_scores_probe", "kv1b_attend_wait_probe",
-           "kv1b_read_status", "kv1b_status_string", "kv1b_version")
+           "kv1b_read_status", "kv1b_status_string", "kv1b_version",
+           "kv1b_paged_bytes", "kv1b_paged_signs", "kv1b_paged_append", "kv1b_paged_attend_workspace_bytes",
+           "kv1b_paged_attend", "kv1b_paged_shared_workspace_bytes", "kv1b_paged_attend_shared")
 
 
 class Kv1bError(RuntimeError):
@@ -86,6 +89,14 @@ def lib() -> ctypes.CDLL:
             "kv1b_read_status": (ctypes.c_int, [D, P, P]),
             "kv1b_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "kv1b_version": (ctypes.c_int, []),
+            "kv1b_paged_bytes": (sz, [i32, i32, i32, i32]),
+            "kv1b_paged_signs": (ctypes.c_int, [P, ctypes.c_uint64, i32, P, P]),
+            "kv1b_paged_append": (ctypes.c_int, [P, P, P, i32, i32, i64, i64, i64, i64, i32, P, P, P, i64, i32, P, P, i64,
+                                                 P, P, i32, i64, i64, i64, i64, P]),
+            "kv1b_paged_attend_workspace_bytes": (sz, [P, i32]),
+            "kv1b_paged_attend": (ctypes.c_int, [P, P, i32, i32, f32, i32, P, i64, i32, P, i32, i32, P, P, sz, P]),
+            "kv1b_paged_shared_workspace_bytes": (sz, [P, i32, i32]),
+            "kv1b_paged_attend_shared": (ctypes.c_int, [P, P, i32, i32, f32, i32, P, i32, P, P, i64, i32, P, P, P, sz, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -420,3 +431,6 @@ def unpack_codes(v_codes: torch.Tensor, length: int) -> torch.Tensor:
     nib = (w[..., None] >> shifts) & 0xF                             # [tiles, 128 ch, 16 words, 8]
     out = nib.permute(0, 2, 3, 1).reshape(ntile * 128, HEAD_DIM)     # token = 128 tile + 8 word + j
     return out[:length].to(torch.uint8)
+
+
+from .paged import PagedCache, Rope  # noqa: E402,F401

@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 SO = os.path.join(PKG, "libkv1b.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "--fmad=false", "-std=c++17",
+    "-O3", "--threads=0", "-lineinfo", "--fmad=false", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
 ]
 

@@ -1,0 +1,85 @@
+// kv1b_paged.h -- internal interface of the paged-cache kernels: the block format, parameter blocks
+// and launchers.
+//
+// A block holds 32 tokens of one kv-head in 3,200 contiguous bytes, so that one untiled bulk copy
+// brings everything a warp needs for its tokens and a page of any multiple of 32 tokens is a row of
+// blocks.  Inside a block the planes are laid out for the attend's tensor-core fragments:
+//   sign bits  row 8 i + 2 t + e is token 8 t + 2 i + e, so that the eight rows of score product i are
+//              128 contiguous bytes (one ldmatrix) and lane t of a quad receives the logits of tokens
+//              8 t .. 8 t + 7, the tokens of its code words;
+//   codes      nibbles p and p + 4 of word w are tokens 8 w + 2 p and 8 w + 2 p + 1, so that one mask
+//              of a word gives a pair of neighbouring tokens in the two halves of a register.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kv1b.h"
+#include "kv1b_launch.h"
+
+namespace kv1b {
+
+constexpr int kBlkTok = KV1B_PAGED_BLOCK_TOKENS;
+constexpr int kBlkBytes = KV1B_PAGED_BLOCK_BYTES;
+constexpr int kBlkOffNc = 512;      // f32 [32]  N / C
+constexpr int kBlkOffScale = 640;   // f16 [4][32]
+constexpr int kBlkOffMin = 896;     // f16 [4][32]
+constexpr int kBlkOffCodes = 1152;  // u32 [128][4]
+static_assert(kBlkTok == 32 && kBlkOffCodes + KV1B_HEAD_DIM * 16 == kBlkBytes && kBlkBytes % 16 == 0, "block layout");
+
+struct PagedView {
+  uint8_t* pages;
+  const float* signs;
+  int32_t* status;     // optional
+  int32_t num_pages, Hkv;
+  int32_t bpp_shift;   // log2 of the blocks per page
+};
+
+struct PagedAppendParams {
+  PagedView c;
+  const void* k;
+  const void* v;
+  int64_t k_st, k_sh, v_st, v_sh;  // element strides: token, head
+  int32_t dtype;
+  int32_t T, B;
+  const int32_t* cu;       // [B + 1] first row of each sequence's new tokens
+  const int32_t* start;    // [B] tokens each sequence holds already
+  const int32_t* table;    // [B][table_stride]
+  int64_t table_stride;
+  int32_t max_pages;
+  // rotary positions (cos_sin null: none)
+  const float* cos_sin;    // [positions][rot]: cos of pair i at i, sin at rot / 2 + i
+  int32_t cs_rows, rot, interleaved;
+  int32_t sec0, sec01;     // pairs below sec0 take axis 0, below sec01 axis 1, the others axis 2
+  const int32_t* pos;      // [axes][pos_stride]
+  int64_t pos_stride;
+  // queries to rotate (q null: none)
+  const void* q;
+  void* q_out;
+  int64_t q_st, q_sh, qo_st, qo_sh;
+  int32_t Hq;
+  int32_t groups;          // bound of the 8-token groups of all sequences
+};
+
+struct PagedAttendParams {
+  PagedView c;
+  const void* q;
+  int32_t q_dtype;
+  int32_t Hq, B;
+  float scale;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t max_pages;
+  const int32_t* lengths;
+  int32_t window, sinks;
+  const int32_t* prefix_pages;  // optional shared prefix: its pages and (device) token count
+  const int32_t* prefix_len;
+  int32_t max_prefix_pages;
+  void* out;               // q_dtype [B][Hq][128]
+  float* part;             // [ctas][2][G][2 + 128]
+  int32_t ncta;
+};
+
+}  // namespace kv1b
+
+cudaError_t kv1b_launch_paged_append(const kv1b::PagedAppendParams& p, cudaStream_t stream);
+cudaError_t kv1b_launch_paged_attend(const kv1b::PagedAttendParams& p, int32_t G, cudaStream_t stream);

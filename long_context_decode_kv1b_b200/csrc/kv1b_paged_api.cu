@@ -1,0 +1,231 @@
+// kv1b_paged_api.cu -- the paged-cache entry points of include/kv1b.h: argument checks on the host,
+// then launches on the caller's stream.  Nothing here allocates device memory or synchronises.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "kv1b.h"
+#include "kv1b_launch.h"
+#include "kv1b_paged.h"
+
+namespace {
+
+constexpr int64_t kMaxBlocks = 1LL << 30;  // blocks of one kv-head that a call's page tables may name
+
+bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
+bool dtype_ok(int32_t dt) { return dt == KV1B_DTYPE_F32 || dt == KV1B_DTYPE_BF16 || dt == KV1B_DTYPE_F16; }
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? KV1B_OK : KV1B_ERR_CUDA; }
+
+int log2_exact(int32_t x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+bool page_tokens_ok(int32_t n) {
+  return n >= KV1B_PAGED_BLOCK_TOKENS && n <= KV1B_PAGED_MAX_PAGE_TOKENS && (n & (n - 1)) == 0;
+}
+
+bool paged_ok(const kv1b_paged_t* c) {
+  return c && c->pages && c->signs && c->num_pages >= 1 && c->num_kv_heads >= 1 && c->num_kv_heads <= KV1B_PAGED_MAX_HEADS &&
+         page_tokens_ok(c->page_tokens) && aligned(c->pages, 128) && aligned(c->signs, 16);
+}
+
+kv1b::PagedView view(const kv1b_paged_t* c) {
+  kv1b::PagedView v;
+  v.pages = static_cast<uint8_t*>(c->pages);
+  v.signs = c->signs;
+  v.status = c->d_status;
+  v.num_pages = c->num_pages;
+  v.Hkv = c->num_kv_heads;
+  v.bpp_shift = log2_exact(c->page_tokens / KV1B_PAGED_BLOCK_TOKENS);
+  return v;
+}
+
+int num_sms() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (cached[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
+int heads_check(const kv1b_paged_t* c, int32_t num_q_heads) {
+  if (num_q_heads < 1 || num_q_heads % c->num_kv_heads != 0) return KV1B_ERR_INVALID_ARG;
+  if (num_q_heads / c->num_kv_heads > KV1B_MAX_GROUP) return KV1B_ERR_UNSUPPORTED;
+  return KV1B_OK;
+}
+
+int table_check(const kv1b_paged_t* c, int32_t num_seqs, int64_t table_stride, int32_t max_pages, int32_t prefix_pages) {
+  if (num_seqs < 1 || max_pages < 1 || table_stride < 0 || prefix_pages < 0) return KV1B_ERR_INVALID_ARG;
+  if (num_seqs > 1 && table_stride < max_pages) return KV1B_ERR_INVALID_ARG;
+  if (num_seqs > KV1B_PAGED_MAX_SEQS) return KV1B_ERR_UNSUPPORTED;
+  const int64_t bpp = c->page_tokens / KV1B_PAGED_BLOCK_TOKENS;
+  if (num_seqs * bpp * (static_cast<int64_t>(max_pages) + prefix_pages) > kMaxBlocks) return KV1B_ERR_UNSUPPORTED;
+  if (bpp * max_pages * KV1B_PAGED_BLOCK_TOKENS > 0x7fffffff || bpp * prefix_pages * KV1B_PAGED_BLOCK_TOKENS > 0x7fffffff)
+    return KV1B_ERR_UNSUPPORTED;
+  return KV1B_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kv1b_paged_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t head_dim, int32_t page_tokens) {
+  if (num_pages < 1 || num_kv_heads < 1 || num_kv_heads > KV1B_PAGED_MAX_HEADS || head_dim != KV1B_HEAD_DIM ||
+      !page_tokens_ok(page_tokens))
+    return 0;
+  return static_cast<size_t>(num_pages) * num_kv_heads * (page_tokens / KV1B_PAGED_BLOCK_TOKENS) * KV1B_PAGED_BLOCK_BYTES;
+}
+
+int kv1b_paged_signs(float* signs, uint64_t seed, int32_t rounds, int32_t* d_status, void* stream) {
+  if (!signs || !d_status || rounds < 1 || rounds > KV1B_MAX_ROUNDS) return KV1B_ERR_INVALID_ARG;
+  if (!aligned(signs, 16) || !aligned(d_status, 4)) return KV1B_ERR_MISALIGNED;
+  return cuda_status(kv1b_launch_init(seed, rounds, signs, nullptr, 0, d_status, static_cast<cudaStream_t>(stream)));
+}
+
+int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, int32_t dtype, int32_t num_tokens,
+                      int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h, int32_t num_seqs,
+                      const int32_t* cu_new, const int32_t* start, const int32_t* page_table, int64_t table_stride,
+                      int32_t max_pages, const kv1b_rope_t* rope, const int32_t* positions, int64_t pos_stride,
+                      const void* q, void* q_out, int32_t num_q_heads, int64_t q_stride_t, int64_t q_stride_h,
+                      int64_t qo_stride_t, int64_t qo_stride_h, void* stream) {
+  if (!paged_ok(cache) || !k || !v || !dtype_ok(dtype) || num_tokens < 0 || !cu_new || !start || !page_table)
+    return KV1B_ERR_INVALID_ARG;
+  const int tc = table_check(cache, num_seqs, table_stride, max_pages, 0);
+  if (tc != KV1B_OK) return tc;
+  if (k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0) return KV1B_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride_t % 4 || k_stride_h % 4 || v_stride_t % 4 || v_stride_h % 4)
+    return KV1B_ERR_MISALIGNED;
+  if (!aligned(cu_new, 4) || !aligned(start, 4) || !aligned(page_table, 4)) return KV1B_ERR_MISALIGNED;
+  if (num_tokens > (1 << 28)) return KV1B_ERR_UNSUPPORTED;
+  kv1b::PagedAppendParams p;
+  memset(&p, 0, sizeof(p));
+  if (rope) {
+    if (!rope->cos_sin || !positions || rope->num_positions < 1 || rope->rot_dim < 8 || rope->rot_dim > KV1B_HEAD_DIM ||
+        rope->axes < 1 || rope->axes > KV1B_ROPE_MAX_AXES || pos_stride < 0 || (rope->axes > 1 && pos_stride < num_tokens))
+      return KV1B_ERR_INVALID_ARG;
+    if (rope->rot_dim % 8) return KV1B_ERR_UNSUPPORTED;
+    int sum = 0;
+    for (int a = 0; a < rope->axes; ++a) {
+      if (rope->sections[a] < 0) return KV1B_ERR_INVALID_ARG;
+      sum += rope->sections[a];
+    }
+    if (sum != rope->rot_dim / 2) return KV1B_ERR_INVALID_ARG;
+    if (!aligned(rope->cos_sin, 16) || !aligned(positions, 4)) return KV1B_ERR_MISALIGNED;
+    p.cos_sin = rope->cos_sin;
+    p.cs_rows = rope->num_positions;
+    p.rot = rope->rot_dim;
+    p.interleaved = rope->interleaved ? 1 : 0;
+    p.sec0 = rope->sections[0];
+    p.sec01 = p.sec0 + (rope->axes > 1 ? rope->sections[1] : 0);
+    p.pos = positions;
+    p.pos_stride = pos_stride;
+  }
+  if (q || q_out) {
+    if (!q || !q_out || q_stride_t < 0 || q_stride_h < 0 || qo_stride_t < 0 || qo_stride_h < 0) return KV1B_ERR_INVALID_ARG;
+    if (num_q_heads < 1 || num_q_heads > KV1B_PAGED_MAX_HEADS) return KV1B_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(num_tokens) * num_q_heads > (1LL << 33)) return KV1B_ERR_UNSUPPORTED;  // rows of one launch
+    if (!aligned(q, 16) || !aligned(q_out, 16) || q_stride_t % 4 || q_stride_h % 4 || qo_stride_t % 4 || qo_stride_h % 4)
+      return KV1B_ERR_MISALIGNED;
+    p.q = q;
+    p.q_out = q_out;
+    p.Hq = num_q_heads;
+    p.q_st = q_stride_t;
+    p.q_sh = q_stride_h;
+    p.qo_st = qo_stride_t;
+    p.qo_sh = qo_stride_h;
+  }
+  if (num_tokens == 0) return KV1B_OK;
+  p.c = view(cache);
+  p.k = k;
+  p.v = v;
+  p.k_st = k_stride_t;
+  p.k_sh = k_stride_h;
+  p.v_st = v_stride_t;
+  p.v_sh = v_stride_h;
+  p.dtype = dtype;
+  p.T = num_tokens;
+  p.B = num_seqs;
+  p.cu = cu_new;
+  p.start = start;
+  p.table = page_table;
+  p.table_stride = table_stride;
+  p.max_pages = max_pages;
+  p.groups = num_tokens / 8 + 2 * num_seqs;
+  return cuda_status(kv1b_launch_paged_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kv1b_paged_attend_workspace_bytes(const kv1b_paged_t* cache, int32_t num_q_heads) {
+  if (!paged_ok(cache) || heads_check(cache, num_q_heads) != KV1B_OK) return 0;
+  const size_t G = num_q_heads / cache->num_kv_heads;
+  const size_t n = static_cast<size_t>(num_sms()) * 2 * G * kv1b::kPartStride * 4;
+  return (n + 255) / 256 * 256;
+}
+
+static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
+                  int32_t num_seqs, const int32_t* prefix_pages, int32_t max_prefix_pages, const int32_t* prefix_length,
+                  const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* lengths,
+                  int32_t window, int32_t sinks, void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!paged_ok(cache) || !q || !out || !ws || !page_table || !lengths || !dtype_ok(q_dtype)) return KV1B_ERR_INVALID_ARG;
+  if (q_dtype == KV1B_DTYPE_F32) return KV1B_ERR_UNSUPPORTED;
+  const int hc = heads_check(cache, num_q_heads);
+  if (hc != KV1B_OK) return hc;
+  const int tc = table_check(cache, num_seqs, table_stride, max_pages, max_prefix_pages);
+  if (tc != KV1B_OK) return tc;
+  if (!(scale == scale) || window < 0 || sinks < 0) return KV1B_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(page_table, 4) || !aligned(lengths, 4) ||
+      !aligned(prefix_pages, 4) || !aligned(prefix_length, 4))
+    return KV1B_ERR_MISALIGNED;
+  if (ws_bytes < kv1b_paged_attend_workspace_bytes(cache, num_q_heads)) return KV1B_ERR_WORKSPACE;
+  kv1b::PagedAttendParams p;
+  memset(&p, 0, sizeof(p));
+  p.c = view(cache);
+  p.q = q;
+  p.q_dtype = q_dtype;
+  p.Hq = num_q_heads;
+  p.B = num_seqs;
+  p.scale = scale;
+  p.table = page_table;
+  p.table_stride = table_stride;
+  p.max_pages = max_pages;
+  p.lengths = lengths;
+  p.window = window;
+  p.sinks = sinks;
+  p.prefix_pages = prefix_pages;
+  p.prefix_len = prefix_length;
+  p.max_prefix_pages = max_prefix_pages;
+  p.out = out;
+  p.part = static_cast<float*>(ws);
+  p.ncta = num_sms();
+  return cuda_status(kv1b_launch_paged_attend(p, num_q_heads / cache->num_kv_heads, static_cast<cudaStream_t>(stream)));
+}
+
+int kv1b_paged_attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
+                      int32_t num_seqs, const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                      const int32_t* lengths, int32_t window, int32_t sinks, void* out, void* ws, size_t ws_bytes,
+                      void* stream) {
+  return attend(cache, q, q_dtype, num_q_heads, scale, num_seqs, nullptr, 0, nullptr, page_table, table_stride, max_pages,
+                lengths, window, sinks, out, ws, ws_bytes, stream);
+}
+
+size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_seqs, int32_t num_q_heads) {
+  if (num_seqs < 1 || num_seqs > KV1B_PAGED_MAX_SEQS) return 0;
+  return kv1b_paged_attend_workspace_bytes(cache, num_q_heads);
+}
+
+int kv1b_paged_attend_shared(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
+                             int32_t num_seqs, const int32_t* prefix_pages, int32_t max_prefix_pages,
+                             const int32_t* prefix_length, const int32_t* page_table, int64_t table_stride,
+                             int32_t max_pages, const int32_t* lengths, void* out, void* ws, size_t ws_bytes,
+                             void* stream) {
+  if (!prefix_pages || !prefix_length || max_prefix_pages < 1) return KV1B_ERR_INVALID_ARG;
+  return attend(cache, q, q_dtype, num_q_heads, scale, num_seqs, prefix_pages, max_prefix_pages, prefix_length, page_table,
+                table_stride, max_pages, lengths, 0, 0, out, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

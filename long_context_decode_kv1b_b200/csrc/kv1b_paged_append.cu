@@ -1,0 +1,448 @@
+// kv1b_paged_append.cu -- encode new tokens into a paged cache, with the rotary position applied to
+// the key on the way in and, in the same call, to the queries.
+//
+// Rotary embedding, pair i of a row: a' = fl(fl(a cos) - fl(b sin)), b' = fl(fl(b cos) + fl(a sin)) in
+// fp32, cos and sin from the caller's table at the position of the pair's axis.  The turned key goes to
+// the encoder in fp32 without a rounding in between.  Encoder: as kv1b_encode.cu (rotation, sign bits,
+// N and 1/C kept as their product, 4-bit values), in the same fixed orders, so every stored bit is
+// reproducible; values are first limited to the finite binary16 range and a group's scale is lowered
+// by one step where min + 15 scale would leave it, so that a reader may expand values to binary16.
+//
+// Work is split in groups of 8 aligned tokens of one sequence and kv-head: the tokens that share a
+// 32-bit word of every channel's codes, so one warp owns every word it rewrites.
+#include "kv1b_device.cuh"
+#include "kv1b_encode_q4.cuh"
+#include "kv1b_paged.h"
+
+namespace kv1b {
+namespace paged {
+
+constexpr float kF16Max = 65504.0f;
+
+__device__ __forceinline__ float limit_value(float v) {
+  return v == v ? fminf(fmaxf(v, -kF16Max), kF16Max) : 0.0f;
+}
+
+// Sequence, first position and positions of the group with index `gi`.  Sequence b owns the indices
+// from cu[b] / 8 + 2 b on: its n tokens touch at most floor(n / 8) + 2 groups, so the ranges never
+// overlap, and both the sequence and the group follow from cu without a prefix sum.
+struct Group {
+  int b;
+  int row0;          // row of the sequence's first new token
+  int64_t L0, L1;    // positions [L0, L1) are new
+  int64_t g0;        // first position of the group
+  bool any;
+};
+
+__device__ __forceinline__ Group find_group(const PagedAppendParams& p, int gi) {
+  const int lane = threadIdx.x & 31;
+  // the last sequence whose first index is <= gi: two rounds of 32 probes (B <= 1024)
+  int lo = 0;
+  if (p.B > 32) {
+    const int step = (p.B + 31) / 32;
+    const int b = lane * step;
+    const bool le = b < p.B && (__ldg(p.cu + b) >> 3) + 2 * b <= gi;
+    const unsigned m = __ballot_sync(kFull, le);
+    lo = m ? (31 - __clz(m)) * step : 0;
+  }
+  const int bb = lo + lane;
+  const int mine = bb < p.B ? __ldg(p.cu + bb) : 0x7fffffff;
+  const bool le2 = bb < p.B && (mine >> 3) + 2 * bb <= gi;
+  const unsigned m2 = __ballot_sync(kFull, le2);
+  const int off = m2 ? 31 - __clz(m2) : 0;
+  Group g;
+  g.b = lo + off;
+  g.row0 = __shfl_sync(kFull, mine, off);
+  const int row1 = __ldg(p.cu + g.b + 1);
+  const int first = __ldg(p.start + g.b);
+  const bool ok = g.row0 >= 0 && row1 >= g.row0 && row1 <= p.T && first >= 0;
+  if (!ok && lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+  g.L0 = first;
+  g.L1 = g.L0 + (ok ? row1 - g.row0 : 0);
+  g.g0 = ((g.L0 >> 3) + (gi - ((g.row0 >> 3) + 2 * g.b))) << 3;
+  g.any = ok && g.g0 < g.L1 && g.g0 + 8 > g.L0;
+  return g;
+}
+
+// The block of position `pos` of sequence b and kv-head h, or null (flagged) if its page is not there.
+__device__ __forceinline__ uint8_t* block_of(const PagedAppendParams& p, int b, int h, int64_t pos) {
+  const int64_t blk = pos >> 5;
+  const int64_t lp = blk >> p.c.bpp_shift;
+  const int page = lp < p.max_pages ? __ldg(p.table + b * p.table_stride + lp) : -1;
+  if (page < 0 || page >= p.c.num_pages) return nullptr;
+  const int64_t in = blk & ((1 << p.c.bpp_shift) - 1);
+  return p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + h) << p.c.bpp_shift) + in) * kBlkBytes);
+}
+
+// Rotary table indices of channel c < rot: pair, and the row of its axis.
+__device__ __forceinline__ int axis_of(const PagedAppendParams& p, int pair) {
+  return (pair >= p.sec0 ? 1 : 0) + (pair >= p.sec01 ? 1 : 0);
+}
+
+// Positions of row t on the three axes (the same for unused ones); false if one is outside the table.
+__device__ __forceinline__ bool positions(const PagedAppendParams& p, int64_t t, int (&ps)[3]) {
+  const int half = p.rot >> 1;
+  ps[0] = __ldg(p.pos + t);
+  ps[1] = p.sec0 < half ? __ldg(p.pos + p.pos_stride + t) : ps[0];
+  ps[2] = p.sec01 < half ? __ldg(p.pos + 2 * p.pos_stride + t) : ps[0];
+  const int n = p.cs_rows;
+  return ps[0] >= 0 && ps[0] < n && ps[1] >= 0 && ps[1] < n && ps[2] >= 0 && ps[2] < n;
+}
+
+__device__ __forceinline__ void store4(void* base, int64_t off, int dtype, const float x[4]) {
+  if (dtype == KV1B_DTYPE_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + off) = make_float4(x[0], x[1], x[2], x[3]);
+    return;
+  }
+  uint32_t h[4];
+  #pragma unroll
+  for (int r = 0; r < 4; ++r)
+    h[r] = dtype == KV1B_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x[r])) : __half_as_ushort(__float2half_rn(x[r]));
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + off) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// Rotary turn of one row held by a warp (lane l: channels 4l .. 4l + 3).  rot is a multiple of 8, so in
+// the half-split form the partner of a lane's channels are another lane's four.
+__device__ __forceinline__ void rope_warp(const PagedAppendParams& p, const int (&ps)[3], float (&x)[4]) {
+  const int lane = threadIdx.x & 31, half = p.rot >> 1;
+  const int c0 = 4 * lane;
+  const bool in = c0 < p.rot;
+  if (p.interleaved) {
+    if (!in) return;
+    #pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = 2 * lane + u;
+      const float* row = p.cos_sin + static_cast<int64_t>(ps[axis_of(p, i)]) * p.rot;
+      const float c = __ldg(row + i), s = __ldg(row + half + i);
+      const float a = x[2 * u], b = x[2 * u + 1];
+      x[2 * u] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+      x[2 * u + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    }
+    return;
+  }
+  const bool upper = c0 >= half;
+  const int src = in ? (upper ? lane - (half >> 2) : lane + (half >> 2)) : lane;
+  #pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float o = __shfl_sync(kFull, x[r], src);
+    if (in) {
+      const int i = c0 + r - (upper ? half : 0);
+      const float* row = p.cos_sin + static_cast<int64_t>(ps[axis_of(p, i)]) * p.rot;
+      const float c = __ldg(row + i), s = __ldg(row + half + i);
+      x[r] = upper ? __fadd_rn(__fmul_rn(x[r], c), __fmul_rn(o, s)) : __fsub_rn(__fmul_rn(x[r], c), __fmul_rn(o, s));
+    }
+  }
+}
+
+// One query row by the calling warp.
+__device__ __forceinline__ void query_row(const PagedAppendParams& p, int64_t t, int h) {
+  const int lane = threadIdx.x & 31;
+  float x[4];
+  load4(p.q, t * p.q_st + h * p.q_sh + 4 * lane, p.dtype, x);
+  if (p.cos_sin) {
+    int ps[3];
+    if (!positions(p, t, ps)) {
+      if (lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+      return;
+    }
+    rope_warp(p, ps, x);
+  }
+  store4(p.q_out, t * p.qo_st + h * p.qo_sh + 4 * lane, p.dtype, x);
+}
+
+// Scale and min of a value group from its limited extremes.
+__device__ __forceinline__ void group_scale(float mn, float mx, uint32_t* scale_bits, uint32_t* min_bits, bool walk) {
+  int sat = 0;
+  *min_bits = half_round_down(mn, &sat);
+  const float mf = __half2float(__ushort_as_half(static_cast<unsigned short>(*min_bits)));
+  uint32_t s = walk ? half_scale_up(mx, mf, &sat) : half_scale_up_fast(mx, mf, &sat);
+  // one step down where the top code would leave the binary16 range: exact in fp64
+  if (static_cast<double>(mf) + 15.0 * half_bits_to_double(s) > 65504.0) --s;
+  *scale_bits = s;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Decode form: one warp per (group, kv-head) and half (key or value), 32 lanes x 4 channels, the
+// group's new tokens one after another (one, in a decode step); then one warp per query row.  The
+// chain of dependent loads (cu, start, page, old words) is what a step waits for.
+__global__ void __launch_bounds__(128) paged_append_token_kernel(const PagedAppendParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t kv_units = 2LL * p.groups * p.c.Hkv;
+  if (unit >= kv_units) {
+    const int64_t r = unit - kv_units;
+    if (!p.q || r >= static_cast<int64_t>(p.T) * p.Hq) return;
+    const int64_t t = r / p.Hq;
+    if (t >= __ldg(p.cu + p.B)) return;  // rows behind the last sequence
+    query_row(p, t, static_cast<int>(r - t * p.Hq));
+    return;
+  }
+  const int h = static_cast<int>(unit % p.c.Hkv);
+  const int64_t gv = unit / p.c.Hkv;
+  const bool value = (gv & 1) != 0;
+  const Group g = find_group(p, static_cast<int>(gv >> 1));
+  if (!g.any) return;
+  int flags = 0;
+  uint8_t* blk = block_of(p, g.b, h, g.g0);
+  const int w = static_cast<int>(g.g0 & 31) >> 3;  // the group's code word of each row
+  uint32_t* words = reinterpret_cast<uint32_t*>(blk + kBlkOffCodes) + w;
+  uint32_t cw[4];
+  if (blk && value) {
+    #pragma unroll
+    for (int r = 0; r < 4; ++r) cw[r] = words[(4 * lane + r) * 4];
+  }
+  bool wrote = false;
+  #pragma unroll 1
+  for (int64_t pos = g.g0 < g.L0 ? g.L0 : g.g0; pos < g.L1 && pos < g.g0 + 8; ++pos) {
+    const int64_t t = g.row0 + (pos - g.L0);
+    const int tok = static_cast<int>(pos & 31);
+    int ps[3] = {0, 0, 0};
+    const bool ok = (!p.cos_sin || positions(p, t, ps)) && blk;
+    if (!ok) {
+      flags |= KV1B_STATUS_BAD_INDEX;
+      continue;
+    }
+    float x[4];
+    if (!value) {
+      load4(p.k, t * p.k_st + h * p.k_sh + 4 * lane, p.dtype, x);
+      if (p.cos_sin) rope_warp(p, ps, x);
+      float sq[4], ab[4];
+      #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        sq[r] = __fmul_rn(x[r], x[r]);
+        if (!isfinite(x[r])) flags |= KV1B_STATUS_NONFINITE;
+      }
+      const float nrm = __fsqrt_rn(tree_sum128(sq));
+      rotate_rounds(x, p.c.signs);
+      uint32_t nib = 0;
+      #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        nib |= static_cast<uint32_t>(x[r] >= 0.0f) << r;
+        ab[r] = fabsf(x[r]);
+      }
+      const uint32_t word = pack_word(nib);
+      const float sabs = tree_sum128(ab);
+      const float cinv = (sabs > 0.0f) ? __fdiv_rn(__fmul_rn(static_cast<float>(kD), nrm), sabs) : 1.0f;
+      const int row = 8 * ((tok >> 1) & 3) + 2 * (tok >> 3) + (tok & 1);
+      if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(blk)[row * 4 + (lane >> 3)] = word;
+      if (lane == 0) reinterpret_cast<float*>(blk + kBlkOffNc)[tok] = __fmul_rn(nrm, cinv);
+    } else {
+      load4(p.v, t * p.v_st + h * p.v_sh + 4 * lane, p.dtype, x);
+      #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (!isfinite(x[r])) flags |= KV1B_STATUS_NONFINITE;
+        else if (fabsf(x[r]) > kF16Max) flags |= KV1B_STATUS_FP16_SATURATED;
+        x[r] = limit_value(x[r]);
+      }
+      float mn = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      #pragma unroll
+      for (int m = 1; m <= 4; m <<= 1) {
+        mn = fminf(mn, __shfl_xor_sync(kFull, mn, m));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
+      }
+      uint32_t sb, mb;
+      group_scale(mn, mx, &sb, &mb, true);
+      const float sf = __half2float(__ushort_as_half(static_cast<unsigned short>(sb)));
+      const float mf = __half2float(__ushort_as_half(static_cast<unsigned short>(mb)));
+      const int j = tok & 7;
+      const int sh = 4 * ((j >> 1) + 4 * (j & 1));
+      #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint32_t c = 0;
+        if (sf > 0.0f) {
+          const float fl = floorf(__fadd_rn(__fdiv_rn(__fsub_rn(x[r], mf), sf), 0.5f));
+          c = !(fl > 0.0f) ? 0u : (fl >= 15.0f ? 15u : static_cast<uint32_t>(fl));
+        }
+        cw[r] = (cw[r] & ~(0xfu << sh)) | (c << sh);
+      }
+      if ((lane & 7) == 0) {
+        reinterpret_cast<uint16_t*>(blk + kBlkOffScale)[32 * (lane >> 3) + tok] = static_cast<uint16_t>(sb);
+        reinterpret_cast<uint16_t*>(blk + kBlkOffMin)[32 * (lane >> 3) + tok] = static_cast<uint16_t>(mb);
+      }
+      wrote = true;
+    }
+  }
+  if (wrote) {
+    #pragma unroll
+    for (int r = 0; r < 4; ++r) words[(4 * lane + r) * 4] = cw[r];
+  }
+  flags = static_cast<int>(__reduce_or_sync(kFull, static_cast<unsigned>(flags)));
+  if (lane == 0 && flags && p.c.status) atomicOr(p.c.status, flags);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Prefill form: one warp per (group, kv-head), 4 lanes per token (kv1b_encode_q4.cuh).
+template <int DT>
+__global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAppendParams p) {
+  typedef typename Elem<DT>::T T;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, tau = lane >> 2, j = lane & 3;
+  const int gi = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (gi >= p.groups) return;
+  const int h = blockIdx.y;
+  const Group g = find_group(p, gi);
+  if (!g.any) return;
+  const int64_t pos = g.g0 + tau;
+  const bool is_new = pos >= g.L0 && pos < g.L1;
+  const int64_t t = g.row0 + (pos - g.L0);
+  uint8_t* blk = block_of(p, g.b, h, g.g0);
+  int flags = 0;
+  int ps[3] = {0, 0, 0};
+  bool on = is_new && blk;
+  if (on && p.cos_sin) on = positions(p, t, ps);
+  if (is_new && !on) flags |= KV1B_STATUS_BAD_INDEX;
+  const int tok = static_cast<int>(pos & 31);
+
+  {  // ---- key: lane j holds channels j + 4 r
+    const T* krow = static_cast<const T*>(p.k) + t * p.k_st + h * p.k_sh;
+    float x[32], a[32];
+    #pragma unroll
+    for (int r = 0; r < 32; ++r) x[r] = on ? Elem<DT>::get(__ldg(krow + j + 4 * r)) : 0.0f;
+    if (p.cos_sin && on) {
+      const int half = p.rot >> 1;
+      #pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const int c = j + 4 * r;
+        if (c < p.rot) {
+          const bool upper = p.interleaved ? (c & 1) != 0 : c >= half;
+          const int i = p.interleaved ? c >> 1 : (upper ? c - half : c);
+          const int pc = p.interleaved ? c ^ 1 : (upper ? c - half : c + half);
+          const float* row = p.cos_sin + static_cast<int64_t>(ps[axis_of(p, i)]) * p.rot;
+          const float cs = __ldg(row + i), sn = __ldg(row + half + i);
+          const float o = Elem<DT>::get(__ldg(krow + pc));
+          x[r] = upper ? __fadd_rn(__fmul_rn(x[r], cs), __fmul_rn(o, sn)) : __fsub_rn(__fmul_rn(x[r], cs), __fmul_rn(o, sn));
+        }
+      }
+    }
+    bool fin = true;
+    #pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      fin &= isfinite(x[r]);
+      a[r] = __fmul_rn(x[r], x[r]);
+    }
+    flags |= fin ? 0 : KV1B_STATUS_NONFINITE;
+    const float nrm = __fsqrt_rn(tree_sum_q4(a));
+    const float f0 = p.c.signs[0], f1 = p.c.signs[kD], f2 = p.c.signs[2 * kD];
+    const int rounds = f0 == 0.0f ? 0 : (f1 == 0.0f ? 1 : (f2 == 0.0f ? 2 : 3));
+    #pragma unroll 1
+    for (int rd = 0; rd < rounds; ++rd) rotate_q4(x, sign_mask(p.c.signs, rd, j), j);
+    uint32_t word = 0u;
+    #pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const uint32_t bal = __ballot_sync(kFull, x[r] >= 0.0f);
+      if ((r >> 3) == j) word |= ((bal >> (4 * tau)) & 0xFu) << (4 * (r & 7));
+      a[r] = fabsf(x[r]);
+    }
+    const float sabs = tree_sum_q4(a);
+    const float cinv = (sabs > 0.0f) ? __fdiv_rn(__fmul_rn(static_cast<float>(kD), nrm), sabs) : 1.0f;
+    if (on) {
+      const int row = 8 * ((tok >> 1) & 3) + 2 * (tok >> 3) + (tok & 1);
+      reinterpret_cast<uint32_t*>(blk)[row * 4 + j] = word;
+      if (j == 0) reinterpret_cast<float*>(blk + kBlkOffNc)[tok] = __fmul_rn(nrm, cinv);
+    }
+  }
+
+  // ---- value: lane j holds group j
+  float v[32];
+  #pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    if (on) load4(p.v, t * p.v_st + h * p.v_sh + 32 * j + 4 * q, DT, v + 4 * q);
+    else v[4 * q] = v[4 * q + 1] = v[4 * q + 2] = v[4 * q + 3] = 0.0f;
+  }
+  float mn = INFINITY, mx = -INFINITY;
+  bool fin = true, big = false;
+  #pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    fin &= isfinite(v[i]);
+    big |= fabsf(v[i]) > kF16Max;
+    v[i] = limit_value(v[i]);
+    mn = fminf(mn, v[i]);
+    mx = fmaxf(mx, v[i]);
+  }
+  flags |= fin ? (big ? KV1B_STATUS_FP16_SATURATED : 0) : KV1B_STATUS_NONFINITE;
+  uint32_t sb, mb;
+  group_scale(mn, mx, &sb, &mb, false);
+  const float sf = __half2float(__ushort_as_half(static_cast<unsigned short>(sb)));
+  const float mf = __half2float(__ushort_as_half(static_cast<unsigned short>(mb)));
+  const float rs = __frcp_rn(sf);
+  uint32_t cw[4];  // token-major: nibble i of word k = channel 32 j + 8 k + i of this token
+  #pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t w = 0u - kMagicPacked;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = __fadd_rn(div_markstein(__fsub_rn(v[8 * k + i], mf), sf, rs), 0.5f);
+      const float c = fminf(fmaxf(y, 0.0f), 15.5f);
+      w += __float_as_uint(__fadd_rd(c, 8388608.0f)) << (4 * i);
+    }
+    cw[k] = (on && sf > 0.0f) ? w : 0u;
+  }
+  if (on) {
+    reinterpret_cast<uint16_t*>(blk + kBlkOffScale)[32 * j + tok] = static_cast<uint16_t>(sb);
+    reinterpret_cast<uint16_t*>(blk + kBlkOffMin)[32 * j + tok] = static_cast<uint16_t>(mb);
+  }
+  // transpose the 8 x 8 nibbles of each word across the 8 token lanes of group j (nibble = token), then
+  // move the even tokens to nibbles 0 .. 3 and the odd ones to 4 .. 7
+  #pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t x = cw[k];
+    uint32_t y = __shfl_xor_sync(kFull, x, 16);
+    x = (tau & 4) ? ((x & 0xFFFF0000u) | (y >> 16)) : ((x & 0x0000FFFFu) | (y << 16));
+    y = __shfl_xor_sync(kFull, x, 8);
+    x = (tau & 2) ? ((x & 0xFF00FF00u) | ((y >> 8) & 0x00FF00FFu)) : ((x & 0x00FF00FFu) | ((y & 0x00FF00FFu) << 8));
+    y = __shfl_xor_sync(kFull, x, 4);
+    x = (tau & 1) ? ((x & 0xF0F0F0F0u) | ((y >> 4) & 0x0F0F0F0Fu)) : ((x & 0x0F0F0F0Fu) | ((y & 0x0F0F0F0Fu) << 4));
+    uint32_t s1 = (x ^ (x >> 4)) & 0x00F000F0u;   // swap nibbles 1 and 2 of each half word
+    x ^= s1 ^ (s1 << 4);
+    s1 = (x ^ (x >> 8)) & 0x0000FF00u;            // swap bytes 1 and 2
+    x ^= s1 ^ (s1 << 8);
+    cw[k] = x;
+  }
+  // the mask of nibbles whose tokens were written, in the same order
+  const uint32_t onb = __ballot_sync(kFull, on && j == 0);  // bit 4 tau
+  uint32_t keep = 0xFFFFFFFFu;
+  #pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (onb & (1u << (4 * i))) keep &= ~(0xFu << (4 * ((i >> 1) + 4 * (i & 1))));
+  if (blk && keep != 0xFFFFFFFFu) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(blk + kBlkOffCodes) + (32 * j + tau) * 4 + (static_cast<int>(g.g0 & 31) >> 3);
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) dst[8 * 4 * k] = keep ? ((dst[8 * 4 * k] & keep) | (cw[k] & ~keep)) : cw[k];
+  }
+  flags = static_cast<int>(__reduce_or_sync(kFull, static_cast<unsigned>(flags)));
+  if (lane == 0 && flags && p.c.status) atomicOr(p.c.status, flags);
+}
+
+// Queries of a prefill: one warp per row.
+__global__ void __launch_bounds__(256) paged_query_kernel(const PagedAppendParams p) {
+  pdl_wait();
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t t = r / p.Hq;
+  if (t >= p.T || t >= __ldg(p.cu + p.B)) return;
+  query_row(p, t, static_cast<int>(r - t * p.Hq));
+}
+
+}  // namespace paged
+}  // namespace kv1b
+
+using namespace kv1b;
+
+cudaError_t kv1b_launch_paged_append(const PagedAppendParams& p, cudaStream_t stream) {
+  if (p.T <= 4 * p.B) {
+    const int64_t units = 2LL * p.groups * p.c.Hkv + (p.q ? static_cast<int64_t>(p.T) * p.Hq : 0);
+    return launch_pdl(paged::paged_append_token_kernel, dim3(static_cast<unsigned>((units + 3) / 4)), dim3(128), 0, stream, p);
+  }
+  const dim3 grid((p.groups + 3) / 4, p.c.Hkv);
+  cudaError_t e;
+  switch (p.dtype) {
+    case KV1B_DTYPE_F32: e = launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_F32>, grid, dim3(128), 0, stream, p); break;
+    case KV1B_DTYPE_BF16: e = launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_BF16>, grid, dim3(128), 0, stream, p); break;
+    default: e = launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_F16>, grid, dim3(128), 0, stream, p); break;
+  }
+  if (e != cudaSuccess || !p.q) return e;
+  const int64_t rows = static_cast<int64_t>(p.T) * p.Hq;
+  return launch_pdl(paged::paged_query_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p);
+}
