@@ -400,7 +400,8 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
 
 /* Workspace bytes of kv1b_paged_attend / kv1b_paged_attend_shared (0 on invalid arguments). */
 size_t kv1b_paged_attend_workspace_bytes(const kv1b_paged_t* cache, int32_t num_q_heads);
-size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_seqs, int32_t num_q_heads);
+size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t max_prefix_pages);
 
 /* Decode attention over a page table: one query token per sequence.
  * q: [num_seqs][num_q_heads][128] contiguous, KV1B_DTYPE_BF16 or _F16, 16-byte aligned; out: the same

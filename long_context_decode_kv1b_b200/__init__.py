@@ -95,7 +95,7 @@ def lib() -> ctypes.CDLL:
                                                  P, P, i32, i64, i64, i64, i64, P]),
             "kv1b_paged_attend_workspace_bytes": (sz, [P, i32]),
             "kv1b_paged_attend": (ctypes.c_int, [P, P, i32, i32, f32, i32, P, i64, i32, P, i32, i32, P, P, sz, P]),
-            "kv1b_paged_shared_workspace_bytes": (sz, [P, i32, i32]),
+            "kv1b_paged_shared_workspace_bytes": (sz, [P, i32, i32, i32]),
             "kv1b_paged_attend_shared": (ctypes.c_int, [P, P, i32, i32, f32, i32, P, i32, P, P, i64, i32, P, P, P, sz, P]),
         }
         for name, (res, args) in sig.items():

@@ -76,10 +76,24 @@ struct PagedAttendParams {
   int32_t max_prefix_pages;
   void* out;               // q_dtype [B][Hq][128]
   float* part;             // [ctas][2][G][2 + 128]
+  float* rows;             // null, or [B][Hq][2 + 128]: whole segments leave (m, l, o) here, none is normalised
   int32_t ncta;
+};
+
+// The queries of a kv-head as the rows of one matrix: R = B G rows, row b G + g.
+struct PagedSharedParams {
+  int32_t R;
+  int32_t two;             // a CTA's two lanes hold 256 rows, or 128 rows twice
+  int32_t row_tiles;       // of 256 or 128 rows
+  int32_t splits;          // token ranges
+  uint8_t* codes;          // [Hkv][R][128] f8
+  float2* factors;         // [Hkv][R]
+  float* pieces;           // [Hkv][row_tiles][splits][2][128][2 + 128]
 };
 
 }  // namespace kv1b
 
 cudaError_t kv1b_launch_paged_append(const kv1b::PagedAppendParams& p, cudaStream_t stream);
 cudaError_t kv1b_launch_paged_attend(const kv1b::PagedAttendParams& p, int32_t G, cudaStream_t stream);
+cudaError_t kv1b_launch_paged_shared(const kv1b::PagedAttendParams& p, const kv1b::PagedSharedParams& s, int32_t G,
+                                     cudaStream_t stream);

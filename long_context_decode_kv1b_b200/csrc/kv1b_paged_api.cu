@@ -167,6 +167,59 @@ size_t kv1b_paged_attend_workspace_bytes(const kv1b_paged_t* cache, int32_t num_
   return (n + 255) / 256 * 256;
 }
 
+namespace {
+
+// How the batch's queries and the prefix are split over CTAs: the number of token ranges whose waves of
+// CTAs take the fewest tile times, a range counted kFixed more for its start and its merge.
+kv1b::PagedSharedParams shared_plan(int32_t Hkv, int32_t G, int32_t num_seqs, int64_t max_tokens) {
+  constexpr int64_t kFixed = 4;
+  kv1b::PagedSharedParams s;
+  memset(&s, 0, sizeof(s));
+  s.R = num_seqs * G;
+  s.two = s.R > 128;
+  const int rows = s.two ? 256 : 128;
+  s.row_tiles = (s.R + rows - 1) / rows;
+  const int64_t tiles = (max_tokens + 127) / 128, units = static_cast<int64_t>(Hkv) * s.row_tiles, sms = num_sms();
+  int64_t best = -1;
+  for (int64_t n = 1; n <= tiles && n <= 148; ++n) {
+    const int64_t cost = (units * n + sms - 1) / sms * ((tiles + n - 1) / n + kFixed);
+    if (best < 0 || cost < best) {
+      best = cost;
+      s.splits = static_cast<int32_t>(n);
+    }
+  }
+  return s;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The buffers of a shared call in its workspace, behind those of the attend; bytes in all.
+size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int32_t Hkv, int32_t G, size_t attend_bytes, uint8_t* ws) {
+  const size_t rows = static_cast<size_t>(Hkv) * s->R, row = kv1b::kPartStride * 4;
+  size_t at = attend_bytes;
+  if (p) p->rows = reinterpret_cast<float*>(ws + at);
+  at += up256(rows * row);
+  s->codes = ws + at;
+  at += up256(rows * KV1B_HEAD_DIM);
+  s->factors = reinterpret_cast<float2*>(ws + at);
+  at += up256(rows * 8);
+  s->pieces = reinterpret_cast<float*>(ws + at);
+  return at + up256(static_cast<size_t>(Hkv) * s->row_tiles * s->splits * 256 * row);
+}
+
+}  // namespace
+
+size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t max_prefix_pages) {
+  if (num_seqs < 1 || num_seqs > KV1B_PAGED_MAX_SEQS || max_prefix_pages < 1) return 0;
+  const size_t attend_bytes = kv1b_paged_attend_workspace_bytes(cache, num_q_heads);
+  if (attend_bytes == 0 || table_check(cache, 1, 0, 1, max_prefix_pages) != KV1B_OK) return 0;
+  const int32_t G = num_q_heads / cache->num_kv_heads;
+  kv1b::PagedSharedParams s =
+      shared_plan(cache->num_kv_heads, G, num_seqs, static_cast<int64_t>(max_prefix_pages) * cache->page_tokens);
+  return shared_carve(&s, nullptr, cache->num_kv_heads, G, attend_bytes, nullptr);
+}
+
 static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
                   int32_t num_seqs, const int32_t* prefix_pages, int32_t max_prefix_pages, const int32_t* prefix_length,
                   const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* lengths,
@@ -181,7 +234,9 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(page_table, 4) || !aligned(lengths, 4) ||
       !aligned(prefix_pages, 4) || !aligned(prefix_length, 4))
     return KV1B_ERR_MISALIGNED;
-  if (ws_bytes < kv1b_paged_attend_workspace_bytes(cache, num_q_heads)) return KV1B_ERR_WORKSPACE;
+  const size_t attend_bytes = kv1b_paged_attend_workspace_bytes(cache, num_q_heads);
+  if (ws_bytes < (prefix_pages ? kv1b_paged_shared_workspace_bytes(cache, num_seqs, num_q_heads, max_prefix_pages) : attend_bytes))
+    return KV1B_ERR_WORKSPACE;
   kv1b::PagedAttendParams p;
   memset(&p, 0, sizeof(p));
   p.c = view(cache);
@@ -202,7 +257,12 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   p.out = out;
   p.part = static_cast<float*>(ws);
   p.ncta = num_sms();
-  return cuda_status(kv1b_launch_paged_attend(p, num_q_heads / cache->num_kv_heads, static_cast<cudaStream_t>(stream)));
+  const int32_t G = num_q_heads / cache->num_kv_heads;
+  if (!prefix_pages) return cuda_status(kv1b_launch_paged_attend(p, G, static_cast<cudaStream_t>(stream)));
+  kv1b::PagedSharedParams s =
+      shared_plan(cache->num_kv_heads, G, num_seqs, static_cast<int64_t>(max_prefix_pages) * cache->page_tokens);
+  shared_carve(&s, &p, cache->num_kv_heads, G, attend_bytes, static_cast<uint8_t*>(ws));
+  return cuda_status(kv1b_launch_paged_shared(p, s, G, static_cast<cudaStream_t>(stream)));
 }
 
 int kv1b_paged_attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
@@ -211,11 +271,6 @@ int kv1b_paged_attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype,
                       void* stream) {
   return attend(cache, q, q_dtype, num_q_heads, scale, num_seqs, nullptr, 0, nullptr, page_table, table_stride, max_pages,
                 lengths, window, sinks, out, ws, ws_bytes, stream);
-}
-
-size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_seqs, int32_t num_q_heads) {
-  if (num_seqs < 1 || num_seqs > KV1B_PAGED_MAX_SEQS) return 0;
-  return kv1b_paged_attend_workspace_bytes(cache, num_q_heads);
 }
 
 int kv1b_paged_attend_shared(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,

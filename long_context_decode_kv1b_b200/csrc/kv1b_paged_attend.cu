@@ -21,8 +21,7 @@
 //            row of ones, so the roundings of the weights cancel in the quotient.
 // Values and weights are rounded to 11 bits because the result is: out has the query's 16-bit type.
 // Weights are 2^(x - m + kBase) <= 2^15, so a weight keeps its 11 bits down to 2^-21 of the reference.
-#include "kv1b_device.cuh"
-#include "kv1b_paged.h"
+#include "kv1b_paged_device.cuh"
 
 namespace kv1b {
 namespace paged {
@@ -30,13 +29,6 @@ namespace paged {
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr float kTau = 8.0f;    // a logit may pass the reference by 2^8 before it is raised
-constexpr float kBase = 7.0f;   // weights are 2^7 at the reference: at most 2^15 < 65504
-constexpr float kNoRef = -1e30f;
-constexpr int kRow = 2 + kD;    // partial row: m (log2 units), l, o[128]
-constexpr int kMinBlocks = 16;  // blocks a CTA takes at least
-constexpr int kMaxSeqs = KV1B_PAGED_MAX_SEQS;
-constexpr int kWaitTries = 4096;
 
 constexpr int kOffPre = kWarps * kStages * kBlkBytes;            // u32 [kMaxSeqs + 1] blocks before each sequence
 constexpr int kOffLen = kOffPre + (kMaxSeqs + 4) * 4;            // i32 [kMaxSeqs]
@@ -44,188 +36,6 @@ constexpr int kOffRed = kOffLen + kMaxSeqs * 4;                  // f32 [kWarps]
 constexpr int smem_bytes(int G) { return kOffRed + kWarps * G * kRow * 4; }
 static_assert(kOffPre % 16 == 0 && kOffRed % 16 == 0, "alignment");
 static_assert(smem_bytes(KV1B_MAX_GROUP) + 2048 <= 227 * 1024, "shared memory");
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void mbar_init(uint64_t* bar, int count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
-}
-__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(500000u)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait (at most kWaitTries suspended tries of 0.5 ms); false when it ran out.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int tries) {
-  for (int i = 0; i < tries; ++i)
-    if (mbar_try(bar, parity)) return true;
-  return false;
-}
-__device__ __forceinline__ void block_g2s(uint32_t dst, const void* src, uint64_t* bar) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(kBlkBytes) : "memory");
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(kBlkBytes), "r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4(uint32_t r[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void lds128(uint32_t r[4], uint32_t addr) {
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void imma(int d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void hmma(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// The four token pairs of a code word as exact binary16 integers 0 .. 15: a nibble in the mantissa of
-// 1024 (low nibble of a byte: 1024 + c; high nibble: 1024 + 16 c), the offset taken off exactly.
-__device__ __forceinline__ void expand_codes(uint32_t w, uint32_t (&c)[4]) {
-  const uint32_t w8 = w >> 8;
-  c[0] = hadd2((w & 0x000F000Fu) | 0x64006400u, 0xE400E400u);               // - 1024
-  c[1] = hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);  // / 16 - 64
-  c[2] = hadd2((w8 & 0x000F000Fu) | 0x64006400u, 0xE400E400u);
-  c[3] = hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
-}
-
-// ---------------------------------------------------------------------------------------------
-// The work plan, computed alike by every CTA of both kernels from the device lengths.
-struct Visible {
-  int blocks;       // prefix + own blocks seen
-  int skip_from;    // own blocks [0, skip_from) and from skip_to on are seen
-  int skip_to;
-};
-__device__ __forceinline__ Visible visible(int len, int npre, int window, int sinks) {
-  Visible v;
-  const int nb = (len + kBlkTok - 1) / kBlkTok;
-  v.skip_from = v.skip_to = 0;
-  if (window > 0 && len > window) {
-    const int wb = (len - window) / kBlkTok;
-    const int s = sinks < len ? sinks : len;
-    const int sb = (s + kBlkTok - 1) / kBlkTok;
-    v.skip_from = sb < wb ? sb : wb;
-    v.skip_to = wb;
-  }
-  v.blocks = npre + nb - (v.skip_to - v.skip_from);
-  return v;
-}
-
-struct Plan {
-  const uint32_t* pre;  // [B + 1] blocks of one kv-head before each sequence
-  const int* len;
-  int B, Hkv, n;        // n: CTAs with work
-  int npre, prefix_len;
-  int64_t S;            // blocks in all
-  __device__ __forceinline__ int64_t begin(int c) const { return S * c / n; }
-  // segment of block r: sequence, head, first block
-  __device__ __forceinline__ void locate(int64_t r, int* b, int* h, int64_t* base) const {
-    int lo = 0, hi = B;  // largest lo with Hkv * pre[lo] <= r
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (static_cast<int64_t>(pre[mid]) * Hkv <= r) lo = mid;
-      else hi = mid;
-    }
-    const int64_t s0 = static_cast<int64_t>(pre[lo]) * Hkv;
-    const int nb = static_cast<int>(pre[lo + 1] - pre[lo]);
-    *b = lo;
-    *h = static_cast<int>((r - s0) / nb);
-    *base = s0 + static_cast<int64_t>(*h) * nb;
-  }
-};
-
-// All threads of the CTA; lengths are limited to what the page table can hold.
-template <int THREADS>
-__device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* pre, int* len, int ncta) {
-  __shared__ uint32_t s_tot[THREADS / 32];
-  const int per = (p.B + THREADS - 1) / THREADS;
-  const int page_shift = p.c.bpp_shift + 5;
-  const int64_t most = static_cast<int64_t>(p.max_pages) << page_shift;
-  Plan pl;
-  pl.prefix_len = 0;
-  bool bad = false;
-  if (p.prefix_len) {
-    const int64_t top = static_cast<int64_t>(p.max_prefix_pages) << page_shift;
-    const int n = __ldg(p.prefix_len);
-    bad |= n < 0 || n > top;
-    pl.prefix_len = n < 0 ? 0 : static_cast<int>(n > top ? top : n);
-  }
-  pl.npre = (pl.prefix_len + kBlkTok - 1) / kBlkTok;
-  const int b0 = threadIdx.x * per;
-  uint32_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = b0 + i;
-    if (b >= p.B) break;
-    const int n = __ldg(p.lengths + b);
-    bad |= n < 0 || n > most;
-    const int nn = n < 0 ? 0 : static_cast<int>(n > most ? most : n);
-    len[b] = nn;
-    mine += static_cast<uint32_t>(visible(nn, pl.npre, p.window, p.sinks).blocks);
-  }
-  if (bad && blockIdx.x == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
-  uint32_t x = mine;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_tot[warp] = x;
-  __syncthreads();
-  uint32_t at = x - mine, total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    at += w < warp ? s_tot[w] : 0u;
-    total += s_tot[w];
-  }
-  for (int i = 0; i < per; ++i) {
-    const int b = b0 + i;
-    if (b >= p.B) break;
-    pre[b] = at;
-    at += static_cast<uint32_t>(visible(len[b], pl.npre, p.window, p.sinks).blocks);
-  }
-  if (threadIdx.x == 0) pre[p.B] = total;
-  __syncthreads();
-  pl.pre = pre;
-  pl.len = len;
-  pl.B = p.B;
-  pl.Hkv = p.c.Hkv;
-  pl.S = static_cast<int64_t>(total) * p.c.Hkv;
-  const int64_t want = (pl.S + kMinBlocks - 1) / kMinBlocks;
-  pl.n = static_cast<int>(want < 1 ? 1 : (want < ncta ? want : ncta));
-  return pl;
-}
 
 // A walk over one warp's blocks of the CTA's range [r0, r1).
 struct Walk {
@@ -235,7 +45,7 @@ struct Walk {
   __device__ __forceinline__ void segment(const Plan& pl, const PagedAttendParams& p, int64_t r, int first) {
     int64_t base;
     pl.locate(r, &b, &h, &base);
-    vis = visible(pl.len[b], pl.npre, p.window, p.sinks);
+    vis = visible(pl.len[b], p.window, p.sinks);
     nb = vis.blocks;
     const int64_t e = base + nb;
     rnext = e < r1 ? e : r1;
@@ -249,19 +59,13 @@ struct Walk {
   }
 };
 
-// Block i of a segment: token offset of the block in its list (prefix or own), and its page's entry.
+// Block i of a segment: its place in the sequence, and its page's entry.
 __device__ __forceinline__ int own_block(const Visible& v, int j) { return j < v.skip_from ? j : j + (v.skip_to - v.skip_from); }
 
 template <typename W>
-__device__ __forceinline__ int page_entry(const PagedAttendParams& p, const Plan& pl, const W& w) {
-  if (w.i < pl.npre) return __ldg(p.prefix_pages + (w.i >> p.c.bpp_shift));
-  const int blk = own_block(w.vis, w.i - pl.npre);
+__device__ __forceinline__ int page_entry(const PagedAttendParams& p, const W& w) {
+  const int blk = own_block(w.vis, w.i);
   return __ldg(p.table + w.b * p.table_stride + (blk >> p.c.bpp_shift));
-}
-
-__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float x) {
-  if (dtype == KV1B_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
-  else static_cast<__half*>(out)[i] = __float2half_rn(x);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAttendParams p, const int G) {
@@ -281,10 +85,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
   }
   pdl_wait();
   pdl_launch_dependents();
-  const Plan pl = make_plan<kThreads>(p, pre, slen, gridDim.x);
+  const Plan pl = make_plan<kThreads>(p, pre, slen, gridDim.x, blockIdx.x == 0);
 
   // sequences that see nothing: zeros
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+  for (int b = p.rows ? p.B : blockIdx.x; b < p.B; b += gridDim.x)
     if (pre[b + 1] == pre[b])
       for (int e = threadIdx.x; e < p.Hq * kD; e += kThreads) store_out(p.out, p.q_dtype, static_cast<int64_t>(b) * p.Hq * kD + e, 0.0f);
   if (static_cast<int>(blockIdx.x) >= pl.n || pl.S == 0) return;
@@ -305,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
   uint32_t absent = 0;  // bit s: stage s holds no block (its page is outside the cache)
   auto issue = [&](int s, int page) {
     const bool ok = page >= 0 && page < p.c.num_pages;
-    const int blk = ahead.i < pl.npre ? ahead.i : own_block(ahead.vis, ahead.i - pl.npre);
+    const int blk = own_block(ahead.vis, ahead.i);
     absent = ok ? absent & ~(1u << s) : absent | (1u << s);
     if (lane == 0) {
       if (ok) {
@@ -324,10 +128,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
     // the first kStages entries
     for (int s = 0; s < kStages && more; ++s) {
       more = settle(ahead);
-      if (more) issue(s, page_entry(p, pl, ahead));
+      if (more) issue(s, page_entry(p, ahead));
     }
     if (more) more = settle(ahead);
-    if (more) pend = page_entry(p, pl, ahead);
+    if (more) pend = page_entry(p, ahead);
   }
 
   Walk cur;
@@ -392,11 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
           gave_up = true;  // every lane alike
         phases ^= 1u << stage;
         // which of the block's tokens the query sees
-        const bool in_prefix = cur.i < pl.npre;
-        const int blk = in_prefix ? cur.i : own_block(cur.vis, cur.i - pl.npre);
-        const int tok0 = blk * kBlkTok;
-        const int len = in_prefix ? pl.prefix_len : pl.len[cur.b];
-        const int wstart = (!in_prefix && p.window > 0 && len > p.window) ? len - p.window : 0;
+        const int tok0 = own_block(cur.vis, cur.i) * kBlkTok;
+        const int len = pl.len[cur.b];
+        const int wstart = (p.window > 0 && len > p.window) ? len - p.window : 0;
         edge = tok0 + kBlkTok > len || (tok0 < wstart && tok0 + kBlkTok > p.sinks);
         uint32_t seen = 0xFFFFFFFFu;
         if (edge) {
@@ -506,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
       if (more && !gave_up) {
         issue(stage, pend);
         more = settle(ahead);
-        if (more) pend = page_entry(p, pl, ahead);
+        if (more) pend = page_entry(p, ahead);
       } else if (gave_up) {
         absent |= 1u << stage;
       }
@@ -550,10 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
           num = __fmaf_rn(f, r[2 + ch], num);
           den = __fmaf_rn(f, r[1], den);
         }
-        if (starts && ends) {
+        if (starts && ends && !p.rows) {
           store_out(p.out, p.q_dtype, (qrow + hd) * kD + ch, den != 0.0f ? __fdiv_rn(num, den) : 0.0f);
         } else {
-          float* row = p.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * G + hd) * kRow;
+          float* row = starts && ends ? p.rows + (qrow + hd) * kRow
+                                      : p.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * G + hd) * kRow;
           if (ch == 0) {
             row[0] = M;
             row[1] = den;
@@ -575,7 +378,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedAttendParam
   __shared__ uint32_t pre[kMaxSeqs + 1];
   __shared__ int slen[kMaxSeqs];
   pdl_wait();
-  const Plan pl = make_plan<128>(p, pre, slen, p.ncta);
+  const Plan pl = make_plan<128>(p, pre, slen, p.ncta, false);
   const int c = blockIdx.x, hd = blockIdx.y;
   if (c + 1 >= pl.n || pl.S == 0) return;
   const int64_t r0 = pl.begin(c), r1 = pl.begin(c + 1);
@@ -617,6 +420,6 @@ cudaError_t kv1b_launch_paged_attend(const PagedAttendParams& p, int32_t G, cuda
                                  paged::smem_bytes(KV1B_MAX_GROUP), &configured);
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged::paged_attend_kernel, dim3(p.ncta), dim3(paged::kThreads), paged::smem_bytes(G), stream, p, G);
-  if (e != cudaSuccess || p.ncta < 2) return e;
+  if (e != cudaSuccess || p.ncta < 2 || p.rows) return e;
   return launch_pdl(paged::paged_merge_kernel, dim3(p.ncta - 1, G), dim3(128), 0, stream, p, G);
 }

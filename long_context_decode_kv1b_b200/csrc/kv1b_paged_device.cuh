@@ -1,0 +1,200 @@
+// kv1b_paged_device.cuh -- device-side pieces shared by the paged attention kernels: bulk copies and
+// bounded waits, code expansion, and the split of the visible blocks over CTAs.
+#pragma once
+#include "kv1b_device.cuh"
+#include "kv1b_paged.h"
+
+namespace kv1b {
+namespace paged {
+
+constexpr float kTau = 8.0f;    // a logit may pass the reference by 2^8 before it is raised
+constexpr float kBase = 7.0f;   // weights are 2^7 at the reference: at most 2^15 < 65504
+constexpr float kNoRef = -1e30f;
+constexpr int kRow = 2 + kD;    // partial row: m (log2 units), l, o[128]
+constexpr int kMinBlocks = 16;  // blocks a CTA of the split takes at least
+constexpr int kMaxSeqs = KV1B_PAGED_MAX_SEQS;
+constexpr int kWaitTries = 4096;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint64_t* bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
+}
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(500000u)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait (at most kWaitTries suspended tries of 0.5 ms); false when it ran out.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int tries) {
+  for (int i = 0; i < tries; ++i)
+    if (mbar_try(bar, parity)) return true;
+  return false;
+}
+__device__ __forceinline__ void block_g2s(uint32_t dst, const void* src, uint64_t* bar) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(kBlkBytes) : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(kBlkBytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t r[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t r[4], uint32_t addr) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void imma(int d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void hmma(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The four token pairs of a code word as exact binary16 integers 0 .. 15: a nibble in the mantissa of
+// 1024 (low nibble of a byte: 1024 + c; high nibble: 1024 + 16 c), the offset taken off exactly.
+__device__ __forceinline__ void expand_codes(uint32_t w, uint32_t (&c)[4]) {
+  const uint32_t w8 = w >> 8;
+  c[0] = hadd2((w & 0x000F000Fu) | 0x64006400u, 0xE400E400u);               // - 1024
+  c[1] = hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);  // / 16 - 64
+  c[2] = hadd2((w8 & 0x000F000Fu) | 0x64006400u, 0xE400E400u);
+  c[3] = hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
+}
+
+__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float x) {
+  if (dtype == KV1B_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
+  else static_cast<__half*>(out)[i] = __float2half_rn(x);
+}
+
+// ---------------------------------------------------------------------------------------------
+// The work plan, computed alike by every CTA of both kernels from the device lengths.
+struct Visible {
+  int blocks;       // blocks seen
+  int skip_from;    // blocks [0, skip_from) and from skip_to on are seen
+  int skip_to;
+};
+__device__ __forceinline__ Visible visible(int len, int window, int sinks) {
+  Visible v;
+  const int nb = (len + kBlkTok - 1) / kBlkTok;
+  v.skip_from = v.skip_to = 0;
+  if (window > 0 && len > window) {
+    const int wb = (len - window) / kBlkTok;
+    const int s = sinks < len ? sinks : len;
+    const int sb = (s + kBlkTok - 1) / kBlkTok;
+    v.skip_from = sb < wb ? sb : wb;
+    v.skip_to = wb;
+  }
+  v.blocks = nb - (v.skip_to - v.skip_from);
+  return v;
+}
+
+struct Plan {
+  const uint32_t* pre;  // [B + 1] blocks of one kv-head before each sequence
+  const int* len;
+  int B, Hkv, n;        // n: CTAs with work
+  int64_t S;            // blocks in all
+  __device__ __forceinline__ int64_t begin(int c) const { return S * c / n; }
+  __device__ __forceinline__ int owner(int64_t r) const {  // the CTA whose range holds block r: begin(c) <= r < begin(c + 1)
+    return static_cast<int>(((r + 1) * n - 1) / S);
+  }
+  // segment of block r: sequence, head, first block
+  __device__ __forceinline__ void locate(int64_t r, int* b, int* h, int64_t* base) const {
+    int lo = 0, hi = B;  // largest lo with Hkv * pre[lo] <= r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<int64_t>(pre[mid]) * Hkv <= r) lo = mid;
+      else hi = mid;
+    }
+    const int64_t s0 = static_cast<int64_t>(pre[lo]) * Hkv;
+    const int nb = static_cast<int>(pre[lo + 1] - pre[lo]);
+    *b = lo;
+    *h = static_cast<int>((r - s0) / nb);
+    *base = s0 + static_cast<int64_t>(*h) * nb;
+  }
+};
+
+// All threads of the CTA; lengths are limited to what the page table can hold.
+template <int THREADS>
+__device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* pre, int* len, int ncta, bool report) {
+  __shared__ uint32_t s_tot[THREADS / 32];
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int page_shift = p.c.bpp_shift + 5;
+  const int64_t most = static_cast<int64_t>(p.max_pages) << page_shift;
+  Plan pl;
+  bool bad = false;
+  const int b0 = threadIdx.x * per;
+  uint32_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = b0 + i;
+    if (b >= p.B) break;
+    const int n = __ldg(p.lengths + b);
+    bad |= n < 0 || n > most;
+    const int nn = n < 0 ? 0 : static_cast<int>(n > most ? most : n);
+    len[b] = nn;
+    mine += static_cast<uint32_t>(visible(nn, p.window, p.sinks).blocks);
+  }
+  if (bad && report && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+  uint32_t x = mine;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  #pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_tot[warp] = x;
+  __syncthreads();
+  uint32_t at = x - mine, total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    at += w < warp ? s_tot[w] : 0u;
+    total += s_tot[w];
+  }
+  for (int i = 0; i < per; ++i) {
+    const int b = b0 + i;
+    if (b >= p.B) break;
+    pre[b] = at;
+    at += static_cast<uint32_t>(visible(len[b], p.window, p.sinks).blocks);
+  }
+  if (threadIdx.x == 0) pre[p.B] = total;
+  __syncthreads();
+  pl.pre = pre;
+  pl.len = len;
+  pl.B = p.B;
+  pl.Hkv = p.c.Hkv;
+  pl.S = static_cast<int64_t>(total) * p.c.Hkv;
+  const int64_t want = (pl.S + kMinBlocks - 1) / kMinBlocks;
+  pl.n = static_cast<int>(want < 1 ? 1 : (want < ncta ? want : ncta));
+  return pl;
+}
+
+}  // namespace paged
+}  // namespace kv1b

@@ -1,0 +1,558 @@
+// kv1b_paged_shared.cu -- attention of a whole batch over one shared prefix: every query of a kv-head
+// against each prefix token once, as products of a matrix of queries on the 5th-generation tensor cores.
+//
+// For kv-head h the batch's queries are R = sequences x G rows.  A CTA takes up to 256 rows (two lanes
+// of 128) and a range of 128-token tiles; the ranges' partial rows (m, l, o) are merged afterwards with
+// the sequences' own tokens.  With at most 128 rows both lanes hold the same rows and take the tiles in
+// turn, so one lane's softmax still runs while the other's products do.
+//
+// Per tile and lane, S = Q K^T (f8, exact: codes 0 .. 15 times signs +-1, sums below 2^11) into tensor
+// memory; each softmax thread owns one row, x = nc (delta I2 + vl I1) with I2 = S and I1 the token's sum
+// of signs, and leaves 2^(x - m + kBase) as binary16 over S; O += P V (f16, fp32 sums in tensor memory).
+// S and P share columns: 2 lanes x (128 + 128) columns are all 512.
+//
+// Warps: 0 - 3 and 4 - 7 the lanes' softmax, 8 - 11 the expansion (signs to f8, codes to f16 values, one
+// rounding), 12 issues the products, 13 the copies.  Each wait is bounded; one that runs out ends the CTA
+// with KV1B_STATUS_TIMEOUT.
+//
+// A tile of 128 tokens x 256 rows costs 512 + 1,024 clocks of products and 32,768 exponentials, 2,048
+// clocks at 16 a clock: the exponentials bound it.
+#include "kv1b_paged_device.cuh"
+
+namespace kv1b {
+namespace paged {
+
+constexpr int kTile = 128;                 // tokens
+constexpr int kTileBlocks = kTile / kBlkTok;
+constexpr int kSoftWarps = 8, kExpandWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kExpandWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kShThreads = 512;            // four warpgroups; the last has two idle warps
+// 512 x 128 registers at launch; the softmax groups take what the others give back: 2 (168 + 88) = 4 x 128
+constexpr int kSoftRegs = 168, kOtherRegs = 88;
+constexpr int kRaw = 3;                    // tiles of packed blocks in flight
+constexpr int kBuf = 3;                    // expanded tiles
+constexpr int kQBytes = 128 * 128;         // one lane's codes
+constexpr int kKBytes = kTile * 128;       // signs as f8
+constexpr int kVBytes = kTile * kD * 2;    // values as f16: two halves of 64 tokens
+constexpr int kRawBytes = kTileBlocks * kBlkBytes;
+
+constexpr int kShQ = 0;
+constexpr int kShK = kShQ + 2 * kQBytes;
+constexpr int kShV = kShK + kBuf * kKBytes;
+constexpr int kShRaw = kShV + kBuf * kVBytes;
+constexpr int kShNc = kShRaw + kRaw * kRawBytes;     // f32 [kBuf][2][128]: nc, nc I1
+constexpr int kShMask = kShNc + kBuf * 2 * kTile * 4;  // u32 [kBuf][4]: tokens seen
+constexpr int kShSmem = kShMask + kBuf * 16 + 1024;    // and the alignment of the base
+static_assert(kRawBytes % 128 == 0 && kShSmem <= 226 * 1024, "shared memory");
+
+// ---- tensor memory and products
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// K-major operand in 128-byte swizzled rows (8-row groups of 1,024 bytes)
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+constexpr uint32_t kShapeM128N128 = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);  // fp32 sums; e4m3 / f16 operands: type 0
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, bool add) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
+               "l"(b), "r"(kShapeM128N128), "r"(static_cast<uint32_t>(add))
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, bool add) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
+               "l"(b), "r"(kShapeM128N128), "r"(static_cast<uint32_t>(add))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+// the registers of a load are valid from here on: the dependency keeps their uses behind the wait
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---- pairs of fp32
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return pair(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Query rows as f8 codes in the order of the expanded signs (channel 32 w + 8 j + r at byte 32 w + 4 r + j),
+// and each row's two factors of the logit.  One warp per row.
+__global__ void __launch_bounds__(256) paged_query_codes_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // [sequence][q head]
+  if (row >= static_cast<int64_t>(p.B) * p.Hq) return;
+  const QueryPrep qp = query_prep_warp(p.q, row * kD, p.q_dtype, p.c.signs);
+  const int b = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - static_cast<int64_t>(b) * p.Hq);
+  const int h = hq / G, g = hq - h * G;
+  const int64_t at = static_cast<int64_t>(h) * s.R + static_cast<int64_t>(b) * G + g;
+  const int w = lane >> 3;  // word of the lane's four channels 4 lane + r
+  #pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int c = 4 * (lane & 7) + r;  // channel within the word
+    uint32_t v = 0;
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t word = w == 0 ? qp.planes[j][0] : (w == 1 ? qp.planes[j][1] : (w == 2 ? qp.planes[j][2] : qp.planes[j][3]));
+      v |= ((word >> c) & 1u) << j;
+    }
+    const int e = 31 - __clz(v | 1u);
+    const uint32_t f8 = v == 0 ? 0u : static_cast<uint32_t>((7 + e) << 3) | ((v << (3 - e)) & 7u);
+    s.codes[at * kD + 32 * w + 4 * (c & 7) + (c >> 3)] = static_cast<uint8_t>(f8);
+  }
+  if (lane == 0) {
+    const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
+    s.factors[at] = make_float2(__fmul_rn(qp.delta, qs), __fmul_rn(qp.vl, qs));
+  }
+}
+
+__device__ __forceinline__ int prefix_tokens(const PagedAttendParams& p, bool report) {
+  const int64_t top = static_cast<int64_t>(p.max_prefix_pages) << (p.c.bpp_shift + 5);
+  const int n = __ldg(p.prefix_len);
+  if (report && (n < 0 || n > top) && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+  return n < 0 ? 0 : static_cast<int>(n > top ? top : n);
+}
+
+__global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const PagedAttendParams p, const PagedSharedParams s) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[kBuf], kv_empty[kBuf], s_full[2], p_full[2], o_done[2];
+  __shared__ uint32_t s_tmem, s_absent[kRaw];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kExpandWarps);
+    for (int i = 0; i < kBuf; ++i) mbar_init(&kv_full[i], kExpandWarps), mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&o_done[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // unit: kv-head, row tile, split
+  const int u = blockIdx.x;
+  const int split = u % s.splits, hr = u / s.splits;
+  const int rt = hr % s.row_tiles, h = hr / s.row_tiles;
+  const int n = prefix_tokens(p, u == 0 && threadIdx.x == 0);
+  const int64_t nt = (n + kTile - 1) / kTile;
+  const int t0 = static_cast<int>(nt * split / s.splits), tiles = static_cast<int>(nt * (split + 1) / s.splits) - t0;
+  if (tiles == 0) return;  // the whole CTA; the merge counts no piece here
+  const bool two = s.two != 0;
+  const int jobs = two ? 2 * tiles : tiles;  // job j: lane j & 1, tile j / 2 or j
+
+  if (warp == 0) tmem_alloc(&s_tmem);
+  {  // the rows' codes, swizzled; zeros behind the last row
+    const int rows = two ? 256 : 128;
+    for (int e = threadIdx.x; e < rows * 8; e += kShThreads) {
+      const int r = e >> 3, c = e & 7, row = rt * rows + r;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (row < s.R) v = *reinterpret_cast<const uint4*>(s.codes + (static_cast<int64_t>(h) * s.R + row) * kD + 16 * c);
+      *reinterpret_cast<uint4*>(smem + kShQ + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = s_tmem;
+  if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  bool ok = true;  // false once a wait ran out
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!__all_sync(kFull, mbar_wait(bar, parity, kWaitTries))) ok = false;
+    return ok;
+  };
+
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ------------------------------------------------------------------ softmax: a thread per row
+    const int w = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const int row = rt * (two ? 256 : 128) + (two ? w * 128 : 0) + r;
+    const bool warp_rows = row - lane < s.R;  // a warp without rows only keeps the barriers going
+    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 256, tO = tS + 128;
+    float2 f = make_float2(0.0f, 0.0f);
+    if (row < s.R) f = s.factors[static_cast<int64_t>(h) * s.R + row];
+    const uint64_t fa = pair(f.x, f.x), fb = pair(f.y, f.y);
+    float m = 0.0f, l = 0.0f;
+    bool have = false;  // a finite logit has set m
+    for (int j = w; j < jobs; j += 2) {
+      const int k = two ? j >> 1 : j, buf = k % kBuf;
+      if (!wait(&s_full[w], (j >> 1) & 1) || !wait(&kv_full[buf], (k / kBuf) & 1)) break;
+      tc_after();
+      if (warp_rows) {
+        const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + kShMask) + buf * 4;
+        const uint4 seen = *reinterpret_cast<const uint4*>(mask);
+        const bool edge = (seen.x & seen.y & seen.z & seen.w) != 0xFFFFFFFFu;
+        const uint32_t nc = sb + kShNc + buf * 2 * kTile * 4;
+        uint32_t pw[64];
+        float sum = 0.0f;
+        #pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          const uint64_t off = pair(kBase - m, kBase - m);
+          float top0 = -INFINITY, top1 = -INFINITY;
+          uint64_t acc = pair(0.0f, 0.0f);
+          uint32_t x[2][16];
+          tmem_ld16(x[0], tS);
+          #pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            tmem_ld_wait(x[c & 1]);
+            if (c < 7) tmem_ld16(x[(c + 1) & 1], tS + 16 * (c + 1));
+            float y[16];
+            #pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t a[4], i1[4];
+              lds128(a, nc + (16 * c + 4 * q) * 4);
+              lds128(i1, nc + (kTile + 16 * c + 4 * q) * 4);
+              #pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint64_t t = mul2(pair(x[c & 1][4 * q + 2 * e], x[c & 1][4 * q + 2 * e + 1]), pair(a[2 * e], a[2 * e + 1]));
+                unpair(fma2(t, fa, fma2(pair(i1[2 * e], i1[2 * e + 1]), fb, off)), y[4 * q + 2 * e], y[4 * q + 2 * e + 1]);
+              }
+            }
+            if (edge) {
+              const uint32_t bits = (c < 2 ? seen.x : (c < 4 ? seen.y : (c < 6 ? seen.z : seen.w))) >> (16 * (c & 1));
+              #pragma unroll
+              for (int q = 0; q < 16; ++q) y[q] = (bits >> q) & 1u ? y[q] : -INFINITY;
+            }
+            #pragma unroll
+            for (int q = 0; q < 16; q += 4) {
+              top0 = max3(top0, y[q], y[q + 1]);
+              top1 = max3(top1, y[q + 2], y[q + 3]);
+            }
+            #pragma unroll
+            for (int q = 0; q < 16; q += 2) {
+              const float e0 = ex2(y[q]), e1 = ex2(y[q + 1]);
+              pw[8 * c + q / 2] = pack_f16(e0, e1);
+              acc = add2(acc, pair(e0, e1));
+            }
+          }
+          float s0, s1;
+          unpair(acc, s0, s1);
+          sum = __fadd_rn(s0, s1);
+          const float top = fmaxf(top0, top1) - kBase;  // relative to m
+          const bool up = top > kTau || (!have && top > -INFINITY);
+          if (pass == 1 || !__any_sync(kFull, up)) break;
+          // raise references: the row's sums so far come down by 2^(m - m')
+          const float alpha = up && have ? ex2(-top) : 1.0f;
+          m = up ? m + top : m;
+          have |= up;
+          l = __fmul_rn(l, alpha);
+          if (j >= 2) {
+            if (!wait(&o_done[w], ((j >> 1) - 1) & 1)) break;
+            tc_after();
+            #pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o, tO + 16 * c);
+              tmem_ld_wait(o);
+              #pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__fmul_rn(__uint_as_float(o[q]), alpha));
+              tmem_st16(tO + 16 * c, o);
+            }
+          }
+        }
+        if (!ok) break;
+        l = __fadd_rn(l, sum);
+        #pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st16(tS + 16 * c, pw + 16 * c);
+        tmem_st_wait();
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[w]);
+    }
+    // the lane's sums
+    const int mine = jobs > w ? (jobs - w + 1) / 2 : 0;
+    if (ok && mine > 0 && wait(&o_done[w], (mine - 1) & 1)) {
+      tc_after();
+      float* out = s.pieces + ((static_cast<int64_t>(u) * 2 + w) * 128 + r) * kRow;
+      if (warp_rows) {
+        if (row < s.R) *reinterpret_cast<float2*>(out) = make_float2(have ? m : kNoRef, l);
+        #pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[16];
+          tmem_ld16(o, tO + 16 * c);
+          tmem_ld_wait(o);
+          if (row < s.R) {
+            #pragma unroll
+            for (int q = 0; q < 16; q += 2)
+              *reinterpret_cast<uint2*>(out + 2 + 16 * c + q) = make_uint2(o[q], o[q + 1]);
+          }
+        }
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ------------------------------------------------------------------ expansion
+    const int g = warp - kSoftWarps;  // block of the tile for the signs, 32-channel group for the values
+    const int ch = 32 * g + lane;
+    const int bit_row = 8 * ((lane >> 1) & 3) + 2 * (lane >> 3) + (lane & 1);
+    for (int k = 0; k < tiles; ++k) {
+      const int raw = k % kRaw, buf = k % kBuf;
+      if (!wait(&raw_full[raw], (k / kRaw) & 1)) break;
+      if (k >= kBuf && !wait(&kv_empty[buf], (k / kBuf - 1) & 1)) break;
+      const uint32_t absent = s_absent[raw];
+      uint8_t* blk = smem + kShRaw + raw * kRawBytes;
+      const uint32_t blk_s = sb + kShRaw + raw * kRawBytes;
+      const int tok0 = (t0 + k) * kTile;
+      {  // token 32 g + lane: signs as +-1 in f8, its factors
+        const bool on = tok0 + 32 * g + lane < n && !((absent >> g) & 1u);
+        uint32_t bits[4];
+        lds128(bits, blk_s + g * kBlkBytes + bit_row * 16);
+        const float ncv = on ? reinterpret_cast<const float*>(blk + g * kBlkBytes + kBlkOffNc)[lane] : 0.0f;
+        const int i1 = 2 * (__popc(bits[0]) + __popc(bits[1]) + __popc(bits[2]) + __popc(bits[3])) - kD;
+        float* ncp = reinterpret_cast<float*>(smem + kShNc) + buf * 2 * kTile + 32 * g + lane;
+        ncp[0] = ncv;
+        ncp[kTile] = __fmul_rn(ncv, static_cast<float>(i1));
+        const uint32_t seen = __ballot_sync(kFull, on);
+        if (lane == 0) reinterpret_cast<uint32_t*>(smem + kShMask)[buf * 4 + g] = seen;
+        uint8_t* krow = smem + kShK + buf * kKBytes + (32 * g + lane) * 128;
+        #pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[4];
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 4 * (c & 1) + i;
+            v[i] = ((~bits[c >> 1] << (7 - rr)) & 0x80808080u) | 0x38383838u;
+          }
+          *reinterpret_cast<uint4*>(krow + ((c ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      // channel ch: the values of all tokens
+      #pragma unroll 1
+      for (int b = 0; b < kTileBlocks; ++b) {
+        const int left = n - tok0 - 32 * b;
+        const bool gone = ((absent >> b) & 1u) != 0;
+        if (left < 32 || gone) {  // unseen tokens' values are zeros, whatever their places hold
+          if (gone || lane >= left) {
+            reinterpret_cast<uint16_t*>(blk + b * kBlkBytes + kBlkOffScale)[32 * g + lane] = 0;
+            reinterpret_cast<uint16_t*>(blk + b * kBlkBytes + kBlkOffMin)[32 * g + lane] = 0;
+          }
+          __syncwarp();
+        }
+        const uint32_t base = blk_s + b * kBlkBytes;
+        uint32_t cw[4];
+        lds128(cw, base + kBlkOffCodes + ch * 16);
+        uint8_t* vrow = smem + kShV + buf * kVBytes + (b >> 1) * (kVBytes / 2) + ch * 128;
+        #pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t c[4], sc[4], mn[4];
+          lds128(sc, base + kBlkOffScale + g * 64 + q * 16);
+          lds128(mn, base + kBlkOffMin + g * 64 + q * 16);
+          expand_codes(cw[q], c);
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) c[i] = hfma2(c[i], sc[i], mn[i]);
+          *reinterpret_cast<uint4*>(vrow + (((4 * (b & 1) + q) ^ (lane & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&kv_full[buf]);
+        mbar_arrive(&raw_empty[raw]);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ products, in the jobs' order
+    auto scores = [&](int j) {
+      const int w = j & 1, k = two ? j >> 1 : j, buf = k % kBuf;
+      if (!wait(&kv_full[buf], (k / kBuf) & 1)) return;
+      tc_after();
+      if (lane == 0) {
+        const uint64_t a = operand(sb + kShQ + (two ? w * kQBytes : 0)), b = operand(sb + kShK + buf * kKBytes);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) mma_f8(tmem + w * 256, a + 2 * i, b + 2 * i, i > 0);  // 32 channels each
+        tc_commit(&s_full[w]);
+      }
+      __syncwarp();
+    };
+    scores(0);
+    if (ok && jobs > 1) scores(1);
+    for (int j = 0; ok && j < jobs; ++j) {
+      const int w = j & 1, k = two ? j >> 1 : j, buf = k % kBuf;
+      if (!wait(&p_full[w], (j >> 1) & 1)) break;
+      tc_after();
+      if (lane == 0) {
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {  // 16 tokens each
+          const uint64_t b = operand(sb + kShV + buf * kVBytes + (i >> 2) * (kVBytes / 2)) + 2 * (i & 3);
+          mma_f16_ta(tmem + w * 256 + 128, tmem + w * 256 + 8 * i, b, j >= 2 || i > 0);
+        }
+        tc_commit(&o_done[w]);
+        if (!two || w == 1) tc_commit(&kv_empty[buf]);
+      }
+      __syncwarp();
+      if (j + 2 < jobs) scores(j + 2);
+    }
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------------ copies: lane b < 4 block b
+    const int nblk = (n + kBlkTok - 1) / kBlkTok;
+    auto entry = [&](int k) {
+      const int blk = (t0 + k) * kTileBlocks + lane;
+      return lane < kTileBlocks && blk < nblk ? __ldg(p.prefix_pages + (blk >> p.c.bpp_shift)) : -1;
+    };
+    int page = entry(0), k = 0;
+    for (; k < tiles; ++k) {
+      const int raw = k % kRaw;
+      if (k >= kRaw && !wait(&raw_empty[raw], (k / kRaw - 1) & 1)) break;
+      const int blk = (t0 + k) * kTileBlocks + lane;
+      const bool want = lane < kTileBlocks && blk < nblk;
+      const bool here = want && page >= 0 && page < p.c.num_pages;
+      const uint32_t have = __ballot_sync(kFull, here);
+      if (want && !here && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+      if (lane == 0) {
+        s_absent[raw] = ~have & 0xFu;
+        asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&raw_full[raw])),
+                     "r"(__popc(have) * kBlkBytes)
+                     : "memory");
+      }
+      __syncwarp();
+      if (here) {
+        const int in = blk & ((1 << p.c.bpp_shift) - 1);
+        const uint8_t* src = p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + h) << p.c.bpp_shift) + in) * kBlkBytes);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         sb + kShRaw + raw * kRawBytes + lane * kBlkBytes),
+                     "l"(src), "r"(kBlkBytes), "r"(smem_u32(&raw_full[raw]))
+                     : "memory");
+      }
+      if (k + 1 < tiles) page = entry(k + 1);
+    }
+    // no copy may outlive the CTA, also where the expansion gave up
+    for (int i = k > kRaw ? k - kRaw : 0; i < k; ++i) mbar_wait(&raw_full[i % kRaw], (i / kRaw) & 1, kWaitTries);
+  }
+  if (!ok && lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_TIMEOUT);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 0) tmem_free(tmem);
+}
+
+// One (sequence, kv-head, query head) per block: the prefix's pieces and the sequence's own.
+__global__ void __launch_bounds__(128) paged_shared_merge_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G) {
+  __shared__ uint32_t pre[kMaxSeqs + 1];
+  __shared__ int slen[kMaxSeqs];
+  pdl_wait();
+  const Plan pl = make_plan<128>(p, pre, slen, p.ncta, false);
+  const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x - b * p.c.Hkv, g = blockIdx.y;
+  const int64_t out_row = static_cast<int64_t>(b) * p.Hq + static_cast<int64_t>(h) * G + g;
+  // own tokens: one row, or the pieces of CTAs c0 .. c1
+  const float* own = nullptr;
+  int own_n = 0;
+  int64_t own_step = 0;
+  const float* own_first = nullptr;
+  if (pre[b + 1] > pre[b]) {
+    const int64_t nb = pre[b + 1] - pre[b], base = static_cast<int64_t>(pre[b]) * pl.Hkv + h * nb, end = base + nb;
+    const int c0 = pl.owner(base), c1 = pl.owner(end - 1);
+    if (c0 == c1) {
+      own_first = p.rows + out_row * kRow;
+      own_n = 1;
+    } else {
+      own_first = p.part + ((static_cast<int64_t>(c0) * 2 + 1) * G + g) * kRow;
+      own = p.part + ((static_cast<int64_t>(c0) * 2) * G + g) * kRow;
+      own_step = 2LL * G * kRow;
+      own_n = c1 - c0 + 1;
+    }
+  }
+  const int r = b * G + g, rows = s.two ? 256 : 128, rt = r / rows, in = r - rt * rows;
+  const int64_t nt = (prefix_tokens(p, false) + kTile - 1) / kTile;
+  const int per = s.two ? 1 : 2;  // pieces of a split
+  const int n = own_n + s.splits * per;
+  auto piece = [&](int i) -> const float* {
+    if (i < own_n) return i == 0 ? own_first : own + i * own_step;
+    const int k = i - own_n, sp = k / per, w = s.two ? in >> 7 : k & 1;
+    const int64_t tiles = nt * (sp + 1) / s.splits - nt * sp / s.splits;
+    if (tiles <= (s.two ? 0 : w)) return nullptr;
+    const int64_t u = (static_cast<int64_t>(h) * s.row_tiles + rt) * s.splits + sp;
+    return s.pieces + ((u * 2 + w) * 128 + (in & 127)) * kRow;
+  };
+  float M = kNoRef;
+  for (int i = 0; i < n; ++i) {
+    const float* r0 = piece(i);
+    if (r0) M = fmaxf(M, r0[0]);
+  }
+  float num = 0.0f, den = 0.0f;
+  #pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* r0 = piece(i);
+    if (!r0) continue;
+    const float f = ex2(r0[0] - M);
+    num = __fmaf_rn(f, r0[2 + threadIdx.x], num);
+    den = __fmaf_rn(f, r0[1], den);
+  }
+  store_out(p.out, p.q_dtype, out_row * kD + threadIdx.x, den != 0.0f ? __fdiv_rn(num, den) : 0.0f);
+}
+
+}  // namespace paged
+}  // namespace kv1b
+
+using namespace kv1b;
+
+cudaError_t kv1b_launch_paged_shared(const PagedAttendParams& p, const PagedSharedParams& s, int32_t G, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = configure_smem(reinterpret_cast<const void*>(paged::paged_prefix_kernel), paged::kShSmem, &configured);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(p.B) * p.Hq;
+  e = launch_pdl(paged::paged_query_codes_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p, s, G);
+  if (e != cudaSuccess) return e;
+  const unsigned units = static_cast<unsigned>(p.c.Hkv) * s.row_tiles * s.splits;
+  e = launch_pdl(paged::paged_prefix_kernel, dim3(units), dim3(paged::kShThreads), paged::kShSmem, stream, p, s);
+  if (e != cudaSuccess) return e;
+  e = kv1b_launch_paged_attend(p, G, stream);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged::paged_shared_merge_kernel, dim3(static_cast<unsigned>(p.B) * p.c.Hkv, G), dim3(128), 0, stream, p, s, G);
+}

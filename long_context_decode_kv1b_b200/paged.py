@@ -197,7 +197,7 @@ class PagedCache:
         if n is None:
             with torch.cuda.device(self.device):
                 n = lib().kv1b_paged_attend_workspace_bytes(self._ref, key[1]) if key[0] == 0 else \
-                    lib().kv1b_paged_shared_workspace_bytes(self._ref, key[0], key[1])
+                    lib().kv1b_paged_shared_workspace_bytes(self._ref, *key)
             if n == 0:
                 raise Kv1bError(-1, "kv1b_paged_attend_workspace_bytes")
             self._ws_bytes[key] = n
@@ -234,7 +234,7 @@ class PagedCache:
             raise ValueError("prefix_length must hold one number and prefix_pages one page at least")
         if q.shape[0] == 0:
             return out
-        ws = self._workspace((q.shape[0], q.shape[1]), s)
+        ws = self._workspace((q.shape[0], q.shape[1], prefix_pages.shape[0]), s)
         with torch.cuda.device(self.device):
             _check(lib().kv1b_paged_attend_shared(self._ref, q.data_ptr(), _dtype_code(q), q.shape[1], scale, q.shape[0],
                                                   prefix_pages.data_ptr(), prefix_pages.shape[0], prefix_length.data_ptr(),

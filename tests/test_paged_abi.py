@@ -45,11 +45,12 @@ def test_bytes(lib):
         assert lib.kv1b_paged_bytes(*bad) == 0
     d = desc()
     assert lib.kv1b_paged_attend_workspace_bytes(ctypes.addressof(d), 8) > 0
-    assert lib.kv1b_paged_shared_workspace_bytes(ctypes.addressof(d), 4, 8) > 0
+    assert lib.kv1b_paged_shared_workspace_bytes(ctypes.addressof(d), 4, 8, 5) > 0
     for hq in (0, 3, 18):
         assert lib.kv1b_paged_attend_workspace_bytes(ctypes.addressof(d), hq) == 0
-    assert lib.kv1b_paged_shared_workspace_bytes(ctypes.addressof(d), 0, 8) == 0
-    assert lib.kv1b_paged_shared_workspace_bytes(ctypes.addressof(d), 1025, 8) == 0
+    assert lib.kv1b_paged_shared_workspace_bytes(ctypes.addressof(d), 0, 8, 5) == 0
+    assert lib.kv1b_paged_shared_workspace_bytes(ctypes.addressof(d), 1025, 8, 5) == 0
+    assert lib.kv1b_paged_shared_workspace_bytes(ctypes.addressof(d), 4, 8, 0) == 0
 
 
 def test_signs_refusals(lib):
