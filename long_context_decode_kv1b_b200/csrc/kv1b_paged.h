@@ -76,6 +76,7 @@ struct PagedAttendParams {
   int32_t max_prefix_pages;
   void* out;               // q_dtype [B][Hq][128]
   float* part;             // [ctas][2][G][2 + 128]
+  float* first;            // [ctas][16 warps][G][2 + 128]: ends of segments inside a warp's run
   float* rows;             // null, or [B][Hq][2 + 128]: whole segments leave (m, l, o) here, none is normalised
   int32_t ncta;
 };

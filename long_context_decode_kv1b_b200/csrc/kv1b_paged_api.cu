@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int64_t kMaxBlocks = 1LL << 30;  // blocks of one kv-head that a call's page tables may name
+constexpr int64_t kMaxBlocks = 1LL << 30;  // blocks of one kv-head that a call's page tables may name; 64 times as many in all
 
 bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 bool dtype_ok(int32_t dt) { return dt == KV1B_DTYPE_F32 || dt == KV1B_DTYPE_BF16 || dt == KV1B_DTYPE_F16; }
@@ -65,7 +65,8 @@ int table_check(const kv1b_paged_t* c, int32_t num_seqs, int64_t table_stride, i
   if (num_seqs > 1 && table_stride < max_pages) return KV1B_ERR_INVALID_ARG;
   if (num_seqs > KV1B_PAGED_MAX_SEQS) return KV1B_ERR_UNSUPPORTED;
   const int64_t bpp = c->page_tokens / KV1B_PAGED_BLOCK_TOKENS;
-  if (num_seqs * bpp * (static_cast<int64_t>(max_pages) + prefix_pages) > kMaxBlocks) return KV1B_ERR_UNSUPPORTED;
+  const int64_t blocks = num_seqs * bpp * (static_cast<int64_t>(max_pages) + prefix_pages);
+  if (blocks > kMaxBlocks || blocks * c->num_kv_heads > kMaxBlocks * 64) return KV1B_ERR_UNSUPPORTED;
   if (bpp * max_pages * KV1B_PAGED_BLOCK_TOKENS > 0x7fffffff || bpp * prefix_pages * KV1B_PAGED_BLOCK_TOKENS > 0x7fffffff)
     return KV1B_ERR_UNSUPPORTED;
   return KV1B_OK;
@@ -163,7 +164,7 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
 size_t kv1b_paged_attend_workspace_bytes(const kv1b_paged_t* cache, int32_t num_q_heads) {
   if (!paged_ok(cache) || heads_check(cache, num_q_heads) != KV1B_OK) return 0;
   const size_t G = num_q_heads / cache->num_kv_heads;
-  const size_t n = static_cast<size_t>(num_sms()) * 2 * G * kv1b::kPartStride * 4;
+  const size_t n = static_cast<size_t>(num_sms()) * (2 + 16) * G * kv1b::kPartStride * 4;  // part, first
   return (n + 255) / 256 * 256;
 }
 
@@ -255,8 +256,9 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   p.prefix_len = prefix_length;
   p.max_prefix_pages = max_prefix_pages;
   p.out = out;
-  p.part = static_cast<float*>(ws);
   p.ncta = num_sms();
+  p.part = static_cast<float*>(ws);
+  p.first = p.part + static_cast<size_t>(p.ncta) * 2 * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride;
   const int32_t G = num_q_heads / cache->num_kv_heads;
   if (!prefix_pages) return cuda_status(kv1b_launch_paged_attend(p, G, static_cast<cudaStream_t>(stream)));
   kv1b::PagedSharedParams s =

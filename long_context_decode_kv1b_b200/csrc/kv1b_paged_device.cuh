@@ -121,6 +121,8 @@ __device__ __forceinline__ Visible visible(int len, int window, int sinks) {
 struct Plan {
   const uint32_t* pre;  // [B + 1] blocks of one kv-head before each sequence
   const int* len;
+  const uint16_t* some; // [nsome] the sequences that see a block, in order (only where asked for)
+  int nsome;
   int B, Hkv, n;        // n: CTAs with work
   int64_t S;            // blocks in all
   __device__ __forceinline__ int64_t begin(int c) const { return S * c / n; }
@@ -145,15 +147,15 @@ struct Plan {
 
 // All threads of the CTA; lengths are limited to what the page table can hold.
 template <int THREADS>
-__device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* pre, int* len, int ncta, bool report) {
-  __shared__ uint32_t s_tot[THREADS / 32];
+__device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* pre, int* len, uint16_t* some, int ncta, bool report) {
+  __shared__ uint64_t s_tot[THREADS / 32];  // blocks, and sequences with some << 40
   const int per = (p.B + THREADS - 1) / THREADS;
   const int page_shift = p.c.bpp_shift + 5;
   const int64_t most = static_cast<int64_t>(p.max_pages) << page_shift;
   Plan pl;
   bool bad = false;
   const int b0 = threadIdx.x * per;
-  uint32_t mine = 0;
+  uint64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = b0 + i;
     if (b >= p.B) break;
@@ -161,36 +163,42 @@ __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* 
     bad |= n < 0 || n > most;
     const int nn = n < 0 ? 0 : static_cast<int>(n > most ? most : n);
     len[b] = nn;
-    mine += static_cast<uint32_t>(visible(nn, p.window, p.sinks).blocks);
+    const int blocks = visible(nn, p.window, p.sinks).blocks;
+    mine += static_cast<uint64_t>(blocks) | (blocks > 0 ? 1ull << 40 : 0ull);
   }
   if (bad && report && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
-  uint32_t x = mine;
+  uint64_t x = mine;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(kFull, x, o);
+    const uint64_t y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) s_tot[warp] = x;
   __syncthreads();
-  uint32_t at = x - mine, total = 0;
+  uint64_t at = x - mine, total = 0;
   for (int w = 0; w < THREADS / 32; ++w) {
-    at += w < warp ? s_tot[w] : 0u;
+    at += w < warp ? s_tot[w] : 0ull;
     total += s_tot[w];
   }
   for (int i = 0; i < per; ++i) {
     const int b = b0 + i;
     if (b >= p.B) break;
-    pre[b] = at;
-    at += static_cast<uint32_t>(visible(len[b], p.window, p.sinks).blocks);
+    pre[b] = static_cast<uint32_t>(at);
+    const int blocks = visible(len[b], p.window, p.sinks).blocks;
+    if (some && blocks > 0) some[at >> 40] = static_cast<uint16_t>(b);
+    at += static_cast<uint64_t>(blocks) | (blocks > 0 ? 1ull << 40 : 0ull);
   }
-  if (threadIdx.x == 0) pre[p.B] = total;
+  const uint32_t total_blocks = static_cast<uint32_t>(total);
+  if (threadIdx.x == 0) pre[p.B] = total_blocks;
   __syncthreads();
   pl.pre = pre;
   pl.len = len;
+  pl.some = some;
+  pl.nsome = static_cast<int>(total >> 40);
   pl.B = p.B;
   pl.Hkv = p.c.Hkv;
-  pl.S = static_cast<int64_t>(total) * p.c.Hkv;
+  pl.S = static_cast<int64_t>(total_blocks) * p.c.Hkv;
   const int64_t want = (pl.S + kMinBlocks - 1) / kMinBlocks;
   pl.n = static_cast<int>(want < 1 ? 1 : (want < ncta ? want : ncta));
   return pl;

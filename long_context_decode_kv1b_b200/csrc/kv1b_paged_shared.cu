@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(128) paged_shared_merge_kernel(const PagedAtte
   __shared__ uint32_t pre[kMaxSeqs + 1];
   __shared__ int slen[kMaxSeqs];
   pdl_wait();
-  const Plan pl = make_plan<128>(p, pre, slen, p.ncta, false);
+  const Plan pl = make_plan<128>(p, pre, slen, nullptr, p.ncta, false);
   const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x - b * p.c.Hkv, g = blockIdx.y;
   const int64_t out_row = static_cast<int64_t>(b) * p.Hq + static_cast<int64_t>(h) * G + g;
   // own tokens: one row, or the pieces of CTAs c0 .. c1
