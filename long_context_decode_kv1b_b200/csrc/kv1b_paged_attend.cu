@@ -17,12 +17,20 @@
 //            with the row order of the block, all eight tokens of its code words, so probabilities are
 //            formed where the next product wants them and nothing is shuffled;
 //   softmax  log2 units against a reference that a warp raises only when a logit passes it by kTau;
-//   P.V      f16 m16n8k16 products: A = 16 channels x 16 tokens expanded from the codes in registers
-//            (v = min + scale code by one fma per pair of tokens, a single rounding to binary16), B = the
-//            probabilities as binary16, fp32 sums.  The normaliser is summed by the same product with a
-//            row of ones, so the roundings of the weights cancel in the quotient.
-// Values and weights are rounded to 11 bits because the result is: out has the query's 16-bit type.
-// Weights are 2^(x - m + kBase) <= 2^15, so a weight keeps its 11 bits down to 2^-21 of the reference.
+//   P.V      v = min + scale code, so sum p v = sum p min + sum (p scale) code.  f16 m16n8k16 products with
+//            fp32 sums: A = 16 channels x 16 tokens of codes, one AND per register (a nibble in the low
+//            mantissa bits is a binary16 subnormal, code 2^-24, or 2^-20 where the nibble is the byte's
+//            upper one: those tokens' weights are 2^-4 lower), B = p scale, one multiplication per pair of
+//            tokens and value group.  A last pair of products with the four groups' mins and a row of ones
+//            gives sum p min and the normaliser from the same binary16 p, so p's rounding cancels in the
+//            quotient.
+// Roundings: p scale is rounded to 11 bits for bf16 results, which have 8; for fp16 results its remainder
+// (exact: the product of two 11-bit numbers has 22) goes through a second set of products.
+// Range: p = 2^(x - m + kBase) <= 2^15 and scale < 2 keep p scale finite; a block with a larger scale lowers
+// the weights by its power of two.  A weight keeps 11 bits down to 2^-21 of the reference.
+//
+// 609 warp instructions a block (values expanded to binary16 by fma, a page entry and an address per
+// block) became about 330: the issue slots were 64 % busy at 243 us for 1M tokens x 8 heads.
 #include "kv1b_paged_device.cuh"
 
 namespace kv1b {
@@ -47,18 +55,24 @@ constexpr int kOffSome = kOffLen + kMaxSeqs * 4;                 // u16 [kMaxSeq
 constexpr int kOffSeg = kOffSome + kMaxSeqs * 2;                 // Seg [kMaxSegs]
 constexpr int kOffPlane = kOffSeg + kMaxSegs * 16;               // u32 [kQuerySlots][4 planes][4]
 constexpr int kOffConst = kOffPlane + kQuerySlots * 64;          // f32 [kQuerySlots][4]: c1, c2, c0
-constexpr int kSmem = kOffConst + kQuerySlots * 16;
+constexpr int kOffRows = kOffConst + kQuerySlots * 16;           // f16 [2][8]: ones, zeros
+constexpr int kSmem = kOffRows + 32;
 constexpr int kOffRed = 0;                                       // f32 [kWarps][G][kRow], over the ring once it is drained
-static_assert(kOffPre % 16 == 0 && kWarps * KV1B_MAX_GROUP * kRow * 4 <= kOffPre && kSmem + 2048 <= 227 * 1024, "shared memory");
+static_assert(kOffPre % 16 == 0 && kOffRows % 16 == 0 && kWarps * KV1B_MAX_GROUP * kRow * 4 <= kOffPre && kSmem + 2048 <= 227 * 1024, "shared memory");
 
 // Block i of a segment: its place in the sequence.
 __device__ __forceinline__ int own_block(const Visible& v, int j) { return j < v.skip_from ? j : j + (v.skip_to - v.skip_from); }
 
-// A place in a round's blocks: segment and block within it.
-struct Walk {
-  int s, i, left;  // segment, block of it, blocks of the warp's run that are left
+// The copy side's place in a round's blocks.  Stretches of blocks that lie behind one another in a page
+// are walked by a pointer; the page entry of the next stretch is loaded when one begins.
+struct Ahead {
+  const uint8_t* ptr;  // next block, null where the page is not there
+  int in;              // blocks of the stretch that are left
+  int left;            // blocks of the warp's run behind the stretch
+  int s, i;            // segment and block behind the stretch
   int b, h, nb;
   Visible vis;
+  int page;            // page entry there
   __device__ __forceinline__ void enter(const Seg* seg, const Plan& pl, const PagedAttendParams& p) {
     const Seg g = seg[s];
     b = g.b;
@@ -66,20 +80,39 @@ struct Walk {
     nb = g.nb;
     vis = visible(pl.len[b], p.window, p.sinks);
   }
-  __device__ __forceinline__ void step(const Seg* seg, const Plan& pl, const PagedAttendParams& p) {
-    --left;
-    if (++i == nb && left > 0) {
-      ++s;
-      i = 0;
-      enter(seg, pl, p);
+  __device__ __forceinline__ void look_up(const PagedAttendParams& p) {
+    page = __ldg(p.table + b * p.table_stride + (own_block(vis, i) >> p.c.bpp_shift));
+  }
+  __device__ __forceinline__ void next_stretch(const Seg* seg, const Plan& pl, const PagedAttendParams& p) {
+    const int blk = own_block(vis, i), off = blk & ((1 << p.c.bpp_shift) - 1);
+    const bool ok = page >= 0 && page < p.c.num_pages;
+    ptr = ok ? p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + h) << p.c.bpp_shift) + off) * kBlkBytes) : nullptr;
+    if (!ok && (threadIdx.x & 31) == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+    in = min(min((1 << p.c.bpp_shift) - off, nb - i), left);
+    if (i < vis.skip_from) in = min(in, vis.skip_from - i);
+    left -= in;
+    i += in;
+    if (left > 0) {
+      if (i == nb) {
+        ++s;
+        i = 0;
+        enter(seg, pl, p);
+      }
+      look_up(p);
     }
   }
 };
 
-__device__ __forceinline__ int page_entry(const PagedAttendParams& p, const Walk& w) {
-  return __ldg(p.table + w.b * p.table_stride + (own_block(w.vis, w.i) >> p.c.bpp_shift));
+// The first block from i on of which the query may see only a part: where the sinks end, where the window
+// begins (the first block of all where there is none), the last one.
+__device__ __forceinline__ int next_edge(const Visible& v, int i, int nb) {
+  return i < v.skip_from ? v.skip_from - 1 : (i == v.skip_from ? i : nb - 1);
 }
 
+constexpr float kCodeUnit = 16777216.0f;  // codes enter the products as binary16 subnormals, units of 2^-24
+
+// kFine: the weights of the codes in two binary16 parts (fp16 results); one part is enough for bf16.
+template <bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAttendParams p, const int G) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
@@ -111,6 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
   const int max_segs = min(kMaxSegs, kQuerySlots / G);
   const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
   float* first = p.first + (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * G * kRow;
+  if (threadIdx.x < 8) reinterpret_cast<uint32_t*>(smem + kOffRows)[threadIdx.x] = threadIdx.x < 4 ? 0x3C003C00u : 0u;
+  const uint32_t side_row = smem_u32(smem) + kOffRows + (g == 4 ? 0 : 16);  // rows 4 and 5 .. 7 of the side product
   uint32_t phases = 0;  // bit s: parity of stage s's next completion
   bool gave_up = false;
 
@@ -125,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
         else hi = mid;
       }
       const int b0 = pl.some[lo];
-      const int h0 = static_cast<int>((a - static_cast<int64_t>(pre[b0]) * pl.Hkv) / (pre[b0 + 1] - pre[b0]));
+      const int h0 = static_cast<int>(quotient(a - static_cast<int64_t>(pre[b0]) * pl.Hkv, pre[b0 + 1] - pre[b0]));
       if (static_cast<int>(threadIdx.x) < max_segs) {
         const int id = h0 + threadIdx.x, k = lo + id / pl.Hkv, h = id % pl.Hkv;
         Seg sg = {0x7fffffff, 0, 0, 0};
@@ -141,30 +176,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
     int nseg = max_segs, n;  // segments and blocks of the round
     while (seg[nseg - 1].nb == 0) --nseg;
     n = static_cast<int>(min(r1 - a, static_cast<int64_t>(seg[nseg - 1].base) + seg[nseg - 1].nb));
-    auto run_begin = [&](int w) { return static_cast<int>(static_cast<int64_t>(n) * w / kWarps); };
-    auto run_owner = [&](int x) { return static_cast<int>(((x + 1LL) * kWarps - 1) / n); };
+    const int run_q = n / kWarps, run_r = n % kWarps;  // the first run_r runs are one longer
+    auto run_begin = [&](int w) { return w * run_q + min(w, run_r); };
+    auto run_owner = [&](int x) {
+      const int longer = run_r * (run_q + 1);
+      return x < longer ? x / (run_q + 1) : run_r + (x - longer) / run_q;
+    };
     const int w0 = run_begin(warp), w1 = run_begin(warp + 1);
 
     // ---- copy side: `ahead` walks kStages blocks in front of the compute
-    Walk ahead, cur;
+    Ahead ahead;
+    ahead.in = 0;
     ahead.left = w1 - w0;
     uint32_t absent = 0;  // bit s: stage s holds no block (its page is outside the cache)
-    int pend = 0;         // page entry of the block `ahead` stands at
-    auto issue = [&](int s, int page) {
-      const bool ok = page >= 0 && page < p.c.num_pages;
-      absent = ok ? absent & ~(1u << s) : absent | (1u << s);
-      if (lane == 0) {
-        if (ok) {
-          const int in = own_block(ahead.vis, ahead.i) & ((1 << p.c.bpp_shift) - 1);
-          const uint8_t* src = p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + ahead.h) << p.c.bpp_shift) + in) * kBlkBytes);
-          block_g2s(ring + s * kBlkBytes, src, &bars[warp][s]);
-        } else if (p.c.status) {
-          atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
-        }
+    auto issue = [&](int s) {
+      if (ahead.in == 0) ahead.next_stretch(seg, pl, p);
+      absent = ahead.ptr ? absent & ~(1u << s) : absent | (1u << s);
+      if (ahead.ptr) {
+        if (lane == 0) block_g2s(ring + s * kBlkBytes, ahead.ptr, &bars[warp][s]);
+        ahead.ptr += kBlkBytes;
       }
-      ahead.step(seg, pl, p);
+      --ahead.in;
     };
-    if (ahead.left > 0) {
+    struct { int s, i, left, b, h, nb; Visible vis; } cur = {0, 0, w1 - w0, 0, 0, 0, {0, 0, 0}};
+    if (cur.left > 0) {
       int k = 0;  // the segment of block w0
       for (int x = lane; x < nseg; x += 32)
         if (seg[x].base <= w0) k = x;
@@ -172,12 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
       ahead.s = k;
       ahead.i = w0 - seg[k].base;
       ahead.enter(seg, pl, p);
-      cur = ahead;
-      for (int s = 0; s < kStages && ahead.left > 0 && !gave_up; ++s) issue(s, page_entry(p, ahead));
-      if (ahead.left > 0) pend = page_entry(p, ahead);
-    } else {
-      cur = Walk();
-      cur.left = 0;
+      ahead.look_up(p);
+      cur = {k, ahead.i, cur.left, ahead.b, ahead.h, ahead.nb, ahead.vis};
+      for (int s = 0; s < kStages && ahead.in + ahead.left > 0 && !gave_up; ++s) issue(s);
     }
 
     // ---- the round's queries
@@ -196,22 +228,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
     }
     __syncthreads();
 
-    float acc[8][4], lsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    // acc: sums of weight scale code (units of 2^-24); side: rows 0 .. 3 sums of weight min per group, row 4 of weight
+    float acc[8][4], side[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
     float m = kNoRef;  // reference of head g
+    // element (i, e, hi) of the weighted value sum of head 2 t + e, channel 16 i + g + 8 hi
+    auto value = [&](int i, int e, int hi) {
+      return __fmaf_rn(acc[i][2 * hi + e], kCodeUnit, __shfl_sync(kFull, side[e], 4 * (i >> 1) + t));
+    };
     // the warp's sums of a segment to a piece [head][kRow]
     auto put_piece = [&](float* w) {
       if (t == 0 && g < G) w[g * kRow] = m;
       #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int hd = 2 * t + e;
-        if (hd < G) {
-          if (g == 0) w[hd * kRow + 1] = lsum[e];
-          #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            w[hd * kRow + 2 + 16 * i + g] = acc[i][e];
-            w[hd * kRow + 2 + 16 * i + g + 8] = acc[i][2 + e];
+        if (g == 4 && hd < G) w[hd * kRow + 1] = side[e];
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float lo = value(i, e, 0), hi = value(i, e, 1);
+          if (hd < G) {
+            w[hd * kRow + 2 + 16 * i + g] = lo;
+            w[hd * kRow + 2 + 16 * i + g + 8] = hi;
           }
         }
       }
@@ -244,28 +282,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
       const float c1 = cc.x, c2 = cc.y, c0 = cc.z;
       #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-      lsum[0] = lsum[1] = lsum[2] = lsum[3] = 0.0f;
-      m = kNoRef;
+      side[0] = side[1] = side[2] = side[3] = 0.0f;
+      m = 0.0f;
+      bool fresh = true;   // no block has set m
+      int top_scale = 0;   // weights are 2^-top_scale lower: no scale reaches 2^(1 + top_scale)
       const bool starts = cur.i == 0;
       const int count = min(cur.left, cur.nb - cur.i);  // blocks of the segment in the warp's run
       const bool ends = cur.i + count == cur.nb;
-      const int len = pl.len[cur.b];
-      const int wstart = (p.window > 0 && len > p.window) ? len - p.window : 0;
+      int edge_at = next_edge(cur.vis, cur.i, cur.nb);
 
-      for (int e = 0; e < count; ++e) {
+      for (int x = cur.i; x < cur.i + count; ++x) {
         const uint32_t st = ring + stage * kBlkBytes;
         if (!((absent >> stage) & 1u)) {
           if (!__all_sync(kFull, mbar_wait(&bars[warp][stage], (phases >> stage) & 1u, gave_up ? 1 : kWaitTries)))
             gave_up = true;  // every lane alike
           phases ^= 1u << stage;
-          // which of the block's tokens the query sees
-          const int tok0 = own_block(cur.vis, cur.i + e) * kBlkTok;
-          const bool edge = tok0 + kBlkTok > len || (tok0 < wstart && tok0 + kBlkTok > p.sinks);
           uint32_t seen = 0xFFFFFFFFu;
-          if (edge) {
-            // unseen tokens: what their places hold (another sequence's remains, infinities) must not
-            // reach a product, so their scale, min and norm become zeros and their weights are zero
-            const int tk = tok0 + lane;
+          if (x == edge_at) {
+            // which of the block's tokens the query sees.  Unseen ones: what their places hold (another
+            // sequence's remains, infinities) must not reach a product, so their scale, min and norm
+            // become zeros and their weights are zero
+            const int len = pl.len[cur.b], tk = own_block(cur.vis, x) * kBlkTok + lane;
+            const int wstart = (p.window > 0 && len > p.window) ? len - p.window : 0;
             const bool on = tk < len && (tk >= wstart || tk < p.sinks);
             seen = __ballot_sync(kFull, on);
             if (!on) {
@@ -276,52 +314,87 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
                 reinterpret_cast<uint16_t*>(bp + kBlkOffScale)[32 * q + lane] = 0;
                 reinterpret_cast<uint16_t*>(bp + kBlkOffMin)[32 * q + lane] = 0;
               }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy to the stage
             }
             __syncwarp();
+            edge_at = next_edge(cur.vis, x + 1, cur.nb);
           }
           // ---- scores
-          float x[8];
+          float dot[8];
+          uint32_t ncr[8];
           {
             uint32_t kw[4];
             ldsm_x4(kw, st + lane * 16);
-            int d[4][4];
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // the sums start at the bits of 1.5 2^23: as a float, an entry is that plus its integer
-              d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0x4B400000;
-              const uint32_t w[2] = {kw[i], kw[i] >> 4};
-              #pragma unroll
-              for (int kb = 0; kb < 4; ++kb) {
-                const int pl0 = 2 * (kb & 1);
-                const uint32_t lo = 0x01010101u << pl0, hi = lo << 1;
-                imma(d[i], aq[kb][0], 0x01010101u << (3 - pl0), aq[kb][1], 0x01010101u << (2 - pl0), w[kb >> 1] & lo, w[kb >> 1] & hi);
-              }
-            }
-            uint32_t ncr[8];
             lds128(ncr, st + kBlkOffNc + 32 * t);
             lds128(ncr + 4, st + kBlkOffNc + 32 * t + 16);
             #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+              // the sums start at the bits of 1.5 2^23: as a float, an entry is that plus its integer
+              int d[4];
+              const uint32_t w[2] = {kw[i], kw[i] >> 4};
+              imma_from(d, 0x4B400000, aq[0][0], 0x08080808u, aq[0][1], 0x04040404u, w[0] & 0x01010101u, w[0] & 0x02020202u);
+              imma(d, aq[1][0], 0x02020202u, aq[1][1], 0x01010101u, w[0] & 0x04040404u, w[0] & 0x08080808u);
+              imma(d, aq[2][0], 0x08080808u, aq[2][1], 0x04040404u, w[1] & 0x01010101u, w[1] & 0x02020202u);
+              imma(d, aq[3][0], 0x02020202u, aq[3][1], 0x01010101u, w[1] & 0x04040404u, w[1] & 0x08080808u);
               #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float a8 = __fadd_rn(__int_as_float(d[i][e]), -12582912.0f);
-                const float b8 = __fadd_rn(__int_as_float(d[i][2 + e]), -12582912.0f);
-                const float dot = __fmaf_rn(c1, a8, __fmaf_rn(c2, b8, c0));
-                x[2 * i + e] = __fmul_rn(dot, __uint_as_float(ncr[2 * i + e]));
+                const float a8 = __fadd_rn(__int_as_float(d[e]), -12582912.0f);
+                const float b8 = __fadd_rn(__int_as_float(d[2 + e]), -12582912.0f);
+                dot[2 * i + e] = __fmaf_rn(c1, a8, __fmaf_rn(c2, b8, c0));
               }
+            }
           }
-          if (edge) {
+          uint32_t sc[4][4];
+          #pragma unroll
+          for (int q = 0; q < 4; ++q) lds128(sc[q], st + kBlkOffScale + q * 64 + 16 * t);
+          {
+            uint32_t any = 0;  // a scale of 2 or more has the top exponent bit
+            #pragma unroll
+            for (int q = 0; q < 4; ++q) any |= sc[q][0] | sc[q][1] | sc[q][2] | sc[q][3];
+            if (__any_sync(kFull, (any & 0x40004000u) != 0)) {  // rare: large values
+              int k = 0;
+              #pragma unroll
+              for (int q = 0; q < 4; ++q)
+                #pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  k = max(k, max(static_cast<int>(sc[q][i] & 0x7C00u), static_cast<int>((sc[q][i] >> 16) & 0x7C00u)));
+              k = __reduce_max_sync(kFull, (k >> 10) - 15);  // all scales are below 2^(1 + k)
+              if (k > top_scale) {
+                const float f = ex2(static_cast<float>(top_scale - k));
+                m += static_cast<float>(k - top_scale);
+                top_scale = k;
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  #pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[i][e] = __fmul_rn(acc[i][e], f);
+                }
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) side[e] = __fmul_rn(side[e], f);
+              }
+            }
+          }
+          // exponents of the weights: logit - m + kBase
+          float y[8];
+          {
+            const float off = kBase - m;
+            #pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = __fmaf_rn(dot[j], __uint_as_float(ncr[j]), off);
+          }
+          if (seen != 0xFFFFFFFFu) {
             const uint32_t mine = seen >> (8 * t);
             #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = (mine >> j) & 1u ? x[j] : -INFINITY;
+            for (int j = 0; j < 8; ++j) y[j] = (mine >> j) & 1u ? y[j] : -INFINITY;
           }
-          float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-          if (__any_sync(kFull, mx > m + kTau)) {  // rare: raise references
+          float mx = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+          const float bar = kBase + kTau - static_cast<float>(top_scale);
+          if (__any_sync(kFull, mx > bar) || fresh) {  // rare: raise references
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-            const bool up = mx > m + kTau;
-            const float alpha = up ? ex2(m - mx) : 1.0f;  // 0 from kNoRef
-            m = up ? mx : m;
+            const float rise = fresh || mx > bar ? mx - (bar - kTau) : 0.0f;
+            const float alpha = fresh ? 0.0f : ex2(-rise);
+            m += rise;
+            #pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] -= rise;
             const float a0 = __shfl_sync(kFull, alpha, 8 * t), a1 = __shfl_sync(kFull, alpha, 8 * t + 4);
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -330,50 +403,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
               acc[i][2] = __fmul_rn(acc[i][2], a0);
               acc[i][3] = __fmul_rn(acc[i][3], a1);
             }
-            lsum[0] = __fmul_rn(lsum[0], a0);
-            lsum[1] = __fmul_rn(lsum[1], a1);
-            lsum[2] = __fmul_rn(lsum[2], a0);
-            lsum[3] = __fmul_rn(lsum[3], a1);
+            side[0] = __fmul_rn(side[0], a0);
+            side[1] = __fmul_rn(side[1], a1);
+            fresh = false;
           }
-          const float mb = m - kBase;
           uint32_t pw[4];
           #pragma unroll
-          for (int i = 0; i < 4; ++i) pw[i] = pack_f16(ex2(x[2 * i] - mb), ex2(x[2 * i + 1] - mb));
-          hmma(lsum, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pw[0], pw[1]);
-          hmma(lsum, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pw[2], pw[3]);
+          for (int i = 0; i < 4; ++i) pw[i] = pack_f16(ex2(y[2 * i]), ex2(y[2 * i + 1]));
+          {
+            uint32_t mn[4];
+            lds128(mn, g < 4 ? st + kBlkOffMin + g * 64 + 16 * t : side_row);
+            hmma(side, mn[0], 0u, mn[1], 0u, pw[0], pw[1]);
+            hmma(side, mn[2], 0u, mn[3], 0u, pw[2], pw[3]);
+          }
+          // the codes of pairs 1 and 3 sit four bits higher
+          pw[1] = hmul2(pw[1], 0x2C002C00u);
+          pw[3] = hmul2(pw[3], 0x2C002C00u);
           // ---- P.V, value group by value group (32 channels: rows of two products)
           #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t sc[4], mn[4], cw[4];
-            lds128(sc, st + kBlkOffScale + q * 64 + 16 * t);
-            lds128(mn, st + kBlkOffMin + q * 64 + 16 * t);
+            uint32_t cw[4], wt[4], rest[4];
             ldsm_x4(cw, st + kBlkOffCodes + (32 * q + lane) * 16);  // rows g, g + 8, g + 16, g + 24; word t
             #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              wt[i] = hmul2(pw[i], sc[q][i]);
+              if (kFine) rest[i] = hfma2(pw[i], sc[q][i], wt[i] ^ 0x80008000u);
+            }
+            #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              uint32_t lo[4], hi[4];
-              expand_codes(cw[2 * u], lo);
-              expand_codes(cw[2 * u + 1], hi);
-              #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                lo[i] = hfma2(lo[i], sc[i], mn[i]);
-                hi[i] = hfma2(hi[i], sc[i], mn[i]);
+              const uint32_t lo = cw[2 * u], hi = cw[2 * u + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+              const uint32_t a0 = lo & 0x000F000Fu, a1 = hi & 0x000F000Fu, a2 = lo & 0x00F000F0u, a3 = hi & 0x00F000F0u;
+              const uint32_t b0 = lo8 & 0x000F000Fu, b1 = hi8 & 0x000F000Fu, b2 = lo8 & 0x00F000F0u, b3 = hi8 & 0x00F000F0u;
+              hmma(acc[2 * q + u], a0, a1, a2, a3, wt[0], wt[1]);
+              hmma(acc[2 * q + u], b0, b1, b2, b3, wt[2], wt[3]);
+              if (kFine) {
+                hmma(acc[2 * q + u], a0, a1, a2, a3, rest[0], rest[1]);
+                hmma(acc[2 * q + u], b0, b1, b2, b3, rest[2], rest[3]);
               }
-              hmma(acc[2 * q + u], lo[0], hi[0], lo[1], hi[1], pw[0], pw[1]);
-              hmma(acc[2 * q + u], lo[2], hi[2], lo[3], hi[3], pw[2], pw[3]);
             }
           }
-          if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // own writes before the next copy
         }
         __syncwarp();
         // ---- the stage's next block
-        if (ahead.left > 0 && !gave_up) {
-          issue(stage, pend);
-          if (ahead.left > 0) pend = page_entry(p, ahead);
-        } else if (gave_up) {
-          absent |= 1u << stage;
-        }
+        if (ahead.in + ahead.left > 0 && !gave_up) issue(stage);
+        else if (gave_up) absent |= 1u << stage;
         stage = stage + 1 == kStages ? 0 : stage + 1;
       }
+      if (fresh) m = kNoRef;
       cur.left -= count;
 
       if (starts && ends) {  // all of it: finished here
@@ -384,12 +460,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
           #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int hd = 2 * t + e;
-            if (hd < G) {
-              const float den = lsum[e];
-              #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                store_out(p.out, p.q_dtype, (qrow + hd) * kD + 16 * i + g, den != 0.0f ? __fdiv_rn(acc[i][e], den) : 0.0f);
-                store_out(p.out, p.q_dtype, (qrow + hd) * kD + 16 * i + g + 8, den != 0.0f ? __fdiv_rn(acc[i][2 + e], den) : 0.0f);
+            const float den = __shfl_sync(kFull, side[e], 16 + t);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float lo = value(i, e, 0), hi = value(i, e, 1);
+              if (hd < G) {
+                store_out(p.out, p.q_dtype, (qrow + hd) * kD + 16 * i + g, den != 0.0f ? __fdiv_rn(lo, den) : 0.0f);
+                store_out(p.out, p.q_dtype, (qrow + hd) * kD + 16 * i + g + 8, den != 0.0f ? __fdiv_rn(hi, den) : 0.0f);
               }
             }
           }
@@ -400,9 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
         last = true;
       }
       if (cur.left > 0) {
-        ++cur.s;
+        const Seg next = seg[++cur.s];
         cur.i = 0;
-        cur.enter(seg, pl, p);
+        cur.b = next.b;
+        cur.h = next.h;
+        cur.nb = next.nb;
+        cur.vis = visible(pl.len[cur.b], p.window, p.sinks);
       }
     }
 
@@ -498,10 +578,12 @@ using namespace kv1b;
 
 cudaError_t kv1b_launch_paged_attend(const PagedAttendParams& p, int32_t G, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = configure_smem(reinterpret_cast<const void*>(paged::paged_attend_kernel),
-                                 paged::kSmem, &configured);
+  static std::atomic<unsigned long long> configured_fine{0};
+  const bool fine = p.q_dtype == KV1B_DTYPE_F16;
+  const auto kernel = fine ? paged::paged_attend_kernel<true> : paged::paged_attend_kernel<false>;
+  cudaError_t e = configure_smem(reinterpret_cast<const void*>(kernel), paged::kSmem, fine ? &configured_fine : &configured);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged::paged_attend_kernel, dim3(p.ncta), dim3(paged::kThreads), paged::kSmem, stream, p, G);
+  e = launch_pdl(kernel, dim3(p.ncta), dim3(paged::kThreads), paged::kSmem, stream, p, G);
   if (e != cudaSuccess || p.ncta < 2 || p.rows) return e;
   return launch_pdl(paged::paged_merge_kernel, dim3(p.ncta - 1, G), dim3(128), 0, stream, p, G);
 }

@@ -55,6 +55,13 @@ __device__ __forceinline__ void imma(int d[4], uint32_t a0, uint32_t a1, uint32_
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same with every sum starting at c
+__device__ __forceinline__ void imma_from(int d[4], int c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c));
+}
 __device__ __forceinline__ void hmma(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -64,6 +71,11 @@ __device__ __forceinline__ void hmma(float d[4], uint32_t a0, uint32_t a1, uint3
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
@@ -118,6 +130,12 @@ __device__ __forceinline__ Visible visible(int len, int window, int sinks) {
   return v;
 }
 
+// a / b for a >= 0, b > 0: a 32-bit division where both fit (the 64-bit one is a long subroutine)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 struct Plan {
   const uint32_t* pre;  // [B + 1] blocks of one kv-head before each sequence
   const int* len;
@@ -125,9 +143,12 @@ struct Plan {
   int nsome;
   int B, Hkv, n;        // n: CTAs with work
   int64_t S;            // blocks in all
-  __device__ __forceinline__ int64_t begin(int c) const { return S * c / n; }
+  int64_t q;            // S / n: the first `rem` ranges are one block longer
+  int rem;
+  __device__ __forceinline__ int64_t begin(int c) const { return c * q + (c < rem ? c : rem); }
   __device__ __forceinline__ int owner(int64_t r) const {  // the CTA whose range holds block r: begin(c) <= r < begin(c + 1)
-    return static_cast<int>(((r + 1) * n - 1) / S);
+    const int64_t longer = rem * (q + 1);
+    return r < longer ? static_cast<int>(quotient(r, q + 1)) : rem + static_cast<int>(quotient(r - longer, q));
   }
   // segment of block r: sequence, head, first block
   __device__ __forceinline__ void locate(int64_t r, int* b, int* h, int64_t* base) const {
@@ -140,7 +161,7 @@ struct Plan {
     const int64_t s0 = static_cast<int64_t>(pre[lo]) * Hkv;
     const int nb = static_cast<int>(pre[lo + 1] - pre[lo]);
     *b = lo;
-    *h = static_cast<int>((r - s0) / nb);
+    *h = static_cast<int>(quotient(r - s0, nb));
     *base = s0 + static_cast<int64_t>(*h) * nb;
   }
 };
@@ -201,6 +222,8 @@ __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* 
   pl.S = static_cast<int64_t>(total_blocks) * p.c.Hkv;
   const int64_t want = (pl.S + kMinBlocks - 1) / kMinBlocks;
   pl.n = static_cast<int>(want < 1 ? 1 : (want < ncta ? want : ncta));
+  pl.q = quotient(pl.S, pl.n);
+  pl.rem = static_cast<int>(pl.S - pl.q * pl.n);
   return pl;
 }
 

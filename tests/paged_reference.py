@@ -91,8 +91,8 @@ def append(pages, k, v, table, start, cu, signs, rope=None, positions=None):
 
 
 def gather(pages, table, h, tokens):
-    """(signs +-1 [n, 128], values f64 [n, 128], nc f64 [n], limit f64 [n, 128]) of tokens of one list of
-    pages; limit is |min| + scale code, what the value's rounding is relative to."""
+    """(signs +-1 [n, 128], values f64 [n, 128], nc f64 [n], scale code f64 [n, 128], scale f64 [n, 128]) of
+    tokens of one list of pages."""
     page_tokens = pages.shape[2] * BLOCK
     bits, nc, scale, least, codes = fields(pages)
     pg = np.asarray(table)[tokens // page_tokens]
@@ -103,38 +103,47 @@ def gather(pages, table, h, tokens):
     c = ((word >> (4 * nibble(tok)).astype(np.uint32)[:, None]) & 15).astype(np.float64)
     s = scale[pg, h, blk].view(np.float16)[np.arange(len(tokens)), :, tok].astype(np.float64).repeat(32, 1)
     m = least[pg, h, blk].view(np.float16)[np.arange(len(tokens)), :, tok].astype(np.float64).repeat(32, 1)
-    return sign, m + s * c, nc[pg, h, blk, tok].astype(np.float64)
+    return sign, m + s * c, nc[pg, h, blk, tok].astype(np.float64), s * c, s
 
 
-def attend_head(q: np.ndarray, signs, scale, parts):
-    """Softmax attention of one query head in 64 bits over `parts` (gather results).  Returns (out [128],
-    weighted mean of |value| [128], the largest magnitude of a logit's terms, largest |value|, tokens)."""
-    r = oracle.query_prep(q, signs)
-    sign = np.concatenate([p[0] for p in parts])
-    val = np.concatenate([p[1] for p in parts])
-    nc = np.concatenate([p[2] for p in parts])
-    if len(nc) == 0:
-        return np.zeros(D), np.zeros(D), 0.0, 0.0, 0
-    code = r["codes"].astype(np.float64)
-    dl, vl = float(r["delta"]), float(r["vl"])
-    s = (sign @ code * dl + sign.sum(1) * vl) * nc * (scale / 128.0)
-    mag = (3 * code.sum() * abs(dl) + 384 * abs(vl)) * float(np.abs(nc).max()) * abs(scale) / 128.0
-    p = np.exp(s - s.max())
-    p /= p.sum()
-    return p @ val, p @ np.abs(val), mag, float(np.abs(val).max()), len(nc)
+class Row:
+    """Softmax attention of one query head in 64 bits over `parts` (gather results), and how far a kernel's
+    output may be from it."""
 
+    def __init__(self, q: np.ndarray, signs, scale, parts):
+        r = oracle.query_prep(q, signs)
+        sign, val, nc, reach, step = (np.concatenate([p[i] for p in parts]) for i in range(5))
+        self.tokens = len(nc)
+        self.out = np.zeros(D)
+        if self.tokens == 0:
+            return
+        code = r["codes"].astype(np.float64)
+        dl, vl = float(r["delta"]), float(r["vl"])
+        s = (sign @ code * dl + sign.sum(1) * vl) * nc * (scale / 128.0)
+        # the magnitude of a logit's terms
+        self.mag = (3 * code.sum() * abs(dl) + 384 * abs(vl)) * float(np.abs(nc).max()) * abs(scale) / 128.0
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        self.out, self.spread, self.reach = p @ val, p @ np.abs(val), p @ np.abs(reach)
+        self.largest, self.step = float(np.abs(val).max()), float(step.max())
 
-def tolerance(out, spread, mag, largest, tokens, eps):
-    """How far a kernel's output may be from the 64-bit one, channel by channel.  Relative to the weighted
-    mean of |value|: a weight's rounding to binary16 in the numerator and in the normaliser (2^-11 each),
-    a value's (2^-11, and 2^-25 absolute where it is subnormal), the fp32 logit (16 roundings of its
-    terms' magnitude) and its exponential (2^-21), twice, and 2^-18 for the fp32 sums.  A weight is 2^7 at
-    its reference, which some token attains, and one below 2^-14 may lose up to 2^-25: 2^-32 of the row's
-    sum a token, times the largest |value|, itself and through the normaliser.  At the end one rounding of
-    the result to its type, eps / 2 of it."""
-    rel = 3 * 2.0 ** -11 + 2 * (16 * 2.0 ** -24 * mag + 2.0 ** -21) + 2.0 ** -18
-    tail = 2 * tokens * 2.0 ** -32 * largest + 2.0 ** -25
-    return (1 + eps) * (rel * spread + tail) + eps / 2 * np.abs(out) + 2.0 ** -25
+    def tolerance(self, eps):
+        """Channel by channel.  Relative to the weighted mean of |value|: a weight's rounding to binary16 in
+        the numerator and in the normaliser, a value's (2^-11 each), the fp32 logit (16 roundings of its
+        terms' magnitude) and its exponential (2^-21), twice, and 2^-18 for the fp32 sums.  Relative to the
+        weighted mean of scale code: the rounding of weight scale to binary16, 2^-11, or of its second
+        part for fp16 results.  Small weights: one is 2^(7 - k) at its reference, which some token attains,
+        where every scale is below 2^(1 + k); as a subnormal it may lose 2^-25, 2^-21 where it enters 2^-4
+        lower, and weight scale may lose 2^-25 times a code of 15: a token adds at most 2^(k - 28) of the
+        largest |value|, twice for the normaliser, and 2^(k - 28) itself.  At the end one rounding of the
+        result to its type, eps / 2 of it, or 2^-25 where it is subnormal."""
+        if self.tokens == 0:
+            return np.full(D, 1e-30)
+        k = max(1.0, 2 * self.step)
+        rel = 3 * 2.0 ** -11 + 2 * (16 * 2.0 ** -24 * self.mag + 2.0 ** -21) + 2.0 ** -18
+        tail = self.tokens * k * 2.0 ** -28 * (2 * self.largest + 1)
+        part = 2.0 ** -11 if eps > 2.0 ** -9 else 2.0 ** -21
+        return (1 + eps) * (rel * self.spread + part * self.reach + tail) + eps / 2 * np.abs(self.out) + 2.0 ** -25
 
 
 def to_np(t: torch.Tensor) -> np.ndarray:

@@ -213,9 +213,9 @@ def check_attend(out, q, cache, signs, scale, table, lengths, window=0, sinks=0,
             if prefix is not None:
                 parts.insert(0, ref.gather(pages, prefix[0], h, np.arange(prefix[1])))
             for r in range(G):
-                want, spread, mag, largest, num = ref.attend_head(qn[b, h * G + r], signs, scale, parts)
-                tol = ref.tolerance(want, spread, mag, largest, num, eps)
-                err = np.abs(got[b, h * G + r] - want)
+                row = ref.Row(qn[b, h * G + r], signs, scale, parts)
+                tol = row.tolerance(eps)
+                err = np.abs(got[b, h * G + r] - row.out)
                 assert (err <= tol).all(), f"seq {b} (length {n}) head {h}.{r}: error {err.max():.3e}, " \
                                            f"{(err / tol).max():.2f} of the tolerance"
 
@@ -277,6 +277,26 @@ def test_attend_rising_logits():
         check_attend(out, q, cache, signs, scale, table, [n])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("size", [1e-4, 30.0, 2000.0, 65504.0])
+def test_attend_small_and_large_values(size, dtype):
+    # value scales from subnormal to the largest, growing along the sequence and within one block
+    n, page = 400, 64
+    cache, signs = new_cache(7, 2, page)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = torch.randn((2, n, 2, 128), generator=g, device="cuda")
+    v *= size * torch.linspace(1e-3, 1, n, device="cuda")[:, None, None]
+    v[37, 0, :32] = size * torch.linspace(-1, 1, 32, device="cuda")
+    v.clamp_(-65504, 65504)
+    table = np.arange(7, dtype=np.int32)[None]
+    cache.append(k, v, dev(table), dev([0], torch.int32), dev([0, n], torch.int32))
+    q = torch.randn((1, 8, 128), generator=g, device="cuda").to(dtype)
+    out = cache.attend(q, SCALE, dev(table), dev([n], torch.int32))
+    check_attend(out, q, cache, signs, SCALE, table, [n])
+    out = cache.attend_shared(q, SCALE, dev(table[0, :3]), dev([192], torch.int32), dev(table[:, 3:]), dev([n - 192], torch.int32))
+    check_attend(out, q, cache, signs, SCALE, table, [n])
+
+
 def test_attend_bad_pages_and_lengths():
     # entries outside the cache count as unseen, lengths are limited to the table, both are reported
     lengths = [200, 150]
@@ -290,9 +310,8 @@ def test_attend_bad_pages_and_lengths():
     for b, gone in ((0, 2), (1, 0)):
         t = np.arange(lengths[b])
         t = t[t // 32 != gone]
-        want, spread, mag, largest, num = ref.attend_head(qn[b, 3], signs, SCALE, [ref.gather(pages, table[b], 1, t)])
-        err = np.abs(ref.to_np(out)[b, 3] - want)
-        assert (err <= ref.tolerance(want, spread, mag, largest, num, torch.finfo(q.dtype).eps)).all()
+        row = ref.Row(qn[b, 3], signs, SCALE, [ref.gather(pages, table[b], 1, t)])
+        assert (np.abs(ref.to_np(out)[b, 3] - row.out) <= row.tolerance(torch.finfo(q.dtype).eps)).all()
     cache.status_word.zero_()
     out = cache.attend(q, SCALE, dev(np.full_like(table, -1)), dev(lengths, torch.int32))
     assert (out == 0).all() and cache.status() == kv.STATUS_BAD_INDEX
@@ -347,9 +366,8 @@ def test_attend_shared_bad_prefix():
     t = t[t // 32 != 1]
     for b in range(3):
         parts = [ref.gather(pages, pre, 1, t), ref.gather(pages, table[b], 1, np.arange(lengths[b]))]
-        want, spread, mag, largest, num = ref.attend_head(qn[b, 5], signs, SCALE, parts)
-        err = np.abs(ref.to_np(out)[b, 5] - want)
-        assert (err <= ref.tolerance(want, spread, mag, largest, num, torch.finfo(q.dtype).eps)).all()
+        row = ref.Row(qn[b, 5], signs, SCALE, parts)
+        assert (np.abs(ref.to_np(out)[b, 5] - row.out) <= row.tolerance(torch.finfo(q.dtype).eps)).all()
     cache.status_word.zero_()
     out = cache.attend_shared(q, SCALE, dev(pre), dev([-4], torch.int32), *args)
     assert cache.status() == kv.STATUS_BAD_INDEX

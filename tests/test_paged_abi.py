@@ -158,11 +158,11 @@ def test_reference_block_fields_round_trip():
     assert np.array_equal(got[1], pages[1])
     for h in range(2):
         e = oracle.encode(k[:, h], v[:, h], signs)
-        sign, val, nc = ref.gather(got, [2, 0], h, np.arange(30, 70))
+        sign, val, nc, _, _ = part = ref.gather(got, [2, 0], h, np.arange(30, 70))
         bits = ((e["bits"][:, :, None] >> np.arange(32, dtype=np.uint32)) & 1).reshape(40, 128)
         assert np.array_equal(sign > 0, bits > 0)
         assert np.array_equal(val, oracle.dequant(e["codes"], e["sm"]))
         assert np.array_equal(nc, (e["norm"] * e["cinv"]).astype(np.float64))
         q = rng.standard_normal(128).astype(np.float32)
-        out = ref.attend_head(q, signs, 0.1, [(sign, val, nc)])[0]
+        out = ref.Row(q, signs, 0.1, [part]).out
         assert np.abs(out - oracle.attend(e, q, signs, 0.1)).max() < 1e-5
