@@ -131,10 +131,8 @@ struct QueryPrep {
   int32_t sq;
 };
 
-__device__ __forceinline__ QueryPrep query_prep_warp(const void* q, int64_t row_off, int dtype, const float* signs) {
-  const int lane = threadIdx.x & 31;
-  float x[4];
-  load4(q, row_off + 4 * lane, dtype, x);
+// x: the lane's four channels of the row (overwritten).
+__device__ __forceinline__ QueryPrep query_prep_values(float x[4], const float* signs) {
   rotate_rounds(x, signs);
   float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
   float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
@@ -170,6 +168,12 @@ __device__ __forceinline__ QueryPrep query_prep_warp(const void* q, int64_t row_
   qp.delta = dl;
   qp.sq = __reduce_add_sync(kFull, csum);
   return qp;
+}
+
+__device__ __forceinline__ QueryPrep query_prep_warp(const void* q, int64_t row_off, int dtype, const float* signs) {
+  float x[4];
+  load4(q, row_off + 4 * (threadIdx.x & 31), dtype, x);
+  return query_prep_values(x, signs);
 }
 
 // ---------------------------------------------------------------------------------------------

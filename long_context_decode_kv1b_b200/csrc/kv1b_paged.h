@@ -78,6 +78,8 @@ struct PagedAttendParams {
   float* part;             // [ctas][2][G][2 + 128]
   float* first;            // [ctas][16 warps][G][2 + 128]: ends of segments inside a warp's run
   float* rows;             // null, or [B][Hq][2 + 128]: whole segments leave (m, l, o) here, none is normalised
+  int2* spread;            // [ctas] first output row and pieces of the segment a range boundary cuts, or with
+                           // rows [B][Hkv] first CTA and pieces of each segment; pieces 0: none
   int32_t ncta;
 };
 

@@ -164,7 +164,7 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
 size_t kv1b_paged_attend_workspace_bytes(const kv1b_paged_t* cache, int32_t num_q_heads) {
   if (!paged_ok(cache) || heads_check(cache, num_q_heads) != KV1B_OK) return 0;
   const size_t G = num_q_heads / cache->num_kv_heads;
-  const size_t n = static_cast<size_t>(num_sms()) * (2 + 16) * G * kv1b::kPartStride * 4;  // part, first
+  const size_t n = static_cast<size_t>(num_sms()) * ((2 + 16) * G * kv1b::kPartStride * 4 + 8);  // part, first, spread
   return (n + 255) / 256 * 256;
 }
 
@@ -200,6 +200,8 @@ size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int3
   size_t at = attend_bytes;
   if (p) p->rows = reinterpret_cast<float*>(ws + at);
   at += up256(rows * row);
+  if (p) p->spread = reinterpret_cast<int2*>(ws + at);
+  at += up256(static_cast<size_t>(Hkv) * (s->R / G) * 8);
   s->codes = ws + at;
   at += up256(rows * KV1B_HEAD_DIM);
   s->factors = reinterpret_cast<float2*>(ws + at);
@@ -259,6 +261,7 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   p.ncta = num_sms();
   p.part = static_cast<float*>(ws);
   p.first = p.part + static_cast<size_t>(p.ncta) * 2 * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride;
+  p.spread = reinterpret_cast<int2*>(p.first + static_cast<size_t>(p.ncta) * 16 * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride);
   const int32_t G = num_q_heads / cache->num_kv_heads;
   if (!prefix_pages) return cuda_status(kv1b_launch_paged_attend(p, G, static_cast<cudaStream_t>(stream)));
   kv1b::PagedSharedParams s =

@@ -56,7 +56,8 @@ constexpr int kOffSeg = kOffSome + kMaxSeqs * 2;                 // Seg [kMaxSeg
 constexpr int kOffPlane = kOffSeg + kMaxSegs * 16;               // u32 [kQuerySlots][4 planes][4]
 constexpr int kOffConst = kOffPlane + kQuerySlots * 64;          // f32 [kQuerySlots][4]: c1, c2, c0
 constexpr int kOffRows = kOffConst + kQuerySlots * 16;           // f16 [2][8]: ones, zeros
-constexpr int kSmem = kOffRows + 32;
+constexpr int kOffSigns = kOffRows + 32;                         // f32 [3][128]
+constexpr int kSmem = kOffSigns + 3 * kD * 4;
 constexpr int kOffRed = 0;                                       // f32 [kWarps][G][kRow], over the ring once it is drained
 static_assert(kOffPre % 16 == 0 && kOffRows % 16 == 0 && kWarps * KV1B_MAX_GROUP * kRow * 4 <= kOffPre && kSmem + 2048 <= 227 * 1024, "shared memory");
 
@@ -130,16 +131,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
   }
   pdl_wait();
   pdl_launch_dependents();
+  float* signs = reinterpret_cast<float*>(smem + kOffSigns);
+  if (threadIdx.x < KV1B_MAX_ROUNDS * kD) signs[threadIdx.x] = __ldg(p.c.signs + threadIdx.x);
   const Plan pl = make_plan<kThreads>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), gridDim.x, blockIdx.x == 0);
 
   // sequences that see nothing: zeros
   for (int b = p.rows ? p.B : blockIdx.x; b < p.B; b += gridDim.x)
     if (pre[b + 1] == pre[b])
       for (int e = threadIdx.x; e < p.Hq * kD; e += kThreads) store_out(p.out, p.q_dtype, static_cast<int64_t>(b) * p.Hq * kD + e, 0.0f);
-  if (static_cast<int>(blockIdx.x) >= pl.n || pl.S == 0) return;
+  if (p.rows)
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < static_cast<int64_t>(p.B) * pl.Hkv;
+         i += static_cast<int64_t>(gridDim.x) * kThreads) {
+      const int b = static_cast<int>(i / pl.Hkv);
+      if (pre[b + 1] == pre[b]) p.spread[i] = make_int2(0, 0);
+    }
+  if (static_cast<int>(blockIdx.x) >= pl.n || pl.S == 0) {
+    if (threadIdx.x == 0 && !p.rows) p.spread[blockIdx.x] = make_int2(0, 0);
+    return;
+  }
 
-  const int64_t r0 = pl.begin(blockIdx.x), r1 = pl.begin(blockIdx.x + 1);
-  if (r0 >= r1) return;
+  const int64_t r0 = pl.begin(blockIdx.x), r1 = pl.begin(blockIdx.x + 1);  // never empty: n is at most S
   const uint32_t ring = smem_u32(smem) + warp * kStages * kBlkBytes;
   const int max_segs = min(kMaxSegs, kQuerySlots / G);
   const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
@@ -152,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
   // ---- rounds of up to max_segs segments; nearly always one
   for (int64_t a = r0; a < r1;) {
     // the round's segments
+    int nseg;
     {
       int lo = 0, hi = pl.nsome;  // the sequence of block a: largest lo with Hkv pre[some[lo]] <= a
       while (hi - lo > 1) {
@@ -161,21 +173,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
       }
       const int b0 = pl.some[lo];
       const int h0 = static_cast<int>(quotient(a - static_cast<int64_t>(pre[b0]) * pl.Hkv, pre[b0 + 1] - pre[b0]));
+      bool valid = false;
       if (static_cast<int>(threadIdx.x) < max_segs) {
         const int id = h0 + threadIdx.x, k = lo + id / pl.Hkv, h = id % pl.Hkv;
-        Seg sg = {0x7fffffff, 0, 0, 0};
         if (k < pl.nsome) {
           const int b = pl.some[k], nb = static_cast<int>(pre[b + 1] - pre[b]);
           const int64_t base = static_cast<int64_t>(pre[b]) * pl.Hkv + static_cast<int64_t>(h) * nb;
-          if (base < r1) sg = {static_cast<int>(base - a), nb, b, h};
+          valid = base < r1;
+          if (valid) seg[threadIdx.x] = {static_cast<int>(base - a), nb, b, h};
         }
-        seg[threadIdx.x] = sg;
       }
+      nseg = __syncthreads_count(valid);
     }
-    __syncthreads();
-    int nseg = max_segs, n;  // segments and blocks of the round
-    while (seg[nseg - 1].nb == 0) --nseg;
-    n = static_cast<int>(min(r1 - a, static_cast<int64_t>(seg[nseg - 1].base) + seg[nseg - 1].nb));
+    const int n = static_cast<int>(min(r1 - a, static_cast<int64_t>(seg[nseg - 1].base) + seg[nseg - 1].nb));
     const int run_q = n / kWarps, run_r = n % kWarps;  // the first run_r runs are one longer
     auto run_begin = [&](int w) { return w * run_q + min(w, run_r); };
     auto run_owner = [&](int x) {
@@ -183,6 +193,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
       return x < longer ? x / (run_q + 1) : run_r + (x - longer) / run_q;
     };
     const int w0 = run_begin(warp), w1 = run_begin(warp + 1);
+
+    // the rows of the round's queries: a warp's first two are loaded before the copies fill the memory's queues
+    auto load_row = [&](int r, float (&x)[4]) {
+      const Seg sg = seg[r / G];
+      load4(p.q, (static_cast<int64_t>(sg.b) * p.Hq + static_cast<int64_t>(sg.h) * G + r % G) * kD + 4 * lane, p.q_dtype, x);
+    };
+    float q0[4], q1[4];
+    if (warp < nseg * G) load_row(warp, q0);
+    if (warp + kWarps < nseg * G) load_row(warp + kWarps, q1);
 
     // ---- copy side: `ahead` walks kStages blocks in front of the compute
     Ahead ahead;
@@ -214,9 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
 
     // ---- the round's queries
     for (int r = warp; r < nseg * G; r += kWarps) {
-      const Seg sg = seg[r / G];
-      const QueryPrep qp = query_prep_warp(p.q, (static_cast<int64_t>(sg.b) * p.Hq + static_cast<int64_t>(sg.h) * G + r % G) * kD,
-                                           p.q_dtype, p.c.signs);
+      if (r >= 2 * kWarps) load_row(r, q0);
+      const QueryPrep qp = query_prep_values(q0, signs);
+      #pragma unroll
+      for (int j = 0; j < 4; ++j) q0[j] = q1[j];
       if (lane == 0) {
         #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -491,38 +511,59 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
     __syncthreads();  // the ring is drained, the pieces in `first` are written
     if (last) put_piece(red + warp * G * kRow);
     __syncthreads();
-    for (int x = 0; x < nseg; ++x) {
+    // for the merge: pieces of the segment that goes on past the range, or of every segment (rows)
+    for (int x = threadIdx.x; x < nseg; x += kThreads) {
+      const Seg sg = seg[x];
+      const bool starts = sg.base >= 0, ends = sg.base + sg.nb <= n;
+      const int pieces = ends ? 1 : pl.owner(a + sg.base + sg.nb - 1) - blockIdx.x + 1;
+      if (p.rows) {
+        if (starts) p.spread[static_cast<int64_t>(sg.b) * pl.Hkv + sg.h] = make_int2(blockIdx.x, pieces);
+      } else if (x == nseg - 1 && a + n == r1) {
+        p.spread[blockIdx.x] = make_int2(sg.b * p.Hq + sg.h * G, starts && !ends ? pieces : 0);
+      }
+    }
+    for (int r = warp; r < nseg * G; r += kWarps) {  // a row (segment, head) per warp, four channels per lane
+      const int x = r / G, hd = r - x * G;
       const Seg sg = seg[x];
       const int s = max(sg.base, 0), e = min(sg.base + sg.nb, n);
       const int wf = run_owner(s), wl = run_owner(e - 1);
       const bool starts = sg.base >= 0, ends = sg.base + sg.nb <= n;
       if (wf == wl && starts && ends) continue;  // finished by its warp
-      const float* tail = e < run_begin(wl + 1) ? p.first + (static_cast<int64_t>(blockIdx.x) * kWarps + wl) * G * kRow : red + wl * G * kRow;
-      const int64_t qrow = static_cast<int64_t>(sg.b) * p.Hq + static_cast<int64_t>(sg.h) * G;
-      for (int i = threadIdx.x; i < G * kD; i += kThreads) {
-        const int hd = i / kD, ch = i - hd * kD;
-        auto piece = [&](int w) { return (w == wl ? tail : red + w * G * kRow) + hd * kRow; };
-        float M = kNoRef;
-        for (int w = wf; w <= wl; ++w) M = fmaxf(M, piece(w)[0]);
-        float num = 0.0f, den = 0.0f;
-        #pragma unroll 4
-        for (int w = wf; w <= wl; ++w) {
-          const float* r = piece(w);
-          const float f = ex2(r[0] - M);
-          num = __fmaf_rn(f, r[2 + ch], num);
-          den = __fmaf_rn(f, r[1], den);
-        }
-        if (starts && ends && !p.rows) {
-          store_out(p.out, p.q_dtype, (qrow + hd) * kD + ch, den != 0.0f ? __fdiv_rn(num, den) : 0.0f);
-        } else {
-          float* row = starts && ends ? p.rows + (qrow + hd) * kRow
-                                      : p.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * G + hd) * kRow;
-          if (ch == 0) {
-            row[0] = M;
-            row[1] = den;
-          }
-          row[2 + ch] = num;
-        }
+      const bool inside = e < run_begin(wl + 1);  // the last piece is in `first`
+      const float* tail = p.first + ((static_cast<int64_t>(blockIdx.x) * kWarps + wl) * G + hd) * kRow;
+      float2 head = make_float2(kNoRef, 0.0f);  // lane w: piece w's m and l
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (lane >= wf && lane <= wl) head = *reinterpret_cast<const float2*>(red + (lane * G + hd) * kRow);
+      if (inside) {
+        if (lane == wl) head = *reinterpret_cast<const float2*>(tail);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = tail[2 + lane + 32 * i];
+      }
+      float M = head.x;
+      #pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+      M = __shfl_sync(kFull, M, 0);  // lanes 0 .. 15 hold the pieces
+      const float f = ex2(head.x - M);
+      float num[4] = {0.0f, 0.0f, 0.0f, 0.0f}, den = 0.0f;
+      #pragma unroll 4
+      for (int w = wf; w <= wl; ++w) {
+        const float fw = __shfl_sync(kFull, f, w), lw = __shfl_sync(kFull, head.y, w);
+        const float* o = red + (w * G + hd) * kRow + 2 + lane;
+        const bool in_first = inside && w == wl;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) num[i] = __fmaf_rn(fw, in_first ? v[i] : o[32 * i], num[i]);
+        den = __fmaf_rn(fw, lw, den);
+      }
+      const int64_t qrow = static_cast<int64_t>(sg.b) * p.Hq + static_cast<int64_t>(sg.h) * G + hd;
+      if (starts && ends && !p.rows) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) store_out(p.out, p.q_dtype, qrow * kD + lane + 32 * i, den != 0.0f ? __fdiv_rn(num[i], den) : 0.0f);
+      } else {
+        float* row = starts && ends ? p.rows + qrow * kRow
+                                    : p.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * G + hd) * kRow;
+        if (lane == 0) *reinterpret_cast<float2*>(row) = make_float2(M, den);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) row[2 + lane + 32 * i] = num[i];
       }
     }
     a += n;
@@ -537,38 +578,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAt
 // Segments cut by a range boundary: block (c, head) merges the one that starts in CTA c's range and goes
 // on past it -- slot 1 of c, then slot 0 of the CTAs after it.
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedAttendParams p, const int G) {
-  __shared__ uint32_t pre[kMaxSeqs + 1];
-  __shared__ int slen[kMaxSeqs];
+  __shared__ float2 s_head[kMaxPieces];
+  __shared__ float s_max[4];
   pdl_wait();
-  const Plan pl = make_plan<128>(p, pre, slen, nullptr, p.ncta, false);
   const int c = blockIdx.x, hd = blockIdx.y;
-  if (c + 1 >= pl.n || pl.S == 0) return;
-  const int64_t r0 = pl.begin(c), r1 = pl.begin(c + 1);
-  if (r0 >= r1) return;
-  int b, h;
-  int64_t base;
-  pl.locate(r1 - 1, &b, &h, &base);
-  const int64_t end = base + (pre[b + 1] - pre[b]);
-  if (base < r0 || end <= r1) return;
-  int last = c + 1;
-  while (last + 1 < pl.n && pl.begin(last + 1) < end) ++last;
-  const int n = last - c + 1;  // pieces
-  const int64_t step = 2LL * G * kRow;
+  const int2 cut = p.spread[c];
+  if (cut.y == 0) return;
   const float* first = p.part + ((static_cast<int64_t>(c) * 2 + 1) * G + hd) * kRow;
   const float* rest = p.part + ((static_cast<int64_t>(c) * 2) * G + hd) * kRow;
-  auto piece = [&](int i) { return i == 0 ? first : rest + i * step; };
-  float M = kNoRef;
-  for (int i = 0; i < n; ++i) M = fmaxf(M, piece(i)[0]);
-  float num = 0.0f, den = 0.0f;
-  #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* r = piece(i);
-    const float f = ex2(r[0] - M);
-    num = __fmaf_rn(f, r[2 + threadIdx.x], num);
-    den = __fmaf_rn(f, r[1], den);
-  }
-  const int64_t row = static_cast<int64_t>(b) * p.Hq + static_cast<int64_t>(h) * G + hd;
-  store_out(p.out, p.q_dtype, row * kD + threadIdx.x, den != 0.0f ? __fdiv_rn(num, den) : 0.0f);
+  const int64_t step = 2LL * G * kRow;
+  merge_pieces(cut.y, [&](int i) { return i == 0 ? first : rest + i * step; }, s_head, s_max, p.out, p.q_dtype,
+               (static_cast<int64_t>(cut.x) + hd) * kD);
 }
 
 }  // namespace paged

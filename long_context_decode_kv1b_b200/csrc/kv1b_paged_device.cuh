@@ -227,5 +227,33 @@ __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* 
   return pl;
 }
 
+constexpr int kMaxPieces = 512;  // a row's pieces: CTAs of the split, and 148 token ranges of two lanes
+
+// Log-sum-exp merge of n <= kMaxPieces partial rows by a block of 128 threads, a channel each.
+template <typename Piece>
+__device__ __forceinline__ void merge_pieces(int n, Piece piece, float2* s_head, float* s_max, void* out, int dtype, int64_t at) {
+  float M = kNoRef;
+  for (int i = threadIdx.x; i < n; i += 128) {
+    const float2 h = *reinterpret_cast<const float2*>(piece(i));
+    s_head[i] = h;
+    M = fmaxf(M, h.x);
+  }
+  #pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  float num = 0.0f, den = 0.0f;
+  #pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const float o = piece(i)[2 + threadIdx.x];
+    const float2 h = s_head[i];
+    const float f = ex2(h.x - M);
+    num = __fmaf_rn(f, o, num);
+    den = __fmaf_rn(f, h.y, den);
+  }
+  store_out(out, dtype, at + threadIdx.x, den != 0.0f ? __fdiv_rn(num, den) : 0.0f);
+}
+
 }  // namespace paged
 }  // namespace kv1b

@@ -192,8 +192,14 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
   const int n = prefix_tokens(p, u == 0 && threadIdx.x == 0);
   const int64_t nt = (n + kTile - 1) / kTile;
   const int t0 = static_cast<int>(nt * split / s.splits), tiles = static_cast<int>(nt * (split + 1) / s.splits) - t0;
-  if (tiles == 0) return;  // the whole CTA; the merge counts no piece here
   const bool two = s.two != 0;
+  if (nt > 0 && (tiles == 0 || (!two && tiles == 1))) {  // empty pieces of the lanes without a tile
+    for (int e = threadIdx.x; e < 256 * kRow; e += kShThreads) {
+      const int w = e / (128 * kRow), ch = e % kRow;
+      if (tiles == 0 || w == 1) s.pieces[static_cast<int64_t>(u) * 256 * kRow + e] = ch == 0 ? kNoRef : 0.0f;
+    }
+  }
+  if (tiles == 0) return;  // the whole CTA
   const int jobs = two ? 2 * tiles : tiles;  // job j: lane j & 1, tile j / 2 or j
 
   if (warp == 0) tmem_alloc(&s_tmem);
@@ -482,59 +488,29 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
   if (warp == 0) tmem_free(tmem);
 }
 
-// One (sequence, kv-head, query head) per block: the prefix's pieces and the sequence's own.
+// One (sequence, kv-head, query head) per block: the sequence's own pieces and the prefix's.
 __global__ void __launch_bounds__(128) paged_shared_merge_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G) {
-  __shared__ uint32_t pre[kMaxSeqs + 1];
-  __shared__ int slen[kMaxSeqs];
+  __shared__ float2 s_head[kMaxPieces];
+  __shared__ float s_max[4];
   pdl_wait();
-  const Plan pl = make_plan<128>(p, pre, slen, nullptr, p.ncta, false);
   const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x - b * p.c.Hkv, g = blockIdx.y;
   const int64_t out_row = static_cast<int64_t>(b) * p.Hq + static_cast<int64_t>(h) * G + g;
-  // own tokens: one row, or the pieces of CTAs c0 .. c1
-  const float* own = nullptr;
-  int own_n = 0;
-  int64_t own_step = 0;
-  const float* own_first = nullptr;
-  if (pre[b + 1] > pre[b]) {
-    const int64_t nb = pre[b + 1] - pre[b], base = static_cast<int64_t>(pre[b]) * pl.Hkv + h * nb, end = base + nb;
-    const int c0 = pl.owner(base), c1 = pl.owner(end - 1);
-    if (c0 == c1) {
-      own_first = p.rows + out_row * kRow;
-      own_n = 1;
-    } else {
-      own_first = p.part + ((static_cast<int64_t>(c0) * 2 + 1) * G + g) * kRow;
-      own = p.part + ((static_cast<int64_t>(c0) * 2) * G + g) * kRow;
-      own_step = 2LL * G * kRow;
-      own_n = c1 - c0 + 1;
-    }
-  }
+  const int2 own = p.spread[blockIdx.x];  // first CTA, pieces
+  const float* own0 = own.y == 1 ? p.rows + out_row * kRow : p.part + ((static_cast<int64_t>(own.x) * 2 + 1) * G + g) * kRow;
+  const float* own1 = p.part + ((static_cast<int64_t>(own.x) * 2) * G + g) * kRow;
+  const int64_t step = 2LL * G * kRow;
   const int r = b * G + g, rows = s.two ? 256 : 128, rt = r / rows, in = r - rt * rows;
-  const int64_t nt = (prefix_tokens(p, false) + kTile - 1) / kTile;
-  const int per = s.two ? 1 : 2;  // pieces of a split
-  const int n = own_n + s.splits * per;
+  // the token ranges with tiles are the same number of pieces each: all of them, or as many as there are
+  // tiles; where two lanes share a range's tiles, one tile is the first lane's
+  const int nt = (prefix_tokens(p, false) + kTile - 1) / kTile;
+  const float* base = s.pieces + ((static_cast<int64_t>(h) * s.row_tiles + rt) * s.splits * 256 + in) * kRow;
+  const int per = s.two ? 1 : 2;
   auto piece = [&](int i) -> const float* {
-    if (i < own_n) return i == 0 ? own_first : own + i * own_step;
-    const int k = i - own_n, sp = k / per, w = s.two ? in >> 7 : k & 1;
-    const int64_t tiles = nt * (sp + 1) / s.splits - nt * sp / s.splits;
-    if (tiles <= (s.two ? 0 : w)) return nullptr;
-    const int64_t u = (static_cast<int64_t>(h) * s.row_tiles + rt) * s.splits + sp;
-    return s.pieces + ((u * 2 + w) * 128 + (in & 127)) * kRow;
+    if (i < own.y) return i == 0 ? own0 : own1 + i * step;
+    i -= own.y;
+    return base + (per == 1 ? static_cast<int64_t>(i) * 256 : static_cast<int64_t>(i >> 1) * 256 + (i & 1) * 128) * kRow;
   };
-  float M = kNoRef;
-  for (int i = 0; i < n; ++i) {
-    const float* r0 = piece(i);
-    if (r0) M = fmaxf(M, r0[0]);
-  }
-  float num = 0.0f, den = 0.0f;
-  #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* r0 = piece(i);
-    if (!r0) continue;
-    const float f = ex2(r0[0] - M);
-    num = __fmaf_rn(f, r0[2 + threadIdx.x], num);
-    den = __fmaf_rn(f, r0[1], den);
-  }
-  store_out(p.out, p.q_dtype, out_row * kD + threadIdx.x, den != 0.0f ? __fdiv_rn(num, den) : 0.0f);
+  merge_pieces(own.y + (nt > 0 ? s.splits * per : 0), piece, s_head, s_max, p.out, p.q_dtype, out_row * kD);
 }
 
 }  // namespace paged
