@@ -10,7 +10,11 @@ import ctypes
 
 import torch
 
-from . import HEAD_DIM, Kv1bError, _check, _dtype_code, lib
+from . import DTYPE_BF16, DTYPE_F16, DTYPE_F32, HEAD_DIM, Kv1bError, _check, lib
+
+# the current stream's handle without a Stream object around it (microseconds a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 BLOCK_TOKENS = 32
 BLOCK_BYTES = 3200
@@ -31,9 +35,12 @@ class RopeDesc(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
-def _int32(t: torch.Tensor, dims: int, device, name: str):
-    if t.dtype != torch.int32 or t.dim() != dims or t.device != device or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be an int32 tensor of {dims} dimension(s) on {device}, unit stride in the last")
+_DTYPE_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _int32(t: torch.Tensor, dims: int, index: int, name: str):
+    if t.dtype is not torch.int32 or t.dim() != dims or t.get_device() != index or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be an int32 tensor of {dims} dimension(s) on cuda:{index}, unit stride in the last")
 
 
 class Rope:
@@ -49,7 +56,7 @@ class Rope:
             raise ValueError("rot_dim must be a multiple of 8 between 8 and 128")
         if not 1 <= len(sections) <= ROPE_MAX_AXES or min(sections) < 0 or sum(sections) != rot // 2:
             raise ValueError("sections: one to three pair counts that add up to rot_dim / 2")
-        self.cos_sin, self.axes = cos_sin, len(sections)
+        self.cos_sin, self.axes, self.index = cos_sin, len(sections), cos_sin.get_device()
         self.desc = RopeDesc(cos_sin.data_ptr(), cos_sin.shape[0], rot, len(sections), int(interleaved),
                              (ctypes.c_int32 * ROPE_MAX_AXES)(*sections), 0)
         self._ref = ctypes.addressof(self.desc)
@@ -101,19 +108,26 @@ class PagedCache:
         self.num_pages, self.num_kv_heads = pages.shape[0], pages.shape[1]
         self.page_tokens = pages.shape[2] * BLOCK_TOKENS
         self.device = pages.device
+        self._index = pages.get_device()
+        self._lib = lib()
         self.desc = PagedDesc(pages.data_ptr(), signs.data_ptr(), status.data_ptr(), self.num_pages, self.num_kv_heads,
                               self.page_tokens, 0)
         self._ref = ctypes.addressof(self.desc)
         self._ws_bytes = {}
 
-    def _launch_stream(self, stream):
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if s.device != self.device:
-            raise ValueError(f"the stream is on {s.device}, the cache on {self.device}")
-        return s
+    def _on(self, stream):
+        """Context of a call's allocations and launches: the cache's device, and `stream` if one is given."""
+        if stream is None:
+            return torch.cuda.device(self._index)
+        if stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
+        return torch.cuda.stream(stream)  # its device too
+
+    def _away(self, stream) -> bool:
+        return stream is not None or torch.cuda.current_device() != self._index
 
     def _on_device(self, t: torch.Tensor, name: str):
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
 
     def append(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, cu_new: torch.Tensor,
@@ -126,99 +140,107 @@ class PagedCache:
         [seqs] how many tokens each sequence holds (not advanced here), page_table int32 [seqs, pages].
         positions: int32 [tokens], or [axes, tokens].  q [tokens, q heads, 128]: turned alike into q_out
         (a new contiguous tensor by default; q itself allowed), which is returned."""
-        dev = self.device
-        if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.shape[1:] != (self.num_kv_heads, HEAD_DIM) \
-                or k.stride(2) != 1 or v.stride(2) != 1:
-            raise ValueError("k and v must be [tokens, num_kv_heads, 128] of one type with unit channel stride")
+        if self._away(stream):
+            with self._on(stream):
+                return self.append(k, v, page_table, start, cu_new, rope, positions, q, q_out)
+        index = self._index
+        T, H, D = shape = k.shape
+        dtype = _DTYPE_CODES.get(k.dtype)
+        (kt, kh, kc), (vt, vh, vc) = k.stride(), v.stride()
+        if H != self.num_kv_heads or D != HEAD_DIM or v.shape != shape or k.dtype is not v.dtype or kc != 1 or vc != 1 \
+                or dtype is None:
+            raise ValueError("k and v must be [tokens, num_kv_heads, 128] of one floating type with unit channel stride")
         self._on_device(k, "k")
         self._on_device(v, "v")
-        T = k.shape[0]
-        _int32(page_table, 2, dev, "page_table")
-        _int32(start, 1, dev, "start")
-        _int32(cu_new, 1, dev, "cu_new")
-        B = page_table.shape[0]
+        _int32(page_table, 2, index, "page_table")
+        _int32(start, 1, index, "start")
+        _int32(cu_new, 1, index, "cu_new")
+        B, pages = page_table.shape
         if start.shape[0] != B or cu_new.shape[0] != B + 1:
             raise ValueError("page_table [seqs, pages], start [seqs] and cu_new [seqs + 1] disagree")
-        ps, pos = 0, None
+        ps, pos, ro = 0, None, None
         if rope is not None:
             if positions is None:
                 raise ValueError("rope needs positions")
-            _int32(positions, positions.dim(), dev, "positions")
-            if positions.shape != ((rope.axes, T) if positions.dim() == 2 else (T,)) or (positions.dim() == 1 and rope.axes > 1):
+            dims = positions.dim()
+            _int32(positions, dims, index, "positions")
+            if positions.shape != ((rope.axes, T) if dims == 2 else (T,)) or (dims == 1 and rope.axes > 1):
                 raise ValueError("positions must be [tokens] or [axes, tokens]")
-            self._on_device(rope.cos_sin, "cos_sin")
-            ps, pos = (positions.stride(0) if rope.axes > 1 else 0), positions.data_ptr()
+            if rope.index != index:
+                raise ValueError(f"cos_sin is on cuda:{rope.index}, the cache on {self.device}")
+            ps, pos, ro = (positions.stride(0) if rope.axes > 1 else 0), positions.data_ptr(), rope._ref
         elif positions is not None:
             raise ValueError("positions need rope")
-        s = self._launch_stream(stream)
         qp = qo = None
         hq = qs0 = qs1 = os0 = os1 = 0
         if q is not None:
-            if q.dim() != 3 or q.shape[0] != T or q.shape[2] != HEAD_DIM or q.dtype != k.dtype or q.stride(2) != 1:
+            tq, hq, dq = q.shape
+            qs0, qs1, qc = q.stride()
+            if tq != T or dq != HEAD_DIM or q.dtype is not k.dtype or qc != 1:
                 raise ValueError("q must be [tokens, q heads, 128] of k's type with unit channel stride")
             self._on_device(q, "q")
             if q_out is None:
-                with torch.cuda.stream(s):
-                    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.stride(2) != 1 or q_out.device != dev:
+                q_out = torch.empty((T, hq, HEAD_DIM), dtype=q.dtype, device=self.device)
+            elif q_out.shape != q.shape or q_out.dtype is not q.dtype or q_out.stride(2) != 1 or q_out.get_device() != index:
                 raise ValueError("q_out must have q's shape, type and device, unit channel stride")
-            hq, qp, qo = q.shape[1], q.data_ptr(), q_out.data_ptr()
-            qs0, qs1, os0, os1 = q.stride(0), q.stride(1), q_out.stride(0), q_out.stride(1)
+            qp, qo = q.data_ptr(), q_out.data_ptr()
+            os0, os1, _ = q_out.stride()
         elif q_out is not None:
             raise ValueError("q_out needs q")
         if T == 0:
             return q_out
-        with torch.cuda.device(dev):
-            _check(lib().kv1b_paged_append(self._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), T, k.stride(0), k.stride(1),
-                                           v.stride(0), v.stride(1), B, cu_new.data_ptr(), start.data_ptr(),
-                                           page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-                                           rope._ref if rope is not None else None, pos, ps, qp, qo, hq, qs0, qs1, os0, os1,
-                                           s.cuda_stream), "kv1b_paged_append")
+        code = self._lib.kv1b_paged_append(self._ref, k.data_ptr(), v.data_ptr(), dtype, T, kt, kh, vt, vh, B,
+                                           cu_new.data_ptr(), start.data_ptr(), page_table.data_ptr(), page_table.stride(0),
+                                           pages, ro, pos, ps, qp, qo, hq, qs0, qs1, os0, os1, _raw_stream(index))
+        if code:
+            _check(code, "kv1b_paged_append")
         return q_out
 
-    def _attend_args(self, q, page_table, lengths, out, s):
-        if q.dim() != 3 or q.shape[2] != HEAD_DIM or not q.is_contiguous():
-            raise ValueError("q must be a contiguous tensor [seqs, q heads, 128]")
+    def _attend_args(self, q, page_table, lengths, out):
+        B, Hq, D = shape = q.shape
+        dtype = _DTYPE_CODES.get(q.dtype)
+        if D != HEAD_DIM or not q.is_contiguous() or dtype is None:
+            raise ValueError("q must be a contiguous floating tensor [seqs, q heads, 128]")
         self._on_device(q, "q")
-        _int32(page_table, 2, self.device, "page_table")
-        _int32(lengths, 1, self.device, "lengths")
-        if page_table.shape[0] != q.shape[0] or lengths.shape[0] != q.shape[0]:
+        _int32(page_table, 2, self._index, "page_table")
+        _int32(lengths, 1, self._index, "lengths")
+        rows, pages = page_table.shape
+        if rows != B or lengths.shape[0] != B:
             raise ValueError("q, page_table and lengths disagree on the number of sequences")
         if out is None:
-            with torch.cuda.stream(s):
-                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != self.device:
+            out = torch.empty(shape, dtype=q.dtype, device=self.device)
+        elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous() or out.get_device() != self._index:
             raise ValueError("out must be a contiguous tensor of q's shape and type")
-        return out
+        return out, B, Hq, dtype, pages
 
-    def _workspace(self, key, s):
+    def _workspace(self, key):
         """A workspace of this call's own, from the stream's memory (a capture's from its graph's)."""
         n = self._ws_bytes.get(key)
         if n is None:
-            with torch.cuda.device(self.device):
-                n = lib().kv1b_paged_attend_workspace_bytes(self._ref, key[1]) if key[0] == 0 else \
-                    lib().kv1b_paged_shared_workspace_bytes(self._ref, *key)
+            n = self._lib.kv1b_paged_attend_workspace_bytes(self._ref, key[1]) if key[0] == 0 else \
+                self._lib.kv1b_paged_shared_workspace_bytes(self._ref, *key)
             if n == 0:
                 raise Kv1bError(-1, "kv1b_paged_attend_workspace_bytes")
             self._ws_bytes[key] = n
-        with torch.cuda.stream(s):
-            return torch.empty(n, dtype=torch.uint8, device=self.device)
+        return torch.empty(n, dtype=torch.uint8, device=self.device), n
 
     def attend(self, q: torch.Tensor, scale: float, page_table: torch.Tensor, lengths: torch.Tensor, window: int = 0,
                sinks: int = 0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Decode attention of q [seqs, q heads, 128] (bf16 / fp16) over each sequence's first lengths[b]
         tokens (int32, on the device); with window > 0 over the last `window` and the first `sinks` of them.
         Returns q's shape and type."""
-        s = self._launch_stream(stream)
-        out = self._attend_args(q, page_table, lengths, out, s)
-        if q.shape[0] == 0:
+        if self._away(stream):
+            with self._on(stream):
+                return self.attend(q, scale, page_table, lengths, window, sinks, out)
+        out, B, Hq, dtype, pages = self._attend_args(q, page_table, lengths, out)
+        if B == 0:
             return out
-        ws = self._workspace((0, q.shape[1]), s)
-        with torch.cuda.device(self.device):
-            _check(lib().kv1b_paged_attend(self._ref, q.data_ptr(), _dtype_code(q), q.shape[1], scale, q.shape[0],
-                                           page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-                                           lengths.data_ptr(), window, sinks, out.data_ptr(), ws.data_ptr(), ws.numel(),
-                                           s.cuda_stream), "kv1b_paged_attend")
+        ws, n = self._workspace((0, Hq))
+        code = self._lib.kv1b_paged_attend(self._ref, q.data_ptr(), dtype, Hq, scale, B, page_table.data_ptr(),
+                                           page_table.stride(0), pages, lengths.data_ptr(), window, sinks, out.data_ptr(),
+                                           ws.data_ptr(), n, _raw_stream(self._index))
+        if code:
+            _check(code, "kv1b_paged_attend")
         return out
 
     def attend_shared(self, q: torch.Tensor, scale: float, prefix_pages: torch.Tensor, prefix_length: torch.Tensor,
@@ -226,25 +248,27 @@ class PagedCache:
                       stream=None) -> torch.Tensor:
         """Decode attention for sequences that all begin with the prefix_length[0] tokens (int32 [1], on the
         device) of prefix_pages (int32 [pages]) and go on with lengths[b] tokens of their own."""
-        s = self._launch_stream(stream)
-        out = self._attend_args(q, page_table, lengths, out, s)
-        _int32(prefix_pages, 1, self.device, "prefix_pages")
-        _int32(prefix_length, 1, self.device, "prefix_length")
-        if prefix_length.shape[0] != 1 or prefix_pages.shape[0] < 1:
+        if self._away(stream):
+            with self._on(stream):
+                return self.attend_shared(q, scale, prefix_pages, prefix_length, page_table, lengths, out)
+        out, B, Hq, dtype, pages = self._attend_args(q, page_table, lengths, out)
+        _int32(prefix_pages, 1, self._index, "prefix_pages")
+        _int32(prefix_length, 1, self._index, "prefix_length")
+        npre = prefix_pages.shape[0]
+        if prefix_length.shape[0] != 1 or npre < 1:
             raise ValueError("prefix_length must hold one number and prefix_pages one page at least")
-        if q.shape[0] == 0:
+        if B == 0:
             return out
-        ws = self._workspace((q.shape[0], q.shape[1], prefix_pages.shape[0]), s)
-        with torch.cuda.device(self.device):
-            _check(lib().kv1b_paged_attend_shared(self._ref, q.data_ptr(), _dtype_code(q), q.shape[1], scale, q.shape[0],
-                                                  prefix_pages.data_ptr(), prefix_pages.shape[0], prefix_length.data_ptr(),
-                                                  page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-                                                  lengths.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
-                                                  s.cuda_stream), "kv1b_paged_attend_shared")
+        ws, n = self._workspace((B, Hq, npre))
+        code = self._lib.kv1b_paged_attend_shared(self._ref, q.data_ptr(), dtype, Hq, scale, B, prefix_pages.data_ptr(), npre,
+                                                  prefix_length.data_ptr(), page_table.data_ptr(), page_table.stride(0), pages,
+                                                  lengths.data_ptr(), out.data_ptr(), ws.data_ptr(), n,
+                                                  _raw_stream(self._index))
+        if code:
+            _check(code, "kv1b_paged_attend_shared")
         return out
 
     def status(self, stream=None) -> int:
         """The KV1B_STATUS_* bits since the cache was made (waits for the stream)."""
-        s = self._launch_stream(stream)
-        with torch.cuda.stream(s):
+        with self._on(stream):
             return int(self.status_word.item())
