@@ -3,17 +3,21 @@
 //
 // For kv-head h the batch's queries are R = sequences x G rows.  A CTA takes up to 256 rows (two lanes
 // of 128) and a range of 128-token tiles; the ranges' partial rows (m, l, o) are merged afterwards with
-// the sequences' own tokens.  With at most 128 rows both lanes hold the same rows and take the tiles in
-// turn, so one lane's softmax still runs while the other's products do.
+// the sequences' own tokens.  With at most 128 rows both lanes hold the same rows, one takes the first
+// half of each tile and one the second.
 //
-// Per tile and lane, S = Q K^T (f8, exact: codes 0 .. 15 times signs +-1, sums below 2^11) into tensor
-// memory; each softmax thread owns one row, x = nc (delta I2 + vl I1) with I2 = S and I1 the token's sum
-// of signs, and leaves 2^(x - m + kBase) as binary16 over S; O += P V (f16, fp32 sums in tensor memory).
-// S and P share columns: 2 lanes x (128 + 128) columns are all 512.
+// A job is 64 tokens of a tile on a lane: S = Q K^T (f8, exact: codes 0 .. 15 times signs +-1, sums below
+// 2^11) into tensor memory; each softmax thread owns one row, x = nc (delta I2 + vl I1) with I2 = S and I1
+// the token's sum of signs, and leaves 2^(x - m + kBase) as binary16; O += P V (f16, fp32 sums in tensor
+// memory).  A softmax thread takes its 64 sums into registers at once and gives S back, so the next job's
+// scores are made while it works, and P has two places, so it never waits for the products: per lane 64
+// columns of S, 2 x 32 of P and 128 of O, for two lanes all 512.  (One S of 128 columns with P written
+// over it, so that each job went round softmax, P V and Q K: 201 us instead of @NEW@ us at 256 rows x
+// 131,072 tokens x 8 kv-heads.)
 //
-// Warps: 0 - 3 and 4 - 7 the lanes' softmax, 8 - 11 the expansion (signs to f8, codes to f16 values, one
-// rounding), 12 issues the products, 13 the copies.  Each wait is bounded; one that runs out ends the CTA
-// with KV1B_STATUS_TIMEOUT.
+// Warps: 0 - 3 and 4 - 7 the lanes' softmax, 8 - 11 the values' expansion (codes to f16, one rounding), 12
+// issues the products, 13 the copies, 14 and 15 the signs' expansion to f8.  Each wait is bounded; one that
+// runs out ends the CTA with KV1B_STATUS_TIMEOUT.
 //
 // A tile of 128 tokens x 256 rows costs 512 + 1,024 clocks of products and 32,768 exponentials, 2,048
 // clocks at 16 a clock: the exponentials bound it.
@@ -24,9 +28,11 @@ namespace paged {
 
 constexpr int kTile = 128;                 // tokens
 constexpr int kTileBlocks = kTile / kBlkTok;
-constexpr int kSoftWarps = 8, kExpandWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kExpandWarps, kCopyWarp = kMmaWarp + 1;
-constexpr int kShThreads = 512;            // four warpgroups; the last has two idle warps
+constexpr int kSoftWarps = 8, kValueWarps = 4, kSignWarps = 2;
+constexpr int kMmaWarp = kSoftWarps + kValueWarps, kCopyWarp = kMmaWarp + 1, kSignWarp = kCopyWarp + 1;
+constexpr int kHalf = 64;                  // tokens of a job
+constexpr float kMostSum = 32768.0f;       // 2^(kBase + kTau): a sum up to it holds no larger weight
+constexpr int kShThreads = 512;            // four warpgroups
 // 512 x 128 registers at launch; the softmax groups take what the others give back: 2 (168 + 88) = 4 x 128
 constexpr int kSoftRegs = 168, kOtherRegs = 88;
 constexpr int kRaw = 3;                    // tiles of packed blocks in flight
@@ -61,20 +67,29 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// One lane of a converged warp.  (The compiler then knows that the branch has one thread and keeps the
+// products' descriptors in uniform registers.)
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one != 0;
+}
 // K-major operand in 128-byte swizzled rows (8-row groups of 1,024 bytes)
 __device__ __forceinline__ uint64_t operand(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) |
          (2ull << 61);
 }
-constexpr uint32_t kShapeM128N128 = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);  // fp32 sums; e4m3 / f16 operands: type 0
+// M 128, fp32 sums; operand types 0 (e4m3, f16)
+constexpr uint32_t kScoreShape = (1u << 4) | ((kHalf / 8) << 17) | ((128u / 16) << 24);
+constexpr uint32_t kValueShape = (1u << 4) | ((kD / 8) << 17) | ((128u / 16) << 24);
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, bool add) {
   asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
-               "l"(b), "r"(kShapeM128N128), "r"(static_cast<uint32_t>(add))
+               "l"(b), "r"(kScoreShape), "r"(static_cast<uint32_t>(add))
                : "memory");
 }
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, bool add) {
   asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
-               "l"(b), "r"(kShapeM128N128), "r"(static_cast<uint32_t>(add))
+               "l"(b), "r"(kValueShape), "r"(static_cast<uint32_t>(add))
                : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
@@ -82,6 +97,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
@@ -92,10 +117,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 // the registers of a load are valid from here on: the dependency keeps their uses behind the wait
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  #pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -168,18 +195,58 @@ __device__ __forceinline__ int prefix_tokens(const PagedAttendParams& p, bool re
   return n < 0 ? 0 : static_cast<int>(n > top ? top : n);
 }
 
+// Exponents of four of a row's weights: logit - m + kBase, -infinity where MASKED and not seen.
+template <bool MASKED>
+__device__ __forceinline__ void exponents(const uint32_t (&x)[2][32], const float4* nc, int q, uint64_t fa, uint64_t fb, uint64_t off,
+                                          uint2 seen, float (&y)[4]) {
+  const float4 a = nc[q], i1 = nc[kTile / 4 + q];
+  const uint32_t* xq = &x[q >> 3][4 * (q & 7)];
+  unpair(fma2(mul2(pair(xq[0], xq[1]), pair(a.x, a.y)), fa, fma2(pair(i1.x, i1.y), fb, off)), y[0], y[1]);
+  unpair(fma2(mul2(pair(xq[2], xq[3]), pair(a.z, a.w)), fa, fma2(pair(i1.z, i1.w), fb, off)), y[2], y[3]);
+  if (MASKED) {
+    const uint32_t bits = (q < 8 ? seen.x : seen.y) >> (4 * (q & 7));
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = (bits >> e) & 1u ? y[e] : -INFINITY;
+  }
+}
+
+// A row's 64 weights as pairs of binary16, and their sum in fp32.
+template <bool MASKED>
+__device__ __forceinline__ float row_weights(const uint32_t (&x)[2][32], const float4* nc, uint64_t fa, uint64_t fb, float offset, uint2 seen,
+                                             uint32_t (&pw)[32]) {
+  const uint64_t off = pair(offset, offset);
+  uint64_t acc0 = pair(0.0f, 0.0f), acc1 = acc0;
+  #pragma unroll
+  for (int q = 0; q < kHalf / 4; ++q) {
+    float y[4];
+    exponents<MASKED>(x, nc, q, fa, fb, off, seen, y);
+    const float e0 = ex2(y[0]), e1 = ex2(y[1]), e2 = ex2(y[2]), e3 = ex2(y[3]);
+    pw[2 * q] = pack_f16(e0, e1);
+    pw[2 * q + 1] = pack_f16(e2, e3);
+    acc0 = add2(acc0, pair(e0, e1));
+    acc1 = add2(acc1, pair(e2, e3));
+  }
+  float s0, s1;
+  unpair(add2(acc0, acc1), s0, s1);
+  return __fadd_rn(s0, s1);
+}
+
 __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const PagedAttendParams p, const PagedSharedParams s) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[kBuf], kv_empty[kBuf], s_full[2], p_full[2], o_done[2];
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[kBuf], kv_empty[kBuf];
+  __shared__ __align__(8) uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2][2];
   __shared__ uint32_t s_tmem, s_absent[kRaw];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // the warp as a uniform value
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kExpandWarps);
-    for (int i = 0; i < kBuf; ++i) mbar_init(&kv_full[i], kExpandWarps), mbar_init(&kv_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&o_done[i], 1);
+    for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kValueWarps + kSignWarps);
+    for (int i = 0; i < kBuf; ++i) mbar_init(&kv_full[i], kValueWarps + kSignWarps), mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1), mbar_init(&s_free[i], 4);
+      for (int e = 0; e < 2; ++e) mbar_init(&p_full[i][e], 4), mbar_init(&pv_done[i][e], 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
@@ -193,14 +260,16 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
   const int64_t nt = (n + kTile - 1) / kTile;
   const int t0 = static_cast<int>(nt * split / s.splits), tiles = static_cast<int>(nt * (split + 1) / s.splits) - t0;
   const bool two = s.two != 0;
-  if (nt > 0 && (tiles == 0 || (!two && tiles == 1))) {  // empty pieces of the lanes without a tile
-    for (int e = threadIdx.x; e < 256 * kRow; e += kShThreads) {
-      const int w = e / (128 * kRow), ch = e % kRow;
-      if (tiles == 0 || w == 1) s.pieces[static_cast<int64_t>(u) * 256 * kRow + e] = ch == 0 ? kNoRef : 0.0f;
-    }
+  if (tiles == 0) {  // the whole CTA: empty pieces (the merge reads none where the prefix is empty)
+    if (nt > 0)
+      for (int e = threadIdx.x; e < 256 * kRow; e += kShThreads)
+        s.pieces[static_cast<int64_t>(u) * 256 * kRow + e] = e % kRow == 0 ? kNoRef : 0.0f;
+    return;
   }
-  if (tiles == 0) return;  // the whole CTA
-  const int jobs = two ? 2 * tiles : tiles;  // job j: lane j & 1, tile j / 2 or j
+  // job j of lane w: half j & 1 of tile j / 2, or half w of tile j where the lanes hold the same rows
+  const int jobs = two ? 2 * tiles : tiles;
+  auto tile_of = [&](int j) { return two ? j >> 1 : j; };
+  auto half_of = [&](int w, int j) { return two ? j & 1 : w; };
 
   if (warp == 0) tmem_alloc(&s_tmem);
   {  // the rows' codes, swizzled; zeros behind the last row
@@ -216,10 +285,11 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(kFull, s_tmem, 0);
   if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   bool ok = true;  // false once a wait ran out
   auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(kFull, mbar_try(bar, parity))) return ok;
     if (!__all_sync(kFull, mbar_wait(bar, parity, kWaitTries))) ok = false;
     return ok;
   };
@@ -237,95 +307,88 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
     const uint64_t fa = pair(f.x, f.x), fb = pair(f.y, f.y);
     float m = 0.0f, l = 0.0f;
     bool have = false;  // a finite logit has set m
-    for (int j = w; j < jobs; j += 2) {
-      const int k = two ? j >> 1 : j, buf = k % kBuf;
-      if (!wait(&s_full[w], (j >> 1) & 1) || !wait(&kv_full[buf], (k / kBuf) & 1)) break;
+    bool cold = true;   // not in all of the warp's rows
+    uint32_t x[2][32];
+    auto load_sums = [&](int j) {
+      if (!wait(&s_full[w], j & 1)) return;
       tc_after();
       if (warp_rows) {
-        const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + kShMask) + buf * 4;
-        const uint4 seen = *reinterpret_cast<const uint4*>(mask);
-        const bool edge = (seen.x & seen.y & seen.z & seen.w) != 0xFFFFFFFFu;
-        const uint32_t nc = sb + kShNc + buf * 2 * kTile * 4;
-        uint32_t pw[64];
-        float sum = 0.0f;
-        #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          const uint64_t off = pair(kBase - m, kBase - m);
-          float top0 = -INFINITY, top1 = -INFINITY;
-          uint64_t acc = pair(0.0f, 0.0f);
-          uint32_t x[2][16];
-          tmem_ld16(x[0], tS);
-          #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            tmem_ld_wait(x[c & 1]);
-            if (c < 7) tmem_ld16(x[(c + 1) & 1], tS + 16 * (c + 1));
-            float y[16];
-            #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t a[4], i1[4];
-              lds128(a, nc + (16 * c + 4 * q) * 4);
-              lds128(i1, nc + (kTile + 16 * c + 4 * q) * 4);
-              #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint64_t t = mul2(pair(x[c & 1][4 * q + 2 * e], x[c & 1][4 * q + 2 * e + 1]), pair(a[2 * e], a[2 * e + 1]));
-                unpair(fma2(t, fa, fma2(pair(i1[2 * e], i1[2 * e + 1]), fb, off)), y[4 * q + 2 * e], y[4 * q + 2 * e + 1]);
-              }
-            }
-            if (edge) {
-              const uint32_t bits = (c < 2 ? seen.x : (c < 4 ? seen.y : (c < 6 ? seen.z : seen.w))) >> (16 * (c & 1));
-              #pragma unroll
-              for (int q = 0; q < 16; ++q) y[q] = (bits >> q) & 1u ? y[q] : -INFINITY;
-            }
-            #pragma unroll
-            for (int q = 0; q < 16; q += 4) {
-              top0 = max3(top0, y[q], y[q + 1]);
-              top1 = max3(top1, y[q + 2], y[q + 3]);
-            }
-            #pragma unroll
-            for (int q = 0; q < 16; q += 2) {
-              const float e0 = ex2(y[q]), e1 = ex2(y[q + 1]);
-              pw[8 * c + q / 2] = pack_f16(e0, e1);
-              acc = add2(acc, pair(e0, e1));
-            }
-          }
-          float s0, s1;
-          unpair(acc, s0, s1);
-          sum = __fadd_rn(s0, s1);
-          const float top = fmaxf(top0, top1) - kBase;  // relative to m
-          const bool up = top > kTau || (!have && top > -INFINITY);
-          if (pass == 1 || !__any_sync(kFull, up)) break;
-          // raise references: the row's sums so far come down by 2^(m - m')
-          const float alpha = up && have ? ex2(-top) : 1.0f;
-          m = up ? m + top : m;
-          have |= up;
-          l = __fmul_rn(l, alpha);
-          if (j >= 2) {
-            if (!wait(&o_done[w], ((j >> 1) - 1) & 1)) break;
-            tc_after();
-            #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t o[16];
-              tmem_ld16(o, tO + 16 * c);
-              tmem_ld_wait(o);
-              #pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__fmul_rn(__uint_as_float(o[q]), alpha));
-              tmem_st16(tO + 16 * c, o);
-            }
-          }
-        }
-        if (!ok) break;
-        l = __fadd_rn(l, sum);
-        #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_st16(tS + 16 * c, pw + 16 * c);
-        tmem_st_wait();
+        tmem_ld32(x[0], tS);
+        tmem_ld32(x[1], tS + 32);
       }
+    };
+    load_sums(0);
+    for (int j = 0; ok && j < jobs; ++j) {
+      const int k = tile_of(j), buf = k % kBuf, half = half_of(w, j), slot = j & 1;
+      // job j's sums are in registers, job j - 1's weights in tensor memory
+      tmem_ld_wait(x[0]);
+      tmem_ld_wait(x[1]);
+      tmem_st_wait();
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[w]);
+      if (lane == 0) {
+        mbar_arrive(&s_free[w]);
+        if (j > 0) mbar_arrive(&p_full[w][slot ^ 1]);
+      }
+      // the tile's factors were written before kv_full, which the products' warp waited for before the scores
+      uint32_t pw[32];
+      if (warp_rows) {
+        const uint2 seen = *(reinterpret_cast<const uint2*>(smem + kShMask) + buf * 2 + half);
+        const float4* nc = reinterpret_cast<const float4*>(smem + kShNc + buf * 2 * kTile * 4) + half * (kHalf / 4);
+        float sum = 0.0f;
+        bool slow = cold || (seen.x & seen.y) != 0xFFFFFFFFu;
+        if (!slow) {
+          sum = row_weights<false>(x, nc, fa, fb, kBase - m, seen, pw);
+          slow = __any_sync(kFull, sum > kMostSum);  // perhaps a weight past the bound
+        }
+        if (slow) {  // the first job, a tile with unseen tokens, or a reference to raise
+          float top = -INFINITY;
+          #pragma unroll
+          for (int q = 0; q < kHalf / 4; ++q) {
+            float y[4];
+            exponents<true>(x, nc, q, fa, fb, pair(-m, -m), seen, y);
+            top = max3(max3(top, y[0], y[1]), y[2], y[3]);
+          }
+          const bool up = top > kTau || (!have && top > -INFINITY);
+          if (__any_sync(kFull, up)) {
+            // the row's sums so far come down by 2^(m - m')
+            const float alpha = up && have ? ex2(-top) : 1.0f;
+            m = up ? m + top : m;
+            have |= up;
+            l = __fmul_rn(l, alpha);
+            if (j >= 1) {
+              if (!wait(&pv_done[w][slot ^ 1], ((j - 1) >> 1) & 1)) break;
+              tc_after();
+              #pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                tmem_ld16(o, tO + 16 * c);
+                tmem_ld_wait(o);
+                #pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__fmul_rn(__uint_as_float(o[q]), alpha));
+                tmem_st16(tO + 16 * c, o);
+              }
+            }
+          }
+          cold = __any_sync(kFull, !have);
+          sum = row_weights<true>(x, nc, fa, fb, kBase - m, seen, pw);
+        }
+        l = __fadd_rn(l, sum);
+      }
+      if (ok && j + 1 < jobs) load_sums(j + 1);
+      if (!ok || (j >= 2 && !wait(&pv_done[w][slot], ((j >> 1) - 1) & 1))) break;  // P's place is free
+      tc_after();
+      if (warp_rows) {
+        tmem_st16(tS + kHalf + 32 * slot, pw);
+        tmem_st16(tS + kHalf + 32 * slot + 16, pw + 16);
+      }
     }
+    tmem_st_wait();
+    tc_before();
+    __syncwarp();
+    if (ok && lane == 0) mbar_arrive(&p_full[w][(jobs - 1) & 1]);
     // the lane's sums
-    const int mine = jobs > w ? (jobs - w + 1) / 2 : 0;
-    if (ok && mine > 0 && wait(&o_done[w], (mine - 1) & 1)) {
+    if (ok && wait(&pv_done[w][(jobs - 1) & 1], ((jobs - 1) >> 1) & 1)) {
       tc_after();
       float* out = s.pieces + ((static_cast<int64_t>(u) * 2 + w) * 128 + r) * kRow;
       if (warp_rows) {
@@ -344,66 +407,78 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
       }
     }
   } else if (warp < kMmaWarp) {
-    // ------------------------------------------------------------------ expansion
-    const int g = warp - kSoftWarps;  // block of the tile for the signs, 32-channel group for the values
+    // ------------------------------------------------------------------ values: 32 channels of all tokens
+    const int g = warp - kSoftWarps;
     const int ch = 32 * g + lane;
-    const int bit_row = 8 * ((lane >> 1) & 3) + 2 * (lane >> 3) + (lane & 1);
     for (int k = 0; k < tiles; ++k) {
       const int raw = k % kRaw, buf = k % kBuf;
       if (!wait(&raw_full[raw], (k / kRaw) & 1)) break;
       if (k >= kBuf && !wait(&kv_empty[buf], (k / kBuf - 1) & 1)) break;
       const uint32_t absent = s_absent[raw];
       uint8_t* blk = smem + kShRaw + raw * kRawBytes;
-      const uint32_t blk_s = sb + kShRaw + raw * kRawBytes;
-      const int tok0 = (t0 + k) * kTile;
-      {  // token 32 g + lane: signs as +-1 in f8, its factors
-        const bool on = tok0 + 32 * g + lane < n && !((absent >> g) & 1u);
-        uint32_t bits[4];
-        lds128(bits, blk_s + g * kBlkBytes + bit_row * 16);
-        const float ncv = on ? reinterpret_cast<const float*>(blk + g * kBlkBytes + kBlkOffNc)[lane] : 0.0f;
+      const int left = n - (t0 + k) * kTile;
+      if (left < kTile || absent) {  // unseen tokens' values are zeros, whatever their places hold
+        #pragma unroll 1
+        for (int b = 0; b < kTileBlocks; ++b)
+          if (((absent >> b) & 1u) || 32 * b + lane >= left) {
+            reinterpret_cast<uint16_t*>(blk + b * kBlkBytes + kBlkOffScale)[32 * g + lane] = 0;
+            reinterpret_cast<uint16_t*>(blk + b * kBlkBytes + kBlkOffMin)[32 * g + lane] = 0;
+          }
+        __syncwarp();
+      }
+      #pragma unroll 2
+      for (int b = 0; b < kTileBlocks; ++b) {
+        const uint8_t* base = blk + b * kBlkBytes;
+        const uint4 cw4 = *reinterpret_cast<const uint4*>(base + kBlkOffCodes + ch * 16);
+        const uint32_t cw[4] = {cw4.x, cw4.y, cw4.z, cw4.w};
+        uint8_t* vrow = smem + kShV + buf * kVBytes + (b >> 1) * (kVBytes / 2) + ch * 128;
+        #pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 sc = *reinterpret_cast<const uint4*>(base + kBlkOffScale + g * 64 + q * 16);
+          const uint4 mn = *reinterpret_cast<const uint4*>(base + kBlkOffMin + g * 64 + q * 16);
+          uint32_t c[4];
+          expand_codes(cw[q], c);
+          *reinterpret_cast<uint4*>(vrow + (((4 * (b & 1) + q) ^ (lane & 7)) << 4)) =
+              make_uint4(hfma2(c[0], sc.x, mn.x), hfma2(c[1], sc.y, mn.y), hfma2(c[2], sc.z, mn.z), hfma2(c[3], sc.w, mn.w));
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&kv_full[buf]);
+        mbar_arrive(&raw_empty[raw]);
+      }
+    }
+  } else if (warp >= kSignWarp) {
+    // ------------------------------------------------------------------ signs as +-1 in f8 and the tokens' factors
+    const int bit_row = 8 * ((lane >> 1) & 3) + 2 * (lane >> 3) + (lane & 1);
+    for (int k = 0; k < tiles; ++k) {
+      const int raw = k % kRaw, buf = k % kBuf;
+      if (!wait(&raw_full[raw], (k / kRaw) & 1)) break;
+      if (k >= kBuf && !wait(&kv_empty[buf], (k / kBuf - 1) & 1)) break;
+      const uint32_t absent = s_absent[raw];
+      const int left = n - (t0 + k) * kTile;
+      #pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = 2 * (warp - kSignWarp) + i, tok = 32 * b + lane;
+        const uint8_t* blk = smem + kShRaw + raw * kRawBytes + b * kBlkBytes;
+        const bool on = tok < left && !((absent >> b) & 1u);
+        const uint4 w4 = *reinterpret_cast<const uint4*>(blk + bit_row * 16);
+        const uint32_t bits[4] = {w4.x, w4.y, w4.z, w4.w};
+        const float ncv = on ? reinterpret_cast<const float*>(blk + kBlkOffNc)[lane] : 0.0f;
         const int i1 = 2 * (__popc(bits[0]) + __popc(bits[1]) + __popc(bits[2]) + __popc(bits[3])) - kD;
-        float* ncp = reinterpret_cast<float*>(smem + kShNc) + buf * 2 * kTile + 32 * g + lane;
+        float* ncp = reinterpret_cast<float*>(smem + kShNc) + buf * 2 * kTile + tok;
         ncp[0] = ncv;
         ncp[kTile] = __fmul_rn(ncv, static_cast<float>(i1));
         const uint32_t seen = __ballot_sync(kFull, on);
-        if (lane == 0) reinterpret_cast<uint32_t*>(smem + kShMask)[buf * 4 + g] = seen;
-        uint8_t* krow = smem + kShK + buf * kKBytes + (32 * g + lane) * 128;
+        if (lane == 0) reinterpret_cast<uint32_t*>(smem + kShMask)[buf * 4 + b] = seen;
+        uint8_t* krow = smem + kShK + buf * kKBytes + tok * 128;
         #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t v[4];
           #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 4 * (c & 1) + i;
-            v[i] = ((~bits[c >> 1] << (7 - rr)) & 0x80808080u) | 0x38383838u;
-          }
+          for (int e = 0; e < 4; ++e) v[e] = ((~bits[c >> 1] << (7 - (4 * (c & 1) + e))) & 0x80808080u) | 0x38383838u;
           *reinterpret_cast<uint4*>(krow + ((c ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-      }
-      // channel ch: the values of all tokens
-      #pragma unroll 1
-      for (int b = 0; b < kTileBlocks; ++b) {
-        const int left = n - tok0 - 32 * b;
-        const bool gone = ((absent >> b) & 1u) != 0;
-        if (left < 32 || gone) {  // unseen tokens' values are zeros, whatever their places hold
-          if (gone || lane >= left) {
-            reinterpret_cast<uint16_t*>(blk + b * kBlkBytes + kBlkOffScale)[32 * g + lane] = 0;
-            reinterpret_cast<uint16_t*>(blk + b * kBlkBytes + kBlkOffMin)[32 * g + lane] = 0;
-          }
-          __syncwarp();
-        }
-        const uint32_t base = blk_s + b * kBlkBytes;
-        uint32_t cw[4];
-        lds128(cw, base + kBlkOffCodes + ch * 16);
-        uint8_t* vrow = smem + kShV + buf * kVBytes + (b >> 1) * (kVBytes / 2) + ch * 128;
-        #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t c[4], sc[4], mn[4];
-          lds128(sc, base + kBlkOffScale + g * 64 + q * 16);
-          lds128(mn, base + kBlkOffMin + g * 64 + q * 16);
-          expand_codes(cw[q], c);
-          #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] = hfma2(c[i], sc[i], mn[i]);
-          *reinterpret_cast<uint4*>(vrow + (((4 * (b & 1) + q) ^ (lane & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -414,36 +489,44 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
       }
     }
   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ products, in the jobs' order
-    auto scores = [&](int j) {
-      const int w = j & 1, k = two ? j >> 1 : j, buf = k % kBuf;
+    // ------------------------------------------------------------------ products
+    auto scores = [&](int w, int j) {
+      const int k = tile_of(j), buf = k % kBuf;
       if (!wait(&kv_full[buf], (k / kBuf) & 1)) return;
       tc_after();
-      if (lane == 0) {
-        const uint64_t a = operand(sb + kShQ + (two ? w * kQBytes : 0)), b = operand(sb + kShK + buf * kKBytes);
+      if (elect()) {
+        const uint64_t a = operand(sb + kShQ + (two ? w * kQBytes : 0));
+        const uint64_t b = operand(sb + kShK + buf * kKBytes + half_of(w, j) * (kKBytes / 2));
         #pragma unroll
         for (int i = 0; i < 4; ++i) mma_f8(tmem + w * 256, a + 2 * i, b + 2 * i, i > 0);  // 32 channels each
         tc_commit(&s_full[w]);
       }
       __syncwarp();
     };
-    scores(0);
-    if (ok && jobs > 1) scores(1);
-    for (int j = 0; ok && j < jobs; ++j) {
-      const int w = j & 1, k = two ? j >> 1 : j, buf = k % kBuf;
-      if (!wait(&p_full[w], (j >> 1) & 1)) break;
-      tc_after();
-      if (lane == 0) {
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) {  // 16 tokens each
-          const uint64_t b = operand(sb + kShV + buf * kVBytes + (i >> 2) * (kVBytes / 2)) + 2 * (i & 3);
-          mma_f16_ta(tmem + w * 256 + 128, tmem + w * 256 + 8 * i, b, j >= 2 || i > 0);
+    scores(0, 0);
+    if (ok) scores(1, 0);
+    for (int j = 0; ok && j <= jobs; ++j) {  // a lane gives S of job j and P of job j - 1 at the same time
+      #pragma unroll 1
+      for (int w = 0; ok && w < 2; ++w) {
+        if (j + 1 < jobs) {
+          if (!wait(&s_free[w], j & 1)) break;
+          tc_after();
+          scores(w, j + 1);
         }
-        tc_commit(&o_done[w]);
-        if (!two || w == 1) tc_commit(&kv_empty[buf]);
+        if (j == 0) continue;
+        const int i = j - 1, half = half_of(w, i), slot = i & 1, k = tile_of(i), buf = k % kBuf;
+        if (!wait(&p_full[w][slot], (i >> 1) & 1)) break;
+        tc_after();
+        if (elect()) {
+          #pragma unroll
+          for (int c = 0; c < 4; ++c)  // 16 tokens each
+            mma_f16_ta(tmem + w * 256 + 128, tmem + w * 256 + kHalf + 32 * slot + 8 * c,
+                       operand(sb + kShV + buf * kVBytes + half * (kVBytes / 2)) + 2 * c, i > 0 || c > 0);
+          tc_commit(&pv_done[w][slot]);
+          if (w == 1 && (!two || half == 1)) tc_commit(&kv_empty[buf]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      if (j + 2 < jobs) scores(j + 2);
     }
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------------ copies: lane b < 4 block b
