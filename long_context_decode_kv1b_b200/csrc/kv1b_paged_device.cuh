@@ -21,17 +21,26 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, int count) {
 }
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(500000u)
-      : "memory");
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
   return ok != 0;
 }
-// Bounded wait (at most kWaitTries suspended tries of 0.5 ms); false when it ran out.
+// Bounded wait: at most `tries` suspended tries of up to 0.5 ms (the first, which finds nearly every barrier
+// complete, without a time: 82 against 118 clocks); false when they ran out.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int tries) {
-  for (int i = 0; i < tries; ++i)
-    if (mbar_try(bar, parity)) return true;
+  if (mbar_try(bar, parity)) return true;
+  #pragma unroll 1
+  for (int i = 0; i < tries; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(500000u)
+        : "memory");
+    if (ok) return true;
+  }
   return false;
 }
 __device__ __forceinline__ void block_g2s(uint32_t dst, const void* src, uint64_t* bar) {

@@ -12,11 +12,11 @@
 // memory).  A softmax thread takes its 64 sums into registers at once and gives S back, so the next job's
 // scores are made while it works, and P has two places, so it never waits for the products: per lane 64
 // columns of S, 2 x 32 of P and 128 of O, for two lanes all 512.  (One S of 128 columns with P written
-// over it, so that each job went round softmax, P V and Q K: 201 us instead of @NEW@ us at 256 rows x
+// over it, so that each job went round softmax, P V and Q K: 201 us instead of 169 us at 256 rows x
 // 131,072 tokens x 8 kv-heads.)
 //
 // Warps: 0 - 3 and 4 - 7 the lanes' softmax, 8 - 11 the values' expansion (codes to f16, one rounding), 12
-// issues the products, 13 the copies, 14 and 15 the signs' expansion to f8.  Each wait is bounded; one that
+// and 13 issue a lane's products each, 14 and 15 expand the signs to f8, 14 also copies the packed blocks.  Each wait is bounded; one that
 // runs out ends the CTA with KV1B_STATUS_TIMEOUT.
 //
 // A tile of 128 tokens x 256 rows costs 512 + 1,024 clocks of products and 32,768 exponentials, 2,048
@@ -29,7 +29,7 @@ namespace paged {
 constexpr int kTile = 128;                 // tokens
 constexpr int kTileBlocks = kTile / kBlkTok;
 constexpr int kSoftWarps = 8, kValueWarps = 4, kSignWarps = 2;
-constexpr int kMmaWarp = kSoftWarps + kValueWarps, kCopyWarp = kMmaWarp + 1, kSignWarp = kCopyWarp + 1;
+constexpr int kMmaWarp = kSoftWarps + kValueWarps, kSignWarp = kMmaWarp + 2;
 constexpr int kHalf = 64;                  // tokens of a job
 constexpr float kMostSum = 32768.0f;       // 2^(kBase + kTau): a sum up to it holds no larger weight
 constexpr int kShThreads = 512;            // four warpgroups
@@ -234,7 +234,7 @@ __device__ __forceinline__ float row_weights(const uint32_t (&x)[2][32], const f
 __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const PagedAttendParams p, const PagedSharedParams s) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[kBuf], kv_empty[kBuf];
-  __shared__ __align__(8) uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2][2];
+  __shared__ __align__(8) uint64_t s_full[2], turn[2], pv_done[2][2];
   __shared__ uint32_t s_tmem, s_absent[kRaw];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kValueWarps + kSignWarps);
-    for (int i = 0; i < kBuf; ++i) mbar_init(&kv_full[i], kValueWarps + kSignWarps), mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < kBuf; ++i) mbar_init(&kv_full[i], kValueWarps + kSignWarps), mbar_init(&kv_empty[i], 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1), mbar_init(&s_free[i], 4);
-      for (int e = 0; e < 2; ++e) mbar_init(&p_full[i][e], 4), mbar_init(&pv_done[i][e], 1);
+      mbar_init(&s_full[i], 1), mbar_init(&turn[i], 4);
+      mbar_init(&pv_done[i][0], 1), mbar_init(&pv_done[i][1], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
   if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   bool ok = true;  // false once a wait ran out
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (__all_sync(kFull, mbar_try(bar, parity))) return ok;
     if (!__all_sync(kFull, mbar_wait(bar, parity, kWaitTries))) ok = false;
     return ok;
   };
@@ -309,31 +308,34 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
     bool have = false;  // a finite logit has set m
     bool cold = true;   // not in all of the warp's rows
     uint32_t x[2][32];
-    auto load_sums = [&](int j) {
-      if (!wait(&s_full[w], j & 1)) return;
-      tc_after();
-      if (warp_rows) {
-        tmem_ld32(x[0], tS);
-        tmem_ld32(x[1], tS + 32);
-      }
+    uint2 seen;  // of the job's tokens
+    // Sums of the next job into registers, with the wait in the same straight line: nothing may copy the
+    // registers of a load in flight.  Warps without rows load and store along, in rows that nobody reads.
+    auto load_sums = [&]() {
+      tmem_ld32(x[0], tS);
+      tmem_ld32(x[1], tS + 32);
     };
-    load_sums(0);
-    for (int j = 0; ok && j < jobs; ++j) {
-      const int k = tile_of(j), buf = k % kBuf, half = half_of(w, j), slot = j & 1;
-      // job j's sums are in registers, job j - 1's weights in tensor memory
+    auto sums_loaded = [&](int j) {
+      seen = *(reinterpret_cast<const uint2*>(smem + kShMask) + (tile_of(j) % kBuf) * 2 + half_of(w, j));
       tmem_ld_wait(x[0]);
       tmem_ld_wait(x[1]);
       tmem_st_wait();
       tc_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s_free[w]);
-        if (j > 0) mbar_arrive(&p_full[w][slot ^ 1]);
-      }
-      // the tile's factors were written before kv_full, which the products' warp waited for before the scores
+      if (elect()) mbar_arrive(&turn[w]);
+    };
+    if (wait(&s_full[w], 0)) {
+      tc_after();
+      load_sums();
+      sums_loaded(0);
+    }
+    for (int j = 0; ok && j < jobs; ++j) {
+      const int k = tile_of(j), buf = k % kBuf, half = half_of(w, j), slot = j & 1;
       uint32_t pw[32];
-      if (warp_rows) {
-        const uint2 seen = *(reinterpret_cast<const uint2*>(smem + kShMask) + buf * 2 + half);
+      if (!warp_rows) {
+        #pragma unroll
+        for (int i = 0; i < 32; ++i) pw[i] = 0;
+      } else {
         const float4* nc = reinterpret_cast<const float4*>(smem + kShNc + buf * 2 * kTile * 4) + half * (kHalf / 4);
         float sum = 0.0f;
         bool slow = cold || (seen.x & seen.y) != 0xFFFFFFFFu;
@@ -375,18 +377,20 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
         }
         l = __fadd_rn(l, sum);
       }
-      if (ok && j + 1 < jobs) load_sums(j + 1);
-      if (!ok || (j >= 2 && !wait(&pv_done[w][slot], ((j >> 1) - 1) & 1))) break;  // P's place is free
+      if (!ok) break;
+      // The next scores' commit covers the products issued before them, P V of job j - 2 among them, so P's
+      // place is free; and the tile's factors and masks were written before the products' warp waited for
+      // the tile.  The commit follows all four warps' turn j; behind the last job, where no scores come, a
+      // warp waits for that turn itself before it arrives for the next.
+      const bool more = j + 1 < jobs;
+      if (!wait(more ? &s_full[w] : &turn[w], more ? (j + 1) & 1 : j & 1)) break;
+      if (!more && j >= 2 && !wait(&pv_done[w][slot], ((j >> 1) - 1) & 1)) break;
       tc_after();
-      if (warp_rows) {
-        tmem_st16(tS + kHalf + 32 * slot, pw);
-        tmem_st16(tS + kHalf + 32 * slot + 16, pw + 16);
-      }
+      load_sums();  // behind the last job: once more, unused
+      tmem_st16(tS + kHalf + 32 * slot, pw);
+      tmem_st16(tS + kHalf + 32 * slot + 16, pw + 16);
+      sums_loaded(more ? j + 1 : j);
     }
-    tmem_st_wait();
-    tc_before();
-    __syncwarp();
-    if (ok && lane == 0) mbar_arrive(&p_full[w][(jobs - 1) & 1]);
     // the lane's sums
     if (ok && wait(&pv_done[w][(jobs - 1) & 1], ((jobs - 1) >> 1) & 1)) {
       tc_after();
@@ -451,7 +455,42 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
     }
   } else if (warp >= kSignWarp) {
     // ------------------------------------------------------------------ signs as +-1 in f8 and the tokens' factors
+    // and, by the first of the two warps, the copies of the packed blocks (lane b < 4 block b of a tile)
     const int bit_row = 8 * ((lane >> 1) & 3) + 2 * (lane >> 3) + (lane & 1);
+    const bool copies = warp == kSignWarp;
+    const int nblk = (n + kBlkTok - 1) / kBlkTok;
+    int copied = 0;  // tiles
+    auto entry = [&](int k) {
+      const int blk = (t0 + k) * kTileBlocks + lane;
+      return lane < kTileBlocks && blk < nblk ? __ldg(p.prefix_pages + (blk >> p.c.bpp_shift)) : -1;
+    };
+    int page = copies ? entry(0) : -1;
+    auto copy_next = [&]() {
+      const int raw = copied % kRaw, blk = (t0 + copied) * kTileBlocks + lane;
+      const bool want = lane < kTileBlocks && blk < nblk;
+      const bool here = want && page >= 0 && page < p.c.num_pages;
+      const uint32_t have = __ballot_sync(kFull, here);
+      if (want && !here && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+      if (lane == 0) {
+        s_absent[raw] = ~have & 0xFu;
+        asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&raw_full[raw])),
+                     "r"(__popc(have) * kBlkBytes)
+                     : "memory");
+      }
+      __syncwarp();
+      if (here) {
+        const int in = blk & ((1 << p.c.bpp_shift) - 1);
+        const uint8_t* src = p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + h) << p.c.bpp_shift) + in) * kBlkBytes);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         sb + kShRaw + raw * kRawBytes + lane * kBlkBytes),
+                     "l"(src), "r"(kBlkBytes), "r"(smem_u32(&raw_full[raw]))
+                     : "memory");
+      }
+      ++copied;
+      if (copied < tiles) page = entry(copied);
+    };
+    if (copies)
+      while (copied < kRaw && copied < tiles) copy_next();
     for (int k = 0; k < tiles; ++k) {
       const int raw = k % kRaw, buf = k % kBuf;
       if (!wait(&raw_full[raw], (k / kRaw) & 1)) break;
@@ -487,12 +526,19 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
         mbar_arrive(&kv_full[buf]);
         mbar_arrive(&raw_empty[raw]);
       }
+      if (copies && copied < tiles) {
+        if (!wait(&raw_empty[raw], (k / kRaw) & 1)) break;
+        copy_next();
+      }
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ products
-    auto scores = [&](int w, int j) {
+    if (copies)  // no copy may outlive the CTA, also where the expansion gave up
+      for (int i = copied > kRaw ? copied - kRaw : 0; i < copied; ++i) mbar_wait(&raw_full[i % kRaw], (i / kRaw) & 1, kWaitTries);
+  } else {
+    // ------------------------------------------------------------------ products of one lane
+    const int w = warp - kMmaWarp;
+    auto scores = [&](int j) {
       const int k = tile_of(j), buf = k % kBuf;
-      if (!wait(&kv_full[buf], (k / kBuf) & 1)) return;
+      if ((!two || (j & 1) == 0) && !wait(&kv_full[buf], (k / kBuf) & 1)) return;
       tc_after();
       if (elect()) {
         const uint64_t a = operand(sb + kShQ + (two ? w * kQBytes : 0));
@@ -503,66 +549,23 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
       }
       __syncwarp();
     };
-    scores(0, 0);
-    if (ok) scores(1, 0);
-    for (int j = 0; ok && j <= jobs; ++j) {  // a lane gives S of job j and P of job j - 1 at the same time
-      #pragma unroll 1
-      for (int w = 0; ok && w < 2; ++w) {
-        if (j + 1 < jobs) {
-          if (!wait(&s_free[w], j & 1)) break;
-          tc_after();
-          scores(w, j + 1);
-        }
-        if (j == 0) continue;
-        const int i = j - 1, half = half_of(w, i), slot = i & 1, k = tile_of(i), buf = k % kBuf;
-        if (!wait(&p_full[w][slot], (i >> 1) & 1)) break;
-        tc_after();
-        if (elect()) {
-          #pragma unroll
-          for (int c = 0; c < 4; ++c)  // 16 tokens each
-            mma_f16_ta(tmem + w * 256 + 128, tmem + w * 256 + kHalf + 32 * slot + 8 * c,
-                       operand(sb + kShV + buf * kVBytes + half * (kVBytes / 2)) + 2 * c, i > 0 || c > 0);
-          tc_commit(&pv_done[w][slot]);
-          if (w == 1 && (!two || half == 1)) tc_commit(&kv_empty[buf]);
-        }
-        __syncwarp();
-      }
-    }
-  } else if (warp == kCopyWarp) {
-    // ------------------------------------------------------------------ copies: lane b < 4 block b
-    const int nblk = (n + kBlkTok - 1) / kBlkTok;
-    auto entry = [&](int k) {
-      const int blk = (t0 + k) * kTileBlocks + lane;
-      return lane < kTileBlocks && blk < nblk ? __ldg(p.prefix_pages + (blk >> p.c.bpp_shift)) : -1;
-    };
-    int page = entry(0), k = 0;
-    for (; k < tiles; ++k) {
-      const int raw = k % kRaw;
-      if (k >= kRaw && !wait(&raw_empty[raw], (k / kRaw - 1) & 1)) break;
-      const int blk = (t0 + k) * kTileBlocks + lane;
-      const bool want = lane < kTileBlocks && blk < nblk;
-      const bool here = want && page >= 0 && page < p.c.num_pages;
-      const uint32_t have = __ballot_sync(kFull, here);
-      if (want && !here && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
-      if (lane == 0) {
-        s_absent[raw] = ~have & 0xFu;
-        asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&raw_full[raw])),
-                     "r"(__popc(have) * kBlkBytes)
-                     : "memory");
+    scores(0);
+    for (int j = 0; ok && j <= jobs; ++j) {  // S of job j has been read and P of job j - 1 written
+      if (!wait(&turn[w], j & 1)) break;
+      if (j + 1 < jobs) scores(j + 1);
+      if (!ok || j == 0) continue;
+      const int i = j - 1, half = half_of(w, i), slot = i & 1, buf = tile_of(i) % kBuf;
+      tc_after();
+      if (elect()) {
+        const uint64_t b = operand(sb + kShV + buf * kVBytes + half * (kVBytes / 2));
+        #pragma unroll
+        for (int c = 0; c < 4; ++c)  // 16 tokens each
+          mma_f16_ta(tmem + w * 256 + 128, tmem + w * 256 + kHalf + 32 * slot + 8 * c, b + 2 * c, i > 0 || c > 0);
+        tc_commit(&pv_done[w][slot]);
+        if (!two || half == 1) tc_commit(&kv_empty[buf]);
       }
       __syncwarp();
-      if (here) {
-        const int in = blk & ((1 << p.c.bpp_shift) - 1);
-        const uint8_t* src = p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + h) << p.c.bpp_shift) + in) * kBlkBytes);
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         sb + kShRaw + raw * kRawBytes + lane * kBlkBytes),
-                     "l"(src), "r"(kBlkBytes), "r"(smem_u32(&raw_full[raw]))
-                     : "memory");
-      }
-      if (k + 1 < tiles) page = entry(k + 1);
     }
-    // no copy may outlive the CTA, also where the expansion gave up
-    for (int i = k > kRaw ? k - kRaw : 0; i < k; ++i) mbar_wait(&raw_full[i % kRaw], (i / kRaw) & 1, kWaitTries);
   }
   if (!ok && lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_TIMEOUT);
   tc_before();

@@ -131,8 +131,11 @@ class Row:
         """Channel by channel.  Relative to the weighted mean of |value|: a weight's rounding to binary16 in
         the numerator and in the normaliser, a value's (2^-11 each), the fp32 logit (16 roundings of its
         terms' magnitude) and its exponential (2^-21), twice, and 2^-18 for the fp32 sums.  Relative to the
-        weighted mean of scale code: the rounding of weight scale to binary16, 2^-11, or of its second
-        part for fp16 results.  Small weights: one is 2^(7 - k) at its reference, which some token attains,
+        weighted mean of scale code: the rounding of weight scale to binary16, 2^-11; or, for fp16 results,
+        which carry it in two parts, what the codes lose as subnormal operands: the tensor cores line a
+        product up by its operands' exponents, and a code c 2^-24 counts as 2^-14, so its sum keeps 2^10
+        fewer of 24 bits; seventeen terms a product of a code that is 8 on the mean, at most 2^-13.  Small
+        weights: one is 2^(7 - k) at its reference, which some token attains,
         where every scale is below 2^(1 + k); as a subnormal it may lose 2^-25, 2^-21 where it enters 2^-4
         lower, and weight scale may lose 2^-25 times a code of 15: a token adds at most 2^(k - 28) of the
         largest |value|, twice for the normaliser, and 2^(k - 28) itself.  At the end one rounding of the
@@ -142,7 +145,7 @@ class Row:
         k = max(1.0, 2 * self.step)
         rel = 3 * 2.0 ** -11 + 2 * (16 * 2.0 ** -24 * self.mag + 2.0 ** -21) + 2.0 ** -18
         tail = self.tokens * k * 2.0 ** -28 * (2 * self.largest + 1)
-        part = 2.0 ** -11 if eps > 2.0 ** -9 else 2.0 ** -21
+        part = 2.0 ** -11 if eps > 2.0 ** -9 else 2.0 ** -13
         return (1 + eps) * (rel * self.spread + part * self.reach + tail) + eps / 2 * np.abs(self.out) + 2.0 ** -25
 
 

@@ -12,6 +12,11 @@ pytestmark = pytest.mark.gpu
 SCALE = 128 ** -0.5
 
 
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(20)
+
+
 def table_for(counts, num_pages, rng, width=None):
     """Shuffled pages: int32 [seqs, width], -1 behind a sequence's pages."""
     order = rng.permutation(num_pages)
