@@ -103,7 +103,9 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
   if (!aligned(k, 16) || !aligned(v, 16) || k_stride_t % 4 || k_stride_h % 4 || v_stride_t % 4 || v_stride_h % 4)
     return KV1B_ERR_MISALIGNED;
   if (!aligned(cu_new, 4) || !aligned(start, 4) || !aligned(page_table, 4)) return KV1B_ERR_MISALIGNED;
-  if (num_tokens > (1 << 28)) return KV1B_ERR_UNSUPPORTED;
+  // rows of one launch
+  if (num_tokens > (1 << 28) || static_cast<int64_t>(num_tokens) * (cache->num_kv_heads + (q ? num_q_heads : 0)) > (1LL << 33))
+    return KV1B_ERR_UNSUPPORTED;
   kv1b::PagedAppendParams p;
   memset(&p, 0, sizeof(p));
   if (rope) {
@@ -130,7 +132,6 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
   if (q || q_out) {
     if (!q || !q_out || q_stride_t < 0 || q_stride_h < 0 || qo_stride_t < 0 || qo_stride_h < 0) return KV1B_ERR_INVALID_ARG;
     if (num_q_heads < 1 || num_q_heads > KV1B_PAGED_MAX_HEADS) return KV1B_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(num_tokens) * num_q_heads > (1LL << 33)) return KV1B_ERR_UNSUPPORTED;  // rows of one launch
     if (!aligned(q, 16) || !aligned(q_out, 16) || q_stride_t % 4 || q_stride_h % 4 || qo_stride_t % 4 || qo_stride_h % 4)
       return KV1B_ERR_MISALIGNED;
     p.q = q;

@@ -74,9 +74,9 @@ __device__ __forceinline__ uint8_t* block_of(const PagedAppendParams& p, int b, 
   return p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + h) << p.c.bpp_shift) + in) * kBlkBytes);
 }
 
-// Rotary table indices of channel c < rot: pair, and the row of its axis.
-__device__ __forceinline__ int axis_of(const PagedAppendParams& p, int pair) {
-  return (pair >= p.sec0 ? 1 : 0) + (pair >= p.sec01 ? 1 : 0);
+// The rotary table's row of a pair: the position on the pair's axis.
+__device__ __forceinline__ const float* factor_row(const PagedAppendParams& p, const int (&ps)[3], int pair) {
+  return p.cos_sin + static_cast<int64_t>(pair < p.sec0 ? ps[0] : (pair < p.sec01 ? ps[1] : ps[2])) * p.rot;
 }
 
 // Positions of row t on the three axes (the same for unused ones); false if one is outside the table.
@@ -112,7 +112,7 @@ __device__ __forceinline__ void rope_warp(const PagedAppendParams& p, const int 
     #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int i = 2 * lane + u;
-      const float* row = p.cos_sin + static_cast<int64_t>(ps[axis_of(p, i)]) * p.rot;
+      const float* row = factor_row(p, ps, i);
       const float c = __ldg(row + i), s = __ldg(row + half + i);
       const float a = x[2 * u], b = x[2 * u + 1];
       x[2 * u] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
@@ -127,9 +127,59 @@ __device__ __forceinline__ void rope_warp(const PagedAppendParams& p, const int 
     const float o = __shfl_sync(kFull, x[r], src);
     if (in) {
       const int i = c0 + r - (upper ? half : 0);
-      const float* row = p.cos_sin + static_cast<int64_t>(ps[axis_of(p, i)]) * p.rot;
+      const float* row = factor_row(p, ps, i);
       const float c = __ldg(row + i), s = __ldg(row + half + i);
       x[r] = upper ? __fadd_rn(__fmul_rn(x[r], c), __fmul_rn(o, s)) : __fsub_rn(__fmul_rn(x[r], c), __fmul_rn(o, s));
+    }
+  }
+}
+
+// Query rows [h0, h1) of token t by the calling warp, lane l channels 4l .. 4l + 3 of each: the token's
+// factors are read once for all of them, eight rows are in flight.
+template <int DT>
+__device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t, int h0, int h1) {
+  typedef typename Elem<DT>::T E;
+  const int lane = threadIdx.x & 31, half = p.rot >> 1, c0 = 4 * lane;
+  const bool in = p.cos_sin && c0 < p.rot;
+  const bool upper = !p.interleaved && c0 >= half;
+  const int src = in && !p.interleaved ? (upper ? lane - (half >> 2) : lane + (half >> 2)) : lane;
+  float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of the channels' pairs
+  if (p.cos_sin) {
+    int ps[3];
+    if (!positions(p, t, ps)) {
+      if (lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+      return;
+    }
+    if (in) {
+      #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = p.interleaved ? (c0 + r) >> 1 : c0 + r - (upper ? half : 0);
+        const float* row = factor_row(p, ps, i);
+        cs[r] = __ldg(row + i);
+        sn[r] = __ldg(row + half + i);
+      }
+    }
+  }
+  const E* q = static_cast<const E*>(p.q) + t * p.q_st + c0;
+  E* out = static_cast<E*>(p.q_out) + t * p.qo_st + c0;
+  constexpr int kRows = 8;
+  #pragma unroll 1
+  for (int h = h0; h < h1; h += kRows) {
+    float x[kRows][4];
+    #pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (h + k < h1) load4(q, (h + k) * p.q_sh, DT, x[k]);
+    #pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (h + k >= h1) break;
+      float y[4];
+      #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float o = p.interleaved ? x[k][r ^ 1] : __shfl_sync(kFull, x[k][r], src);
+        const float a = __fmul_rn(x[k][r], cs[r]), b = __fmul_rn(o, sn[r]);
+        y[r] = in ? ((p.interleaved ? (r & 1) != 0 : upper) ? __fadd_rn(a, b) : __fsub_rn(a, b)) : x[k][r];
+      }
+      store4(out, (h + k) * p.qo_sh, DT, y);
     }
   }
 }
@@ -274,15 +324,45 @@ __global__ void __launch_bounds__(128) paged_append_token_kernel(const PagedAppe
 }
 
 // ---------------------------------------------------------------------------------------------
-// Prefill form: one warp per (group, kv-head), 4 lanes per token (kv1b_encode_q4.cuh).
+// Prefill form: one warp per (group, kv-head), 4 lanes per token (kv1b_encode_q4.cuh).  The group's rotary
+// factors are staged per warp in shared memory, [token][pair], rows kFactorRow apart so that the 8 x 4
+// lanes read 32 banks.
+constexpr int kFactorRow = 68;  // kD / 2 + 4
+constexpr int kPrefillGroupsPerBlock = 4;
+constexpr int kQueryHeads = 32;  // query rows of a token that a warp turns
+
+// Half-split pairs (c, c + 4 HQ) both sit in the lane: x[r] and x[r + HQ].
+template <int HQ>
+__device__ __forceinline__ void rope_in_lane(float (&x)[32], const float* cs, const float* sn, int j) {
+  #pragma unroll
+  for (int r = 0; r < HQ; ++r) {
+    const float c = cs[j + 4 * r], s = sn[j + 4 * r], a = x[r], b = x[r + HQ];
+    x[r] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    x[r + HQ] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  }
+}
+
 template <int DT>
-__global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAppendParams p) {
+__global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAppendParams p, const int64_t kv_blocks) {
   typedef typename Elem<DT>::T T;
+  __shared__ float s_factors[kPrefillGroupsPerBlock][2][8 * kFactorRow];
   pdl_wait();
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31, tau = lane >> 2, j = lane & 3;
-  const int gi = blockIdx.x * 4 + (threadIdx.x >> 5);
+  // Blocks of keys and values, which are bound by their instructions, and blocks of queries, by memory,
+  // are spread evenly among one another: both kinds run on every SM at all times.
+  const int64_t u = blockIdx.x, kv0 = u * kv_blocks / gridDim.x;
+  if ((u + 1) * kv_blocks / gridDim.x == kv0) {
+    const int chunks = (p.Hq + kQueryHeads - 1) / kQueryHeads;
+    const int64_t unit = (u - kv0) * 4 + (threadIdx.x >> 5), t = unit / chunks;
+    if (t >= p.T || t >= __ldg(p.cu + p.B)) return;
+    const int h0 = static_cast<int>(unit - t * chunks) * kQueryHeads;
+    query_rows<DT>(p, t, h0, min(h0 + kQueryHeads, p.Hq));
+    return;
+  }
+  const int gi = static_cast<int>(kv0 / p.c.Hkv) * kPrefillGroupsPerBlock + (threadIdx.x >> 5);
   if (gi >= p.groups) return;
-  const int h = blockIdx.y;
+  const int h = static_cast<int>(kv0 % p.c.Hkv);
   const Group g = find_group(p, gi);
   if (!g.any) return;
   const int64_t pos = g.g0 + tau;
@@ -301,20 +381,55 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
     float x[32], a[32];
     #pragma unroll
     for (int r = 0; r < 32; ++r) x[r] = on ? Elem<DT>::get(__ldg(krow + j + 4 * r)) : 0.0f;
-    if (p.cos_sin && on) {
+    if (p.cos_sin) {
       const int half = p.rot >> 1;
-      #pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        const int c = j + 4 * r;
-        if (c < p.rot) {
-          const bool upper = p.interleaved ? (c & 1) != 0 : c >= half;
-          const int i = p.interleaved ? c >> 1 : (upper ? c - half : c);
-          const int pc = p.interleaved ? c ^ 1 : (upper ? c - half : c + half);
-          const float* row = p.cos_sin + static_cast<int64_t>(ps[axis_of(p, i)]) * p.rot;
-          const float cs = __ldg(row + i), sn = __ldg(row + half + i);
-          const float o = Elem<DT>::get(__ldg(krow + pc));
-          x[r] = upper ? __fadd_rn(__fmul_rn(x[r], cs), __fmul_rn(o, sn)) : __fsub_rn(__fmul_rn(x[r], cs), __fmul_rn(o, sn));
+      float* cs = s_factors[threadIdx.x >> 5][0];
+      float* sn = s_factors[threadIdx.x >> 5][1];
+      // lane (tau, j) brings the pairs j, j + 4, ... of token tau
+      if (on) {
+        #pragma unroll 4
+        for (int i = j; i < half; i += 4) {
+          const float* row = factor_row(p, ps, i);
+          cs[tau * kFactorRow + i] = __ldg(row + i);
+          sn[tau * kFactorRow + i] = __ldg(row + half + i);
         }
+      }
+      __syncwarp();
+      cs += tau * kFactorRow;
+      sn += tau * kFactorRow;
+      if (p.interleaved) {  // the partner of channel c is c ^ 1, lane j ^ 1
+        #pragma unroll
+        for (int r = 0; r < 32; ++r) {
+          if (4 * r >= p.rot) break;  // rot is a multiple of 8
+          const float o = __shfl_xor_sync(kFull, x[r], 1);
+          const int i = (j >> 1) + 2 * r;
+          const float a = __fmul_rn(x[r], cs[i]), b = __fmul_rn(o, sn[i]);
+          x[r] = (j & 1) ? __fadd_rn(a, b) : __fsub_rn(a, b);
+        }
+      } else if (half == 64) {
+        rope_in_lane<16>(x, cs, sn, j);
+      } else if (half == 32) {
+        rope_in_lane<8>(x, cs, sn, j);
+      } else if (half == 16) {
+        rope_in_lane<4>(x, cs, sn, j);
+      } else if (half == 48) {
+        rope_in_lane<12>(x, cs, sn, j);
+      } else if (on) {  // other widths: the partner is read again
+        #pragma unroll
+        for (int r = 0; r < 32; ++r) {
+          const int c = j + 4 * r;
+          if (c < p.rot) {
+            const bool upper = c >= half;
+            const int i = upper ? c - half : c;
+            const float o = Elem<DT>::get(__ldg(krow + (upper ? c - half : c + half)));
+            const float a = __fmul_rn(x[r], cs[i]), b = __fmul_rn(o, sn[i]);
+            x[r] = upper ? __fadd_rn(a, b) : __fsub_rn(a, b);
+          }
+        }
+      }
+      if (!on) {  // a place without a token: nothing of it is kept, but it takes part in the exchanges
+        #pragma unroll
+        for (int r = 0; r < 32; ++r) x[r] = 0.0f;
       }
     }
     bool fin = true;
@@ -416,15 +531,6 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
   if (lane == 0 && flags && p.c.status) atomicOr(p.c.status, flags);
 }
 
-// Queries of a prefill: one warp per row.
-__global__ void __launch_bounds__(256) paged_query_kernel(const PagedAppendParams p) {
-  pdl_wait();
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t t = r / p.Hq;
-  if (t >= p.T || t >= __ldg(p.cu + p.B)) return;
-  query_row(p, t, static_cast<int>(r - t * p.Hq));
-}
-
 }  // namespace paged
 }  // namespace kv1b
 
@@ -435,14 +541,16 @@ cudaError_t kv1b_launch_paged_append(const PagedAppendParams& p, cudaStream_t st
     const int64_t units = 2LL * p.groups * p.c.Hkv + (p.q ? static_cast<int64_t>(p.T) * p.Hq : 0);
     return launch_pdl(paged::paged_append_token_kernel, dim3(static_cast<unsigned>((units + 3) / 4)), dim3(128), 0, stream, p);
   }
-  const dim3 grid((p.groups + 3) / 4, p.c.Hkv);
-  cudaError_t e;
+  const int64_t kv_blocks = static_cast<int64_t>((p.groups + paged::kPrefillGroupsPerBlock - 1) / paged::kPrefillGroupsPerBlock) * p.c.Hkv;
+  const int64_t units = p.q ? static_cast<int64_t>(p.T) * ((p.Hq + paged::kQueryHeads - 1) / paged::kQueryHeads) : 0;
+  const int64_t blocks = kv_blocks + (units + 3) / 4;
+  const dim3 grid(static_cast<unsigned>(blocks));
   switch (p.dtype) {
-    case KV1B_DTYPE_F32: e = launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_F32>, grid, dim3(128), 0, stream, p); break;
-    case KV1B_DTYPE_BF16: e = launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_BF16>, grid, dim3(128), 0, stream, p); break;
-    default: e = launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_F16>, grid, dim3(128), 0, stream, p); break;
+    case KV1B_DTYPE_F32:
+      return launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_F32>, grid, dim3(128), 0, stream, p, kv_blocks);
+    case KV1B_DTYPE_BF16:
+      return launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_BF16>, grid, dim3(128), 0, stream, p, kv_blocks);
+    default:
+      return launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_F16>, grid, dim3(128), 0, stream, p, kv_blocks);
   }
-  if (e != cudaSuccess || !p.q) return e;
-  const int64_t rows = static_cast<int64_t>(p.T) * p.Hq;
-  return launch_pdl(paged::paged_query_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p);
 }
