@@ -13,6 +13,7 @@
 #include "kv1b_device.cuh"
 #include "kv1b_encode_q4.cuh"
 #include "kv1b_paged.h"
+#include "kv1b_paged_device.cuh"
 
 namespace kv1b {
 namespace paged {
@@ -134,16 +135,44 @@ __device__ __forceinline__ void rope_warp(const PagedAppendParams& p, const int 
   }
 }
 
-// Query rows [h0, h1) of token t by the calling warp, lane l channels 4l .. 4l + 3 of each: the token's
-// factors are read once for all of them, eight rows are in flight.
+// Two channels of a row: as they lie in memory, as fp32, and back.
+template <int DT> struct Two { typedef uint32_t Raw; };
+template <> struct Two<KV1B_DTYPE_F32> { typedef float2 Raw; };
+__device__ __forceinline__ float2 as_floats(float2 raw, int) { return raw; }
+__device__ __forceinline__ float2 as_floats(uint32_t raw, int dtype) {
+  if (dtype == KV1B_DTYPE_BF16) return make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&raw));
+}
+template <int DT>
+__device__ __forceinline__ void store2(typename Elem<DT>::T* at, float2 v) {
+  if (DT == KV1B_DTYPE_F32) {
+    *reinterpret_cast<float2*>(at) = v;
+  } else if (DT == KV1B_DTYPE_BF16) {
+    *reinterpret_cast<__nv_bfloat162*>(at) = __floats2bfloat162_rn(v.x, v.y);
+  } else {
+    *reinterpret_cast<__half2*>(at) = __floats2half2_rn(v.x, v.y);
+  }
+}
+
+// a b for two pairs, each product rounded by itself.  (The assembler joins a product of pairs with a sum of
+// pairs behind it into one fma, also where both say .rn; it leaves single products alone.)
+__device__ __forceinline__ uint64_t products(uint64_t a, uint64_t b) {
+  float a0, a1, b0, b1;
+  unpair(a, a0, a1);
+  unpair(b, b0, b1);
+  return pair(__fmul_rn(a0, b0), __fmul_rn(a1, b1));
+}
+
+// Query rows [h0, h1) of token t by the calling warp.  A lane holds two pairs of each row, so that nothing is
+// exchanged (channels a, a + 1 and b, b + 1: a row's pairs in order, then what is not turned); the token's
+// factors are read once for all rows, eight of which are in flight.
 template <int DT>
 __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t, int h0, int h1) {
   typedef typename Elem<DT>::T E;
-  const int lane = threadIdx.x & 31, half = p.rot >> 1, c0 = 4 * lane;
-  const bool in = p.cos_sin && c0 < p.rot;
-  const bool upper = !p.interleaved && c0 >= half;
-  const int src = in && !p.interleaved ? (upper ? lane - (half >> 2) : lane + (half >> 2)) : lane;
-  float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of the channels' pairs
+  const int lane = threadIdx.x & 31, half = p.rot >> 1, first = 2 * lane;  // pairs first, first + 1
+  const bool in = p.cos_sin && first < half;
+  int a = 4 * lane, b = a + 2;
+  uint64_t cs = 0, sn = 0, ns = 0;  // cos, sin, -sin of the two pairs
   if (p.cos_sin) {
     int ps[3];
     if (!positions(p, t, ps)) {
@@ -151,35 +180,47 @@ __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t
       return;
     }
     if (in) {
-      #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = p.interleaved ? (c0 + r) >> 1 : c0 + r - (upper ? half : 0);
-        const float* row = factor_row(p, ps, i);
-        cs[r] = __ldg(row + i);
-        sn[r] = __ldg(row + half + i);
-      }
+      if (!p.interleaved) a = first, b = first + half;
+      const float* r0 = factor_row(p, ps, first) + first;
+      const float* r1 = factor_row(p, ps, first + 1) + first + 1;
+      cs = pair(__ldg(r0), __ldg(r1));
+      const float s0 = __ldg(r0 + half), s1 = __ldg(r1 + half);
+      sn = pair(s0, s1);
+      ns = pair(-s0, -s1);
     }
   }
-  const E* q = static_cast<const E*>(p.q) + t * p.q_st + c0;
-  E* out = static_cast<E*>(p.q_out) + t * p.qo_st + c0;
+  const E* q = static_cast<const E*>(p.q) + t * p.q_st;
+  E* out = static_cast<E*>(p.q_out) + t * p.qo_st;
   constexpr int kRows = 8;
+  typedef typename Two<DT>::Raw Raw;
   #pragma unroll 1
   for (int h = h0; h < h1; h += kRows) {
-    float x[kRows][4];
+    Raw ra[kRows], rb[kRows];
     #pragma unroll
-    for (int k = 0; k < kRows; ++k)
-      if (h + k < h1) load4(q, (h + k) * p.q_sh, DT, x[k]);
+    for (int k = 0; k < kRows; ++k) {  // behind the last row: it again
+      const E* row = q + min(h + k, h1 - 1) * p.q_sh;
+      ra[k] = *reinterpret_cast<const Raw*>(row + a);
+      rb[k] = *reinterpret_cast<const Raw*>(row + b);
+    }
     #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       if (h + k >= h1) break;
-      float y[4];
-      #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float o = p.interleaved ? x[k][r ^ 1] : __shfl_sync(kFull, x[k][r], src);
-        const float a = __fmul_rn(x[k][r], cs[r]), b = __fmul_rn(o, sn[r]);
-        y[r] = in ? ((p.interleaved ? (r & 1) != 0 : upper) ? __fadd_rn(a, b) : __fsub_rn(a, b)) : x[k][r];
+      float2 x = as_floats(ra[k], DT), y = as_floats(rb[k], DT);
+      if (in) {
+        // the pairs' first and second members
+        const uint64_t u = p.interleaved ? pair(x.x, y.x) : pair(x.x, x.y);
+        const uint64_t v = p.interleaved ? pair(x.y, y.y) : pair(y.x, y.y);
+        const uint64_t un = add2(products(u, cs), products(v, ns)), vn = add2(products(v, cs), products(u, sn));
+        if (p.interleaved) {
+          unpair(un, x.x, y.x);
+          unpair(vn, x.y, y.y);
+        } else {
+          unpair(un, x.x, x.y);
+          unpair(vn, y.x, y.y);
+        }
       }
-      store4(out, (h + k) * p.qo_sh, DT, y);
+      store2<DT>(out + (h + k) * p.qo_sh + a, x);
+      store2<DT>(out + (h + k) * p.qo_sh + b, y);
     }
   }
 }
@@ -325,9 +366,9 @@ __global__ void __launch_bounds__(128) paged_append_token_kernel(const PagedAppe
 
 // ---------------------------------------------------------------------------------------------
 // Prefill form: one warp per (group, kv-head), 4 lanes per token (kv1b_encode_q4.cuh).  The group's rotary
-// factors are staged per warp in shared memory, [token][pair], rows kFactorRow apart so that the 8 x 4
-// lanes read 32 banks.
-constexpr int kFactorRow = 68;  // kD / 2 + 4
+// factors are staged per warp in shared memory, a row per token (cos, then sin), kFactorRow apart so that the
+// 8 x 4 lanes read 32 banks.
+constexpr int kFactorRow = kD + 4;
 constexpr int kPrefillGroupsPerBlock = 4;
 constexpr int kQueryHeads = 32;  // query rows of a token that a warp turns
 
@@ -342,10 +383,99 @@ __device__ __forceinline__ void rope_in_lane(float (&x)[32], const float* cs, co
   }
 }
 
+// rotate_q4 (kv1b_encode_q4.cuh) with the butterflies that join two registers done for two of them at once:
+// the same sums and differences, a - c as fma(-1, c, a).
+__device__ __forceinline__ void rotate_pairs(float (&x)[32], uint32_t smask, int j) {
+  #pragma unroll
+  for (int r = 0; r < 32; ++r)  // D: flip the sign bit where the mask has a 1
+    x[r] = __int_as_float(__float_as_int(x[r]) ^ static_cast<int>((smask << (31 - r)) & 0x80000000u));
+  #pragma unroll
+  for (int h = 1; h <= 2; h <<= 1) {
+    const float sgn = (j & h) ? -1.0f : 1.0f;  // the lane of the pair's upper element forms a - c
+    const uint64_t s2 = pair(sgn, sgn);
+    #pragma unroll
+    for (int r = 0; r < 32; r += 2)
+      unpair(fma2(s2, pair(x[r], x[r + 1]), pair(__shfl_xor_sync(kFull, x[r], h), __shfl_xor_sync(kFull, x[r + 1], h))), x[r], x[r + 1]);
+  }
+  #pragma unroll
+  for (int r = 0; r < 32; r += 2) {
+    const float a = x[r], c = x[r + 1];
+    x[r] = __fadd_rn(a, c);
+    x[r + 1] = __fsub_rn(a, c);
+  }
+  const uint64_t minus = pair(-1.0f, -1.0f);
+  #pragma unroll
+  for (int hr = 2; hr <= 16; hr <<= 1) {
+    #pragma unroll
+    for (int r = 0; r < 32; r += 2) {
+      if (r & hr) continue;
+      const uint64_t a = pair(x[r], x[r + 1]), c = pair(x[r + hr], x[r + hr + 1]);
+      unpair(add2(a, c), x[r], x[r + 1]);
+      unpair(fma2(minus, c, a), x[r + hr], x[r + hr + 1]);
+    }
+  }
+}
+
+// tree_sum_q4 of the squares.
+__device__ __forceinline__ float square_sum_pairs(const float (&x)[32]) {
+  uint64_t a[16];
+  #pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = products(pair(x[2 * i], x[2 * i + 1]), pair(x[2 * i], x[2 * i + 1]));
+  #pragma unroll
+  for (int n = 8; n >= 1; n >>= 1)
+    #pragma unroll
+    for (int i = 0; i < n; ++i) a[i] = add2(a[i], a[i + n]);
+  float s0, s1;
+  unpair(a[0], s0, s1);
+  float s = __fadd_rn(s0, s1);
+  s = __fadd_rn(s, __shfl_xor_sync(kFull, s, 2));  // h = 2: lanes j < 2 add lane j + 2
+  s = __fadd_rn(s, __shfl_xor_sync(kFull, s, 1));  // h = 1: lane 0 adds lane 1
+  return __shfl_sync(kFull, s, (threadIdx.x & 31) & ~3);
+}
+
+// The token's word j of bits x >= 0 from its four lanes: each lane shifts its 32 sign bits into a mask, spreads
+// a byte of it (channels j, j + 4, .. of a word) to every fourth bit, and the four lanes swap.
+__device__ __forceinline__ uint32_t sign_word(const float (&x)[32], int j) {
+  uint32_t m = 0u;  // bit r: x[r] negative
+  #pragma unroll
+  for (int r = 30; r >= 0; r -= 2) {
+    float a, b;
+    unpair(add2(pair(x[r], x[r + 1]), pair(0.0f, 0.0f)), a, b);  // -0 counts as >= 0
+    m = __funnelshift_l(__float_as_uint(b), m, 1);
+    m = __funnelshift_l(__float_as_uint(a), m, 1);
+  }
+  m = ~m;
+  uint32_t w[4];  // this lane's bits of the token's words
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t v = (m >> (8 * i)) & 0xFFu;
+    v = (v | (v << 12)) & 0x000F000Fu;
+    v = (v | (v << 6)) & 0x03030303u;
+    v = (v | (v << 3)) & 0x11111111u;
+    w[i] = v << j;
+  }
+  // lanes j and j ^ 2 share words 0, 1 against 2, 3; then j and j ^ 1
+  const bool up = (j & 2) != 0, odd = (j & 1) != 0;
+  const uint32_t k0 = (up ? w[2] : w[0]) | __shfl_xor_sync(kFull, up ? w[0] : w[2], 2);
+  const uint32_t k1 = (up ? w[3] : w[1]) | __shfl_xor_sync(kFull, up ? w[1] : w[3], 2);
+  return (odd ? k1 : k0) | __shfl_xor_sync(kFull, odd ? k0 : k1, 1);
+}
+
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int DT>
 __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAppendParams p, const int64_t kv_blocks) {
   typedef typename Elem<DT>::T T;
-  __shared__ float s_factors[kPrefillGroupsPerBlock][2][8 * kFactorRow];
+  __shared__ __align__(16) float s_factors[kPrefillGroupsPerBlock][8 * kFactorRow];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, tau = lane >> 2, j = lane & 3;
@@ -378,25 +508,31 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
 
   {  // ---- key: lane j holds channels j + 4 r
     const T* krow = static_cast<const T*>(p.k) + t * p.k_st + h * p.k_sh;
-    float x[32], a[32];
+    float x[32];
     #pragma unroll
     for (int r = 0; r < 32; ++r) x[r] = on ? Elem<DT>::get(__ldg(krow + j + 4 * r)) : 0.0f;
     if (p.cos_sin) {
       const int half = p.rot >> 1;
-      float* cs = s_factors[threadIdx.x >> 5][0];
-      float* sn = s_factors[threadIdx.x >> 5][1];
-      // lane (tau, j) brings the pairs j, j + 4, ... of token tau
+      float* cs = s_factors[threadIdx.x >> 5] + tau * kFactorRow;  // of token tau, brought by its four lanes
+      float* sn = cs + half;
       if (on) {
-        #pragma unroll 4
-        for (int i = j; i < half; i += 4) {
-          const float* row = factor_row(p, ps, i);
-          cs[tau * kFactorRow + i] = __ldg(row + i);
-          sn[tau * kFactorRow + i] = __ldg(row + half + i);
+        if (((p.sec0 | p.sec01) & 3) == 0) {  // four pairs behind one another are of one axis
+          #pragma unroll 4
+          for (int i = 4 * j; i < half; i += 16) {
+            const float* row = factor_row(p, ps, i) + i;
+            *reinterpret_cast<float4*>(cs + i) = __ldg(reinterpret_cast<const float4*>(row));
+            *reinterpret_cast<float4*>(sn + i) = __ldg(reinterpret_cast<const float4*>(row + half));
+          }
+        } else {
+          #pragma unroll 1
+          for (int i = j; i < half; i += 4) {
+            const float* row = factor_row(p, ps, i) + i;
+            cs[i] = __ldg(row);
+            sn[i] = __ldg(row + half);
+          }
         }
       }
       __syncwarp();
-      cs += tau * kFactorRow;
-      sn += tau * kFactorRow;
       if (p.interleaved) {  // the partner of channel c is c ^ 1, lane j ^ 1
         #pragma unroll
         for (int r = 0; r < 32; ++r) {
@@ -432,25 +568,30 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
         for (int r = 0; r < 32; ++r) x[r] = 0.0f;
       }
     }
+    const float squares = square_sum_pairs(x);
+    const float nrm = __fsqrt_rn(squares);
     bool fin = true;
-    #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      fin &= isfinite(x[r]);
-      a[r] = __fmul_rn(x[r], x[r]);
+    if (!isfinite(squares)) {  // an entry is not finite, or its square is not
+      #pragma unroll
+      for (int r = 0; r < 32; ++r) fin &= isfinite(x[r]);
+      flags |= fin ? 0 : KV1B_STATUS_NONFINITE;
     }
-    flags |= fin ? 0 : KV1B_STATUS_NONFINITE;
-    const float nrm = __fsqrt_rn(tree_sum_q4(a));
     const float f0 = p.c.signs[0], f1 = p.c.signs[kD], f2 = p.c.signs[2 * kD];
     const int rounds = f0 == 0.0f ? 0 : (f1 == 0.0f ? 1 : (f2 == 0.0f ? 2 : 3));
     #pragma unroll 1
-    for (int rd = 0; rd < rounds; ++rd) rotate_q4(x, sign_mask(p.c.signs, rd, j), j);
-    uint32_t word = 0u;
-    #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      const uint32_t bal = __ballot_sync(kFull, x[r] >= 0.0f);
-      if ((r >> 3) == j) word |= ((bal >> (4 * tau)) & 0xFu) << (4 * (r & 7));
-      a[r] = fabsf(x[r]);
+    for (int rd = 0; rd < rounds; ++rd) rotate_pairs(x, sign_mask(p.c.signs, rd, j), j);
+    uint32_t word = sign_word(x, j);
+    if (__any_sync(kFull, !isfinite(squares))) {  // NaN is not >= 0, whatever its sign bit
+      word = 0u;
+      #pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const uint32_t bal = __ballot_sync(kFull, x[r] >= 0.0f);
+        if ((r >> 3) == j) word |= ((bal >> (4 * tau)) & 0xFu) << (4 * (r & 7));
+      }
     }
+    float a[32];
+    #pragma unroll
+    for (int r = 0; r < 32; ++r) a[r] = fabsf(x[r]);
     const float sabs = tree_sum_q4(a);
     const float cinv = (sabs > 0.0f) ? __fdiv_rn(__fmul_rn(static_cast<float>(kD), nrm), sabs) : 1.0f;
     if (on) {
@@ -467,31 +608,45 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
     if (on) load4(p.v, t * p.v_st + h * p.v_sh + 32 * j + 4 * q, DT, v + 4 * q);
     else v[4 * q] = v[4 * q + 1] = v[4 * q + 2] = v[4 * q + 3] = 0.0f;
   }
-  float mn = INFINITY, mx = -INFINITY;
-  bool fin = true, big = false;
+  float mn = v[0], mx = v[0];  // NaN if one of them is
   #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    fin &= isfinite(v[i]);
-    big |= fabsf(v[i]) > kF16Max;
-    v[i] = limit_value(v[i]);
-    mn = fminf(mn, v[i]);
-    mx = fmaxf(mx, v[i]);
+  for (int i = 0; i < 32; i += 2) {
+    mn = min3_nan(mn, v[i], v[i + 1]);
+    mx = max3_nan(mx, v[i], v[i + 1]);
   }
-  flags |= fin ? (big ? KV1B_STATUS_FP16_SATURATED : 0) : KV1B_STATUS_NONFINITE;
+  if (!(mn >= -kF16Max && mx <= kF16Max)) {  // rare: limit the values
+    bool fin = true, big = false;
+    mn = INFINITY;
+    mx = -INFINITY;
+    #pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      fin &= isfinite(v[i]);
+      big |= fabsf(v[i]) > kF16Max;
+      v[i] = limit_value(v[i]);
+      mn = fminf(mn, v[i]);
+      mx = fmaxf(mx, v[i]);
+    }
+    flags |= fin ? (big ? KV1B_STATUS_FP16_SATURATED : 0) : KV1B_STATUS_NONFINITE;
+  }
   uint32_t sb, mb;
   group_scale(mn, mx, &sb, &mb, false);
   const float sf = __half2float(__ushort_as_half(static_cast<unsigned short>(sb)));
   const float mf = __half2float(__ushort_as_half(static_cast<unsigned short>(mb)));
   const float rs = __frcp_rn(sf);
+  const uint64_t sf2 = pair(-sf, -sf), rs2 = pair(rs, rs), mf2 = pair(-mf, -mf), half2 = pair(0.5f, 0.5f);
   uint32_t cw[4];  // token-major: nibble i of word k = channel 32 j + 8 k + i of this token
   #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint32_t w = 0u - kMagicPacked;
     #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = __fadd_rn(div_markstein(__fsub_rn(v[8 * k + i], mf), sf, rs), 0.5f);
-      const float c = fminf(fmaxf(y, 0.0f), 15.5f);
-      w += __float_as_uint(__fadd_rd(c, 8388608.0f)) << (4 * i);
+    for (int i = 0; i < 8; i += 2) {
+      // div_markstein for two: q0 + (x - s q0) / s; x >= 0, the group's least value rounded down
+      const uint64_t x = add2(pair(v[8 * k + i], v[8 * k + i + 1]), mf2);
+      const uint64_t q0 = mul2(x, rs2);
+      float y0, y1;
+      unpair(add2(fma2(fma2(sf2, q0, x), rs2, q0), half2), y0, y1);
+      w += __float_as_uint(__fadd_rd(fminf(y0, 15.5f), 8388608.0f)) << (4 * i);
+      w += __float_as_uint(__fadd_rd(fminf(y1, 15.5f), 8388608.0f)) << (4 * i + 4);
     }
     cw[k] = (on && sf > 0.0f) ? w : 0u;
   }
