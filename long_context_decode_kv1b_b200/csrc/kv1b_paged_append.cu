@@ -365,12 +365,38 @@ __global__ void __launch_bounds__(128) paged_append_token_kernel(const PagedAppe
 }
 
 // ---------------------------------------------------------------------------------------------
-// Prefill form: one warp per (group, kv-head), 4 lanes per token (kv1b_encode_q4.cuh).  The group's rotary
-// factors are staged per warp in shared memory, a row per token (cos, then sin), kFactorRow apart so that the
-// 8 x 4 lanes read 32 banks.
+// Prefill form: one warp per group and a few kv-heads, one after another, 4 lanes per token
+// (kv1b_encode_q4.cuh).  The rows of the next head are copied to shared memory while this one's are worked on:
+// the key's as soon as its values are in registers, the value's likewise (loads into registers instead, with
+// 20 warps an SM and nothing ahead of them, left the issue slots idle for a third of the time).  The group's
+// rotary factors are staged too, a row per token (cos, then sin).
+// Rows lie so far apart that lanes (token, part) read 32 banks: keys one element at a time, values 8
+// channels at a time, part j beginning with its j-th eight.
 constexpr int kFactorRow = kD + 4;
-constexpr int kPrefillGroupsPerBlock = 4;
 constexpr int kQueryHeads = 32;  // query rows of a token that a warp turns
+template <int DT> struct Prefill {
+  static constexpr int kEs = DT == KV1B_DTYPE_F32 ? 4 : 2;
+  static constexpr int kWarps = DT == KV1B_DTYPE_F32 ? 2 : 4;
+  static constexpr int kKeyRow = kD * kEs + (DT == KV1B_DTYPE_F32 ? 16 : 8);
+  static constexpr int kValueRow = kD * kEs + 16;
+  static constexpr int kStage = 8 * (kKeyRow + kValueRow);  // bytes per warp
+};
+
+// Rows of a group's eight tokens (row i where bit i of `on` is set, zeros elsewhere) to shared memory; `first`:
+// the first of them that is set.
+template <int BYTES>
+__device__ __forceinline__ void copy_rows(uint32_t dst, int row_bytes, const uint8_t* first, int64_t stride, uint32_t on) {
+  const int lane = threadIdx.x & 31, skip = __ffs(on) - 1;
+  #pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t d = dst + i * row_bytes + lane * BYTES;
+    const bool is = (on >> i) & 1u;
+    const uint8_t* s = first + (is ? (i - skip) * stride : 0) + lane * BYTES;
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(s), "r"(is ? 16 : 0) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(s), "r"(is ? 8 : 0) : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 
 // Half-split pairs (c, c + 4 HQ) both sit in the lane: x[r] and x[r + HQ].
 template <int HQ>
@@ -473,26 +499,31 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAppendParams p, const int64_t kv_blocks) {
+__global__ void __launch_bounds__(32 * Prefill<DT>::kWarps, 20 / Prefill<DT>::kWarps) paged_append_prefill_kernel(const PagedAppendParams p, const int64_t kv_blocks,
+                                                                                       const int heads_per_warp) {
   typedef typename Elem<DT>::T T;
-  __shared__ __align__(16) float s_factors[kPrefillGroupsPerBlock][8 * kFactorRow];
+  typedef Prefill<DT> F;
+  __shared__ __align__(16) uint8_t s_rows[F::kWarps][F::kStage];
+  __shared__ __align__(16) float s_factors[F::kWarps][8 * kFactorRow];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, tau = lane >> 2, j = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tau = lane >> 2, j = lane & 3;
   // Blocks of keys and values, which are bound by their instructions, and blocks of queries, by memory,
   // are spread evenly among one another: both kinds run on every SM at all times.
   const int64_t u = blockIdx.x, kv0 = u * kv_blocks / gridDim.x;
   if ((u + 1) * kv_blocks / gridDim.x == kv0) {
     const int chunks = (p.Hq + kQueryHeads - 1) / kQueryHeads;
-    const int64_t unit = (u - kv0) * 4 + (threadIdx.x >> 5), t = unit / chunks;
+    const int64_t unit = (u - kv0) * F::kWarps + warp, t = unit / chunks;
     if (t >= p.T || t >= __ldg(p.cu + p.B)) return;
     const int h0 = static_cast<int>(unit - t * chunks) * kQueryHeads;
     query_rows<DT>(p, t, h0, min(h0 + kQueryHeads, p.Hq));
     return;
   }
-  const int gi = static_cast<int>(kv0 / p.c.Hkv) * kPrefillGroupsPerBlock + (threadIdx.x >> 5);
+  const int head_chunks = (p.c.Hkv + heads_per_warp - 1) / heads_per_warp;
+  const int gi = static_cast<int>(kv0 / head_chunks) * F::kWarps + warp;
   if (gi >= p.groups) return;
-  const int h = static_cast<int>(kv0 % p.c.Hkv);
+  int h = static_cast<int>(kv0 % head_chunks) * heads_per_warp;
+  const int h_end = min(h + heads_per_warp, p.c.Hkv);
   const Group g = find_group(p, gi);
   if (!g.any) return;
   const int64_t pos = g.g0 + tau;
@@ -505,34 +536,65 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
   if (on && p.cos_sin) on = positions(p, t, ps);
   if (is_new && !on) flags |= KV1B_STATUS_BAD_INDEX;
   const int tok = static_cast<int>(pos & 31);
+  const uint32_t onb = __ballot_sync(kFull, on && j == 0);  // bit 4 tau
+  if (onb == 0u) {
+    flags = static_cast<int>(__reduce_or_sync(kFull, static_cast<unsigned>(flags)));
+    if (lane == 0 && flags && p.c.status) atomicOr(p.c.status, flags);
+    return;
+  }
+  uint32_t on8 = 0u, keep = 0xFFFFFFFFu;  // bit per token; nibbles of a code word whose tokens are not written
+  #pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (onb & (1u << (4 * i))) {
+      on8 |= 1u << i;
+      keep &= ~(0xFu << (4 * ((i >> 1) + 4 * (i & 1))));
+    }
 
+  const uint32_t rows = smem_u32(s_rows[warp]);
+  const int64_t t0 = g.row0 + (g.g0 - g.L0) + (__ffs(on8) - 1);  // the first written token
+  auto copy_keys = [&](int hh) {
+    copy_rows<4 * F::kEs>(rows, F::kKeyRow, static_cast<const uint8_t*>(p.k) + (t0 * p.k_st + hh * p.k_sh) * F::kEs, p.k_st * F::kEs, on8);
+  };
+  auto copy_values = [&](int hh) {
+    copy_rows<4 * F::kEs>(rows + 8 * F::kKeyRow, F::kValueRow, static_cast<const uint8_t*>(p.v) + (t0 * p.v_st + hh * p.v_sh) * F::kEs,
+                          p.v_st * F::kEs, on8);
+  };
+  copy_keys(h);
+  copy_values(h);
+  const int half = p.rot >> 1;
+  float* const cs = s_factors[warp] + tau * kFactorRow;  // of token tau, brought by its four lanes
+  float* const sn = cs + half;
+  if (p.cos_sin && on) {
+    if (((p.sec0 | p.sec01) & 3) == 0) {  // four pairs behind one another are of one axis
+      #pragma unroll 4
+      for (int i = 4 * j; i < half; i += 16) {
+        const float* row = factor_row(p, ps, i) + i;
+        *reinterpret_cast<float4*>(cs + i) = __ldg(reinterpret_cast<const float4*>(row));
+        *reinterpret_cast<float4*>(sn + i) = __ldg(reinterpret_cast<const float4*>(row + half));
+      }
+    } else {
+      #pragma unroll 1
+      for (int i = j; i < half; i += 4) {
+        const float* row = factor_row(p, ps, i) + i;
+        cs[i] = __ldg(row);
+        sn[i] = __ldg(row + half);
+      }
+    }
+  }
+  const float f0 = p.c.signs[0], f1 = p.c.signs[kD], f2 = p.c.signs[2 * kD];
+  const int rounds = f0 == 0.0f ? 0 : (f1 == 0.0f ? 1 : (f2 == 0.0f ? 2 : 3));
+  const uint32_t smask0 = sign_mask(p.c.signs, 0, j);
+
+  #pragma unroll 1
+  for (; h < h_end; ++h, blk += static_cast<int64_t>(kBlkBytes) << p.c.bpp_shift) {
   {  // ---- key: lane j holds channels j + 4 r
-    const T* krow = static_cast<const T*>(p.k) + t * p.k_st + h * p.k_sh;
+    const T* krow = reinterpret_cast<const T*>(s_rows[warp] + tau * F::kKeyRow);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // the value's rows may still be under way
+    __syncwarp();
     float x[32];
     #pragma unroll
-    for (int r = 0; r < 32; ++r) x[r] = on ? Elem<DT>::get(__ldg(krow + j + 4 * r)) : 0.0f;
+    for (int r = 0; r < 32; ++r) x[r] = Elem<DT>::get(krow[j + 4 * r]);
     if (p.cos_sin) {
-      const int half = p.rot >> 1;
-      float* cs = s_factors[threadIdx.x >> 5] + tau * kFactorRow;  // of token tau, brought by its four lanes
-      float* sn = cs + half;
-      if (on) {
-        if (((p.sec0 | p.sec01) & 3) == 0) {  // four pairs behind one another are of one axis
-          #pragma unroll 4
-          for (int i = 4 * j; i < half; i += 16) {
-            const float* row = factor_row(p, ps, i) + i;
-            *reinterpret_cast<float4*>(cs + i) = __ldg(reinterpret_cast<const float4*>(row));
-            *reinterpret_cast<float4*>(sn + i) = __ldg(reinterpret_cast<const float4*>(row + half));
-          }
-        } else {
-          #pragma unroll 1
-          for (int i = j; i < half; i += 4) {
-            const float* row = factor_row(p, ps, i) + i;
-            cs[i] = __ldg(row);
-            sn[i] = __ldg(row + half);
-          }
-        }
-      }
-      __syncwarp();
       if (p.interleaved) {  // the partner of channel c is c ^ 1, lane j ^ 1
         #pragma unroll
         for (int r = 0; r < 32; ++r) {
@@ -557,7 +619,7 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
           if (c < p.rot) {
             const bool upper = c >= half;
             const int i = upper ? c - half : c;
-            const float o = Elem<DT>::get(__ldg(krow + (upper ? c - half : c + half)));
+            const float o = Elem<DT>::get(krow[upper ? c - half : c + half]);
             const float a = __fmul_rn(x[r], cs[i]), b = __fmul_rn(o, sn[i]);
             x[r] = upper ? __fadd_rn(a, b) : __fsub_rn(a, b);
           }
@@ -568,6 +630,9 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
         for (int r = 0; r < 32; ++r) x[r] = 0.0f;
       }
     }
+    __syncwarp();
+    if (h + 1 < h_end) copy_keys(h + 1);
+    else asm volatile("cp.async.commit_group;" ::: "memory");
     const float squares = square_sum_pairs(x);
     const float nrm = __fsqrt_rn(squares);
     bool fin = true;
@@ -576,10 +641,8 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
       for (int r = 0; r < 32; ++r) fin &= isfinite(x[r]);
       flags |= fin ? 0 : KV1B_STATUS_NONFINITE;
     }
-    const float f0 = p.c.signs[0], f1 = p.c.signs[kD], f2 = p.c.signs[2 * kD];
-    const int rounds = f0 == 0.0f ? 0 : (f1 == 0.0f ? 1 : (f2 == 0.0f ? 2 : 3));
     #pragma unroll 1
-    for (int rd = 0; rd < rounds; ++rd) rotate_pairs(x, sign_mask(p.c.signs, rd, j), j);
+    for (int rd = 0; rd < rounds; ++rd) rotate_pairs(x, rd == 0 ? smask0 : sign_mask(p.c.signs, rd, j), j);
     uint32_t word = sign_word(x, j);
     if (__any_sync(kFull, !isfinite(squares))) {  // NaN is not >= 0, whatever its sign bit
       word = 0u;
@@ -601,13 +664,35 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
     }
   }
 
-  // ---- value: lane j holds group j
+  // ---- value: lane j holds group j, its eights i ^ j
   float v[32];
-  #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    if (on) load4(p.v, t * p.v_st + h * p.v_sh + 32 * j + 4 * q, DT, v + 4 * q);
-    else v[4 * q] = v[4 * q + 1] = v[4 * q + 2] = v[4 * q + 3] = 0.0f;
+  asm volatile("cp.async.wait_group 1;" ::: "memory");  // the next key's rows may still be under way
+  __syncwarp();
+  {
+    const uint8_t* vrow = s_rows[warp] + 8 * F::kKeyRow + tau * F::kValueRow + 32 * j * F::kEs;
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4* at = reinterpret_cast<const uint4*>(vrow + (q ^ j) * 8 * F::kEs);
+      const uint4 w0 = at[0];
+      if (DT == KV1B_DTYPE_F32) {
+        const uint4 w1 = at[1];
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * q + i] = __uint_as_float(w[i]);
+      } else {
+        const uint32_t w[4] = {w0.x, w0.y, w0.z, w0.w};
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = as_floats(w[i], DT);
+          v[8 * q + 2 * i] = f.x;
+          v[8 * q + 2 * i + 1] = f.y;
+        }
+      }
+    }
   }
+  __syncwarp();
+  if (h + 1 < h_end) copy_values(h + 1);
+  else asm volatile("cp.async.commit_group;" ::: "memory");
   float mn = v[0], mx = v[0];  // NaN if one of them is
   #pragma unroll
   for (int i = 0; i < 32; i += 2) {
@@ -634,7 +719,7 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
   const float mf = __half2float(__ushort_as_half(static_cast<unsigned short>(mb)));
   const float rs = __frcp_rn(sf);
   const uint64_t sf2 = pair(-sf, -sf), rs2 = pair(rs, rs), mf2 = pair(-mf, -mf), half2 = pair(0.5f, 0.5f);
-  uint32_t cw[4];  // token-major: nibble i of word k = channel 32 j + 8 k + i of this token
+  uint32_t cw[4];  // token-major: nibble i of word k = channel 32 j + 8 (k ^ j) + i of this token
   #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint32_t w = 0u - kMagicPacked;
@@ -671,16 +756,14 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
     x ^= s1 ^ (s1 << 8);
     cw[k] = x;
   }
-  // the mask of nibbles whose tokens were written, in the same order
-  const uint32_t onb = __ballot_sync(kFull, on && j == 0);  // bit 4 tau
-  uint32_t keep = 0xFFFFFFFFu;
-  #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (onb & (1u << (4 * i))) keep &= ~(0xFu << (4 * ((i >> 1) + 4 * (i & 1))));
-  if (blk && keep != 0xFFFFFFFFu) {
+  {
     uint32_t* dst = reinterpret_cast<uint32_t*>(blk + kBlkOffCodes) + (32 * j + tau) * 4 + (static_cast<int>(g.g0 & 31) >> 3);
     #pragma unroll
-    for (int k = 0; k < 4; ++k) dst[8 * 4 * k] = keep ? ((dst[8 * 4 * k] & keep) | (cw[k] & ~keep)) : cw[k];
+    for (int k = 0; k < 4; ++k) {
+      uint32_t* at = dst + 8 * 4 * (k ^ j);
+      *at = keep ? ((*at & keep) | (cw[k] & ~keep)) : cw[k];
+    }
+  }
   }
   flags = static_cast<int>(__reduce_or_sync(kFull, static_cast<unsigned>(flags)));
   if (lane == 0 && flags && p.c.status) atomicOr(p.c.status, flags);
@@ -691,21 +774,26 @@ __global__ void __launch_bounds__(128) paged_append_prefill_kernel(const PagedAp
 
 using namespace kv1b;
 
+template <int DT>
+static cudaError_t launch_prefill(const PagedAppendParams& p, int heads, cudaStream_t stream) {
+  constexpr int kWarps = paged::Prefill<DT>::kWarps;
+  const int64_t kv_blocks = static_cast<int64_t>((p.groups + kWarps - 1) / kWarps) * ((p.c.Hkv + heads - 1) / heads);
+  const int64_t rows = p.q ? static_cast<int64_t>(p.T) * ((p.Hq + paged::kQueryHeads - 1) / paged::kQueryHeads) : 0;
+  const dim3 grid(static_cast<unsigned>(kv_blocks + (rows + kWarps - 1) / kWarps));
+  return launch_pdl(paged::paged_append_prefill_kernel<DT>, grid, dim3(32 * kWarps), 0, stream, p, kv_blocks, heads);
+}
+
 cudaError_t kv1b_launch_paged_append(const PagedAppendParams& p, cudaStream_t stream) {
   if (p.T <= 4 * p.B) {
     const int64_t units = 2LL * p.groups * p.c.Hkv + (p.q ? static_cast<int64_t>(p.T) * p.Hq : 0);
     return launch_pdl(paged::paged_append_token_kernel, dim3(static_cast<unsigned>((units + 3) / 4)), dim3(128), 0, stream, p);
   }
-  const int64_t kv_blocks = static_cast<int64_t>((p.groups + paged::kPrefillGroupsPerBlock - 1) / paged::kPrefillGroupsPerBlock) * p.c.Hkv;
-  const int64_t units = p.q ? static_cast<int64_t>(p.T) * ((p.Hq + paged::kQueryHeads - 1) / paged::kQueryHeads) : 0;
-  const int64_t blocks = kv_blocks + (units + 3) / 4;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  // Heads a warp takes in turn: as many as leave every SM about three rounds of warps.
+  const int64_t units = static_cast<int64_t>(p.groups) * p.c.Hkv;
+  const int heads = static_cast<int>(units / (148 * 20 * 3) < 1 ? 1 : (units / (148 * 20 * 3) > 4 ? 4 : units / (148 * 20 * 3)));
   switch (p.dtype) {
-    case KV1B_DTYPE_F32:
-      return launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_F32>, grid, dim3(128), 0, stream, p, kv_blocks);
-    case KV1B_DTYPE_BF16:
-      return launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_BF16>, grid, dim3(128), 0, stream, p, kv_blocks);
-    default:
-      return launch_pdl(paged::paged_append_prefill_kernel<KV1B_DTYPE_F16>, grid, dim3(128), 0, stream, p, kv_blocks);
+    case KV1B_DTYPE_F32: return launch_prefill<KV1B_DTYPE_F32>(p, heads, stream);
+    case KV1B_DTYPE_BF16: return launch_prefill<KV1B_DTYPE_BF16>(p, heads, stream);
+    default: return launch_prefill<KV1B_DTYPE_F16>(p, heads, stream);
   }
 }
