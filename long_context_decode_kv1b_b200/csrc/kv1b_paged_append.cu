@@ -135,24 +135,32 @@ __device__ __forceinline__ void rope_warp(const PagedAppendParams& p, const int 
   }
 }
 
-// Two channels of a row: as they lie in memory, as fp32, and back.
-template <int DT> struct Two { typedef uint32_t Raw; };
-template <> struct Two<KV1B_DTYPE_F32> { typedef float2 Raw; };
-__device__ __forceinline__ float2 as_floats(float2 raw, int) { return raw; }
+// Channels of a row as they lie in memory, as fp32, and back: two from a word, four from a Four.
 __device__ __forceinline__ float2 as_floats(uint32_t raw, int dtype) {
   if (dtype == KV1B_DTYPE_BF16) return make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xFFFF0000u));
   return __half22float2(*reinterpret_cast<const __half2*>(&raw));
 }
-template <int DT>
-__device__ __forceinline__ void store2(typename Elem<DT>::T* at, float2 v) {
-  if (DT == KV1B_DTYPE_F32) {
-    *reinterpret_cast<float2*>(at) = v;
-  } else if (DT == KV1B_DTYPE_BF16) {
-    *reinterpret_cast<__nv_bfloat162*>(at) = __floats2bfloat162_rn(v.x, v.y);
-  } else {
-    *reinterpret_cast<__half2*>(at) = __floats2half2_rn(v.x, v.y);
+__device__ __forceinline__ uint32_t as_word(float a, float b, int dtype) {
+  if (dtype == KV1B_DTYPE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
   }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
+template <int DT> struct Four {
+  typedef uint2 Raw;
+  static __device__ __forceinline__ void get(Raw w, float* x) {
+    const float2 a = as_floats(w.x, DT), b = as_floats(w.y, DT);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+  }
+  static __device__ __forceinline__ Raw put(const float* x) { return make_uint2(as_word(x[0], x[1], DT), as_word(x[2], x[3], DT)); }
+};
+template <> struct Four<KV1B_DTYPE_F32> {
+  typedef float4 Raw;
+  static __device__ __forceinline__ void get(Raw w, float* x) { x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w; }
+  static __device__ __forceinline__ Raw put(const float* x) { return make_float4(x[0], x[1], x[2], x[3]); }
+};
 
 // a b for two pairs, each product rounded by itself.  (The assembler joins a product of pairs with a sum of
 // pairs behind it into one fma, also where both say .rn; it leaves single products alone.)
@@ -163,16 +171,17 @@ __device__ __forceinline__ uint64_t products(uint64_t a, uint64_t b) {
   return pair(__fmul_rn(a0, b0), __fmul_rn(a1, b1));
 }
 
-// Query rows [h0, h1) of token t by the calling warp.  A lane holds two pairs of each row, so that nothing is
-// exchanged (channels a, a + 1 and b, b + 1: a row's pairs in order, then what is not turned); the token's
-// factors are read once for all rows, eight of which are in flight.
+// Query rows [h0, h1) of token t by the calling warp, a row by 16 lanes.  A lane holds four pairs of each of
+// its rows, so that nothing is exchanged (channels a .. a + 3 and b .. b + 3: a row's pairs in order, then what
+// is not turned); the token's factors are read once for all rows, sixteen of which are in flight.
 template <int DT>
 __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t, int h0, int h1) {
   typedef typename Elem<DT>::T E;
-  const int lane = threadIdx.x & 31, half = p.rot >> 1, first = 2 * lane;  // pairs first, first + 1
+  typedef typename Four<DT>::Raw Raw;
+  const int lane = threadIdx.x & 31, half = p.rot >> 1, first = 4 * (lane & 15);  // pairs first .. first + 3
   const bool in = p.cos_sin && first < half;
-  int a = 4 * lane, b = a + 2;
-  uint64_t cs = 0, sn = 0, ns = 0;  // cos, sin, -sin of the two pairs
+  int a = 2 * first, b = a + 4;
+  float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (p.cos_sin) {
     int ps[3];
     if (!positions(p, t, ps)) {
@@ -181,46 +190,54 @@ __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t
     }
     if (in) {
       if (!p.interleaved) a = first, b = first + half;
-      const float* r0 = factor_row(p, ps, first) + first;
-      const float* r1 = factor_row(p, ps, first + 1) + first + 1;
-      cs = pair(__ldg(r0), __ldg(r1));
-      const float s0 = __ldg(r0 + half), s1 = __ldg(r1 + half);
-      sn = pair(s0, s1);
-      ns = pair(-s0, -s1);
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* row = factor_row(p, ps, first + i) + first + i;
+        cs[i] = __ldg(row);
+        sn[i] = __ldg(row + half);
+      }
     }
   }
   const E* q = static_cast<const E*>(p.q) + t * p.q_st;
   E* out = static_cast<E*>(p.q_out) + t * p.qo_st;
-  constexpr int kRows = 8;
-  typedef typename Two<DT>::Raw Raw;
+  constexpr int kSteps = 8;  // two rows each
   #pragma unroll 1
-  for (int h = h0; h < h1; h += kRows) {
-    Raw ra[kRows], rb[kRows];
+  for (int h = h0 + (lane >> 4); h < h1; h += 2 * kSteps) {
+    Raw ra[kSteps], rb[kSteps];
     #pragma unroll
-    for (int k = 0; k < kRows; ++k) {  // behind the last row: it again
-      const E* row = q + min(h + k, h1 - 1) * p.q_sh;
+    for (int k = 0; k < kSteps; ++k) {  // behind the last row: it again
+      const E* row = q + min(h + 2 * k, h1 - 1) * p.q_sh;
       ra[k] = *reinterpret_cast<const Raw*>(row + a);
       rb[k] = *reinterpret_cast<const Raw*>(row + b);
     }
     #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      if (h + k >= h1) break;
-      float2 x = as_floats(ra[k], DT), y = as_floats(rb[k], DT);
+    for (int k = 0; k < kSteps; ++k) {
+      if (h + 2 * k >= h1) break;
       if (in) {
-        // the pairs' first and second members
-        const uint64_t u = p.interleaved ? pair(x.x, y.x) : pair(x.x, x.y);
-        const uint64_t v = p.interleaved ? pair(x.y, y.y) : pair(y.x, y.y);
-        const uint64_t un = add2(products(u, cs), products(v, ns)), vn = add2(products(v, cs), products(u, sn));
+        float x[8];
+        Four<DT>::get(ra[k], x);
+        Four<DT>::get(rb[k], x + 4);
+        const uint64_t c0 = pair(cs[0], cs[1]), c1 = pair(cs[2], cs[3]);
+        const uint64_t s0 = pair(sn[0], sn[1]), s1 = pair(sn[2], sn[3]), n0 = pair(-sn[0], -sn[1]), n1 = pair(-sn[2], -sn[3]);
         if (p.interleaved) {
-          unpair(un, x.x, y.x);
-          unpair(vn, x.y, y.y);
+          const uint64_t u0 = pair(x[0], x[2]), v0 = pair(x[1], x[3]), u1 = pair(x[4], x[6]), v1 = pair(x[5], x[7]);
+          unpair(add2(products(u0, c0), products(v0, n0)), x[0], x[2]);
+          unpair(add2(products(v0, c0), products(u0, s0)), x[1], x[3]);
+          unpair(add2(products(u1, c1), products(v1, n1)), x[4], x[6]);
+          unpair(add2(products(v1, c1), products(u1, s1)), x[5], x[7]);
         } else {
-          unpair(un, x.x, x.y);
-          unpair(vn, y.x, y.y);
+          const uint64_t u0 = pair(x[0], x[1]), v0 = pair(x[4], x[5]), u1 = pair(x[2], x[3]), v1 = pair(x[6], x[7]);
+          unpair(add2(products(u0, c0), products(v0, n0)), x[0], x[1]);
+          unpair(add2(products(v0, c0), products(u0, s0)), x[4], x[5]);
+          unpair(add2(products(u1, c1), products(v1, n1)), x[2], x[3]);
+          unpair(add2(products(v1, c1), products(u1, s1)), x[6], x[7]);
         }
+        ra[k] = Four<DT>::put(x);
+        rb[k] = Four<DT>::put(x + 4);
       }
-      store2<DT>(out + (h + k) * p.qo_sh + a, x);
-      store2<DT>(out + (h + k) * p.qo_sh + b, y);
+      E* row = out + (h + 2 * k) * p.qo_sh;
+      *reinterpret_cast<Raw*>(row + a) = ra[k];
+      *reinterpret_cast<Raw*>(row + b) = rb[k];
     }
   }
 }
