@@ -131,8 +131,8 @@ struct QueryPrep {
   int32_t sq;
 };
 
-// x: the lane's four channels of the row (overwritten).
-__device__ __forceinline__ QueryPrep query_prep_values(float x[4], const float* signs) {
+// The lane's four codes of a row, its grid origin and step.  x: the lane's four channels (overwritten).
+__device__ __forceinline__ void query_quantise(float x[4], const float* signs, int code[4], float* origin, float* step) {
   rotate_rounds(x, signs);
   float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
   float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
@@ -142,8 +142,6 @@ __device__ __forceinline__ QueryPrep query_prep_values(float x[4], const float* 
     hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, m));
   }
   const float dl = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
-  int code[4];
-  int csum = 0;
   #pragma unroll
   for (int r = 0; r < 4; ++r) {
     int c = 0;
@@ -152,8 +150,16 @@ __device__ __forceinline__ QueryPrep query_prep_values(float x[4], const float* 
       c = !(fl > 0.0f) ? 0 : (fl >= 15.0f ? 15 : static_cast<int>(fl));
     }
     code[r] = c;
-    csum += c;
   }
+  *origin = lo;
+  *step = dl;
+}
+
+__device__ __forceinline__ QueryPrep query_prep_values(float x[4], const float* signs) {
+  int code[4];
+  float lo, dl;
+  query_quantise(x, signs, code, &lo, &dl);
+  const int csum = code[0] + code[1] + code[2] + code[3];
   QueryPrep qp;
   #pragma unroll
   for (int j = 0; j < 4; ++j) {

@@ -203,10 +203,6 @@ size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int3
   at += up256(rows * row);
   if (p) p->spread = reinterpret_cast<int2*>(ws + at);
   at += up256(static_cast<size_t>(Hkv) * (s->R / G) * 8);
-  s->codes = ws + at;
-  at += up256(rows * KV1B_HEAD_DIM);
-  s->factors = reinterpret_cast<float2*>(ws + at);
-  at += up256(rows * 8);
   s->pieces = reinterpret_cast<float*>(ws + at);
   return at + up256(static_cast<size_t>(Hkv) * s->row_tiles * s->splits * 256 * row);
 }

@@ -1,0 +1,582 @@
+// kv1b_paged_attend.cuh -- decode attention over a paged cache, one query token per sequence, uneven
+// lengths read on the device: one CTA's part.
+//
+// Split.  The visible 32-token blocks of all (sequence, kv-head) segments are laid end to end and cut
+// into one equal contiguous range per CTA (one CTA per SM), whatever the lengths, and a CTA's range into
+// one equal run per warp.  Each warp streams its run through its own ring of kStages shared-memory
+// buffers (one 3,200-byte bulk copy per block, an mbarrier each), so nothing waits on another warp until
+// the end.  A segment inside one run is finished by its warp; the warps' pieces of a longer one meet in
+// shared memory; one that a range boundary cuts leaves a partial row per CTA, which a second kernel
+// merges.  (One segment at a time for the whole CTA, every 16th block a warp's, cost 5 us a segment in
+// barriers and restarts: 53 us for 32 segments of 61 tokens on 4 CTAs.)
+//
+// Per block and warp (lane (g, t) = (lane / 4, lane % 4)), for up to 8 query heads g:
+//   scores   s8 m16n8k32 products: rows 0 - 7 of A are the heads' 4-bit codes, rows 8 - 15 ones, columns
+//            of B eight tokens' sign bits, one AND per register (the bit stays in place and the code
+//            carries 2^(3 - place)).  Lane (g, t) gets 8 A and 8 Bc of head g, tokens 8 t + 2 i + {0, 1}:
+//            with the row order of the block, all eight tokens of its code words, so probabilities are
+//            formed where the next product wants them and nothing is shuffled;
+//   softmax  log2 units against a reference that a warp raises only when a logit passes it by kTau;
+//   P.V      v = min + scale code, so sum p v = sum p min + sum (p scale) code.  f16 m16n8k16 products with
+//            fp32 sums: A = 16 channels x 16 tokens of codes, one AND per register (a nibble in the low
+//            mantissa bits is a binary16 subnormal, code 2^-24, or 2^-20 where the nibble is the byte's
+//            upper one: those tokens' weights are 2^-4 lower), B = p scale, one multiplication per pair of
+//            tokens and value group.  A last pair of products with the four groups' mins and a row of ones
+//            gives sum p min and the normaliser from the same binary16 p, so p's rounding cancels in the
+//            quotient.
+// Roundings: p scale is rounded to 11 bits for bf16 results, which have 8; for fp16 results its remainder
+// (exact: the product of two 11-bit numbers has 22) goes through a second set of products.  What is left is
+// the subnormal codes' own loss: the tensor cores line a product up by its operands' exponents, so the sums
+// of scale code keep some ten bits fewer than fp32's 24 (2^-14.6 of them seen).
+// Range: p = 2^(x - m + kBase) <= 2^15 and scale < 2 keep p scale finite; a block with a larger scale lowers
+// the weights by its power of two.  A weight keeps 11 bits down to 2^-21 of the reference.
+//
+// 609 warp instructions a block (values expanded to binary16 by fma, a page entry and an address per
+// block) became about 330: the issue slots were 64 % busy at 243 us for 1M tokens x 8 heads.
+#pragma once
+#include "kv1b_paged_device.cuh"
+
+namespace kv1b {
+namespace paged {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+
+constexpr int kQuerySlots = 128;  // prepared query rows a round holds
+constexpr int kMaxSegs = 64;      // segments a round holds
+
+// a segment of a round, in blocks from the round's start
+struct Seg {
+  int base, nb;  // first block (below 0 where the CTA's range begins inside the segment), blocks
+  int b, h;
+};
+
+constexpr int kOffPre = kWarps * kStages * kBlkBytes;            // u32 [kMaxSeqs + 1] blocks before each sequence
+constexpr int kOffLen = kOffPre + (kMaxSeqs + 4) * 4;            // i32 [kMaxSeqs]
+constexpr int kOffSome = kOffLen + kMaxSeqs * 4;                 // u16 [kMaxSeqs]
+constexpr int kOffSeg = kOffSome + kMaxSeqs * 2;                 // Seg [kMaxSegs]
+constexpr int kOffPlane = kOffSeg + kMaxSegs * 16;               // u32 [kQuerySlots][4 planes][4]
+constexpr int kOffConst = kOffPlane + kQuerySlots * 64;          // f32 [kQuerySlots][4]: c1, c2, c0
+constexpr int kOffRows = kOffConst + kQuerySlots * 16;           // f16 [2][8]: ones, zeros
+constexpr int kOffSigns = kOffRows + 32;                         // f32 [3][128]
+constexpr int kSmem = kOffSigns + 3 * kD * 4;
+constexpr int kOffRed = 0;                                       // f32 [kWarps][G][kRow], over the ring once it is drained
+static_assert(kOffPre % 16 == 0 && kOffRows % 16 == 0 && kWarps * KV1B_MAX_GROUP * kRow * 4 <= kOffPre && kSmem + 2048 <= 227 * 1024, "shared memory");
+
+// Block i of a segment: its place in the sequence.
+__device__ __forceinline__ int own_block(const Visible& v, int j) { return j < v.skip_from ? j : j + (v.skip_to - v.skip_from); }
+
+// The copy side's place in a round's blocks.  Stretches of blocks that lie behind one another in a page
+// are walked by a pointer; the page entry of the next stretch is loaded when one begins.
+struct Ahead {
+  const uint8_t* ptr;  // next block, null where the page is not there
+  int in;              // blocks of the stretch that are left
+  int left;            // blocks of the warp's run behind the stretch
+  int s, i;            // segment and block behind the stretch
+  int b, h, nb;
+  Visible vis;
+  int page;            // page entry there
+  __device__ __forceinline__ void enter(const Seg* seg, const Plan& pl, const PagedAttendParams& p) {
+    const Seg g = seg[s];
+    b = g.b;
+    h = g.h;
+    nb = g.nb;
+    vis = visible(pl.len[b], p.window, p.sinks);
+  }
+  __device__ __forceinline__ void look_up(const PagedAttendParams& p) {
+    page = __ldg(p.table + b * p.table_stride + (own_block(vis, i) >> p.c.bpp_shift));
+  }
+  __device__ __forceinline__ void next_stretch(const Seg* seg, const Plan& pl, const PagedAttendParams& p) {
+    const int blk = own_block(vis, i), off = blk & ((1 << p.c.bpp_shift) - 1);
+    const bool ok = page >= 0 && page < p.c.num_pages;
+    ptr = ok ? p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + h) << p.c.bpp_shift) + off) * kBlkBytes) : nullptr;
+    if (!ok && (threadIdx.x & 31) == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+    in = min(min((1 << p.c.bpp_shift) - off, nb - i), left);
+    if (i < vis.skip_from) in = min(in, vis.skip_from - i);
+    left -= in;
+    i += in;
+    if (left > 0) {
+      if (i == nb) {
+        ++s;
+        i = 0;
+        enter(seg, pl, p);
+      }
+      look_up(p);
+    }
+  }
+};
+
+// The first block from i on of which the query may see only a part: where the sinks end, where the window
+// begins (the first block of all where there is none), the last one.
+__device__ __forceinline__ int next_edge(const Visible& v, int i, int nb) {
+  return i < v.skip_from ? v.skip_from - 1 : (i == v.skip_from ? i : nb - 1);
+}
+
+constexpr float kCodeUnit = 16777216.0f;  // codes enter the products as binary16 subnormals, units of 2^-24
+
+// kFine: the weights of the codes in two binary16 parts (fp16 results); one part is enough for bf16.
+// `cta` of p.ncta, kThreads threads, kSmem bytes at `smem` (128-byte aligned).
+template <bool kFine>
+__device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int G, const int cta, uint8_t* smem) {
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint32_t* pre = reinterpret_cast<uint32_t*>(smem + kOffPre);
+  int* slen = reinterpret_cast<int*>(smem + kOffLen);
+  Seg* seg = reinterpret_cast<Seg*>(smem + kOffSeg);
+  uint32_t* planes = reinterpret_cast<uint32_t*>(smem + kOffPlane);
+  float4* consts = reinterpret_cast<float4*>(smem + kOffConst);
+  float* red = reinterpret_cast<float*>(smem + kOffRed);
+
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[warp][s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  float* signs = reinterpret_cast<float*>(smem + kOffSigns);
+  if (threadIdx.x < KV1B_MAX_ROUNDS * kD) signs[threadIdx.x] = __ldg(p.c.signs + threadIdx.x);
+  const Plan pl = make_plan<kThreads>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), p.ncta, cta == 0);
+
+  // sequences that see nothing: zeros
+  for (int b = p.rows ? p.B : cta; b < p.B; b += p.ncta)
+    if (pre[b + 1] == pre[b])
+      for (int e = threadIdx.x; e < p.Hq * kD; e += kThreads) store_out(p.out, p.q_dtype, static_cast<int64_t>(b) * p.Hq * kD + e, 0.0f);
+  if (p.rows)
+    for (int64_t i = static_cast<int64_t>(cta) * kThreads + threadIdx.x; i < static_cast<int64_t>(p.B) * pl.Hkv;
+         i += static_cast<int64_t>(p.ncta) * kThreads) {
+      const int b = static_cast<int>(i / pl.Hkv);
+      if (pre[b + 1] == pre[b]) p.spread[i] = make_int2(0, 0);
+    }
+  if (cta >= pl.n || pl.S == 0) {
+    if (threadIdx.x == 0 && !p.rows) p.spread[cta] = make_int2(0, 0);
+    return;
+  }
+
+  const int64_t r0 = pl.begin(cta), r1 = pl.begin(cta + 1);  // never empty: n is at most S
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kBlkBytes;
+  const int max_segs = min(kMaxSegs, kQuerySlots / G);
+  const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
+  float* first = p.first + (static_cast<int64_t>(cta) * kWarps + warp) * G * kRow;
+  if (threadIdx.x < 8) reinterpret_cast<uint32_t*>(smem + kOffRows)[threadIdx.x] = threadIdx.x < 4 ? 0x3C003C00u : 0u;
+  const uint32_t side_row = smem_u32(smem) + kOffRows + (g == 4 ? 0 : 16);  // rows 4 and 5 .. 7 of the side product
+  uint32_t phases = 0;  // bit s: parity of stage s's next completion
+  bool gave_up = false;
+
+  // ---- rounds of up to max_segs segments; nearly always one
+  for (int64_t a = r0; a < r1;) {
+    // the round's segments
+    int nseg;
+    {
+      int lo = 0, hi = pl.nsome;  // the sequence of block a: largest lo with Hkv pre[some[lo]] <= a
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<int64_t>(pre[pl.some[mid]]) * pl.Hkv <= a) lo = mid;
+        else hi = mid;
+      }
+      const int b0 = pl.some[lo];
+      const int h0 = static_cast<int>(quotient(a - static_cast<int64_t>(pre[b0]) * pl.Hkv, pre[b0 + 1] - pre[b0]));
+      bool valid = false;
+      if (static_cast<int>(threadIdx.x) < max_segs) {
+        const int id = h0 + threadIdx.x, k = lo + id / pl.Hkv, h = id % pl.Hkv;
+        if (k < pl.nsome) {
+          const int b = pl.some[k], nb = static_cast<int>(pre[b + 1] - pre[b]);
+          const int64_t base = static_cast<int64_t>(pre[b]) * pl.Hkv + static_cast<int64_t>(h) * nb;
+          valid = base < r1;
+          if (valid) seg[threadIdx.x] = {static_cast<int>(base - a), nb, b, h};
+        }
+      }
+      nseg = __syncthreads_count(valid);
+    }
+    const int n = static_cast<int>(min(r1 - a, static_cast<int64_t>(seg[nseg - 1].base) + seg[nseg - 1].nb));
+    const int run_q = n / kWarps, run_r = n % kWarps;  // the first run_r runs are one longer
+    auto run_begin = [&](int w) { return w * run_q + min(w, run_r); };
+    auto run_owner = [&](int x) {
+      const int longer = run_r * (run_q + 1);
+      return x < longer ? x / (run_q + 1) : run_r + (x - longer) / run_q;
+    };
+    const int w0 = run_begin(warp), w1 = run_begin(warp + 1);
+
+    // the rows of the round's queries: a warp's first two are loaded before the copies fill the memory's queues
+    auto load_row = [&](int r, float (&x)[4]) {
+      const Seg sg = seg[r / G];
+      load4(p.q, (static_cast<int64_t>(sg.b) * p.Hq + static_cast<int64_t>(sg.h) * G + r % G) * kD + 4 * lane, p.q_dtype, x);
+    };
+    float q0[4], q1[4];
+    if (warp < nseg * G) load_row(warp, q0);
+    if (warp + kWarps < nseg * G) load_row(warp + kWarps, q1);
+
+    // ---- copy side: `ahead` walks kStages blocks in front of the compute
+    Ahead ahead;
+    ahead.in = 0;
+    ahead.left = w1 - w0;
+    uint32_t absent = 0;  // bit s: stage s holds no block (its page is outside the cache)
+    auto issue = [&](int s) {
+      if (ahead.in == 0) ahead.next_stretch(seg, pl, p);
+      absent = ahead.ptr ? absent & ~(1u << s) : absent | (1u << s);
+      if (ahead.ptr) {
+        if (lane == 0) block_g2s(ring + s * kBlkBytes, ahead.ptr, &bars[warp][s]);
+        ahead.ptr += kBlkBytes;
+      }
+      --ahead.in;
+    };
+    struct { int s, i, left, b, h, nb; Visible vis; } cur = {0, 0, w1 - w0, 0, 0, 0, {0, 0, 0}};
+    if (cur.left > 0) {
+      int k = 0;  // the segment of block w0
+      for (int x = lane; x < nseg; x += 32)
+        if (seg[x].base <= w0) k = x;
+      k = __reduce_max_sync(kFull, k);
+      ahead.s = k;
+      ahead.i = w0 - seg[k].base;
+      ahead.enter(seg, pl, p);
+      ahead.look_up(p);
+      cur = {k, ahead.i, cur.left, ahead.b, ahead.h, ahead.nb, ahead.vis};
+      for (int s = 0; s < kStages && ahead.in + ahead.left > 0 && !gave_up; ++s) issue(s);
+    }
+
+    // ---- the round's queries
+    for (int r = warp; r < nseg * G; r += kWarps) {
+      if (r >= 2 * kWarps) load_row(r, q0);
+      const QueryPrep qp = query_prep_values(q0, signs);
+      #pragma unroll
+      for (int j = 0; j < 4; ++j) q0[j] = q1[j];
+      if (lane == 0) {
+        #pragma unroll
+        for (int j = 0; j < 4; ++j)
+          reinterpret_cast<uint4*>(planes)[r * 4 + j] = make_uint4(qp.planes[j][0], qp.planes[j][1], qp.planes[j][2], qp.planes[j][3]);
+        // log2 logit = (c1 8A + c2 8Bc + c0) (N/C):  delta (2A - Sq) + vl (2 Bc - 128), times scale log2(e) / 128
+        consts[r] = make_float4(__fmul_rn(0.25f * qp.delta, qs), __fmul_rn(0.25f * qp.vl, qs),
+                                -__fmul_rn(__fadd_rn(__fmul_rn(qp.delta, static_cast<float>(qp.sq)), 128.0f * qp.vl), qs), 0.0f);
+      }
+    }
+    __syncthreads();
+
+    // acc: sums of weight scale code (units of 2^-24); side: rows 0 .. 3 sums of weight min per group, row 4 of weight
+    float acc[8][4], side[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+    float m = kNoRef;  // reference of head g
+    // element (i, e, hi) of the weighted value sum of head 2 t + e, channel 16 i + g + 8 hi
+    auto value = [&](int i, int e, int hi) {
+      return __fmaf_rn(acc[i][2 * hi + e], kCodeUnit, __shfl_sync(kFull, side[e], 4 * (i >> 1) + t));
+    };
+    // the warp's sums of a segment to a piece [head][kRow]
+    auto put_piece = [&](float* w) {
+      if (t == 0 && g < G) w[g * kRow] = m;
+      #pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hd = 2 * t + e;
+        if (g == 4 && hd < G) w[hd * kRow + 1] = side[e];
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float lo = value(i, e, 0), hi = value(i, e, 1);
+          if (hd < G) {
+            w[hd * kRow + 2 + 16 * i + g] = lo;
+            w[hd * kRow + 2 + 16 * i + g + 8] = hi;
+          }
+        }
+      }
+    };
+    int stage = 0;
+    bool last = w0 == w1;  // the sums in registers are a piece that the CTA merges (an empty run's: nothing)
+    while (cur.left > 0) {
+      // A operand: k-row 4 t + j of product kb, half hi is channel 32 t + 8 j + r, r = 2 kb + hi, its code
+      // times 2^(3 - (r & 3)) (the sign bit stays at place r & 3 of its byte)
+      uint32_t aq[4][2];
+      float4 cc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      {
+        uint32_t pw[4] = {0u, 0u, 0u, 0u};
+        if (g < G) {
+          #pragma unroll
+          for (int j = 0; j < 4; ++j) pw[j] = planes[((cur.s * G + g) * 4 + j) * 4 + t];
+          cc = consts[cur.s * G + g];
+        }
+        #pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+          #pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            const int r = 2 * kb + hi;
+            uint32_t code = 0u;
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) code |= ((pw[j] >> r) & 0x01010101u) << j;
+            aq[kb][hi] = code << (3 - (r & 3));
+          }
+      }
+      const float c1 = cc.x, c2 = cc.y, c0 = cc.z;
+      #pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+      side[0] = side[1] = side[2] = side[3] = 0.0f;
+      m = 0.0f;
+      bool fresh = true;   // no block has set m
+      int top_scale = 0;   // weights are 2^-top_scale lower: no scale reaches 2^(1 + top_scale)
+      const bool starts = cur.i == 0;
+      const int count = min(cur.left, cur.nb - cur.i);  // blocks of the segment in the warp's run
+      const bool ends = cur.i + count == cur.nb;
+      int edge_at = next_edge(cur.vis, cur.i, cur.nb);
+
+      for (int x = cur.i; x < cur.i + count; ++x) {
+        const uint32_t st = ring + stage * kBlkBytes;
+        if (!((absent >> stage) & 1u)) {
+          if (!__all_sync(kFull, mbar_wait(&bars[warp][stage], (phases >> stage) & 1u, gave_up ? 1 : kWaitTries)))
+            gave_up = true;  // every lane alike
+          phases ^= 1u << stage;
+          uint32_t seen = 0xFFFFFFFFu;
+          if (x == edge_at) {
+            // which of the block's tokens the query sees.  Unseen ones: what their places hold (another
+            // sequence's remains, infinities) must not reach a product, so their scale, min and norm
+            // become zeros and their weights are zero
+            const int len = pl.len[cur.b], tk = own_block(cur.vis, x) * kBlkTok + lane;
+            const int wstart = (p.window > 0 && len > p.window) ? len - p.window : 0;
+            const bool on = tk < len && (tk >= wstart || tk < p.sinks);
+            seen = __ballot_sync(kFull, on);
+            if (!on) {
+              uint8_t* bp = smem + (warp * kStages + stage) * kBlkBytes;
+              reinterpret_cast<float*>(bp + kBlkOffNc)[lane] = 0.0f;
+              #pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                reinterpret_cast<uint16_t*>(bp + kBlkOffScale)[32 * q + lane] = 0;
+                reinterpret_cast<uint16_t*>(bp + kBlkOffMin)[32 * q + lane] = 0;
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy to the stage
+            }
+            __syncwarp();
+            edge_at = next_edge(cur.vis, x + 1, cur.nb);
+          }
+          // ---- scores
+          float dot[8];
+          uint32_t ncr[8];
+          {
+            uint32_t kw[4];
+            ldsm_x4(kw, st + lane * 16);
+            lds128(ncr, st + kBlkOffNc + 32 * t);
+            lds128(ncr + 4, st + kBlkOffNc + 32 * t + 16);
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // the sums start at the bits of 1.5 2^23: as a float, an entry is that plus its integer
+              int d[4];
+              const uint32_t w[2] = {kw[i], kw[i] >> 4};
+              imma_from(d, 0x4B400000, aq[0][0], 0x08080808u, aq[0][1], 0x04040404u, w[0] & 0x01010101u, w[0] & 0x02020202u);
+              imma(d, aq[1][0], 0x02020202u, aq[1][1], 0x01010101u, w[0] & 0x04040404u, w[0] & 0x08080808u);
+              imma(d, aq[2][0], 0x08080808u, aq[2][1], 0x04040404u, w[1] & 0x01010101u, w[1] & 0x02020202u);
+              imma(d, aq[3][0], 0x02020202u, aq[3][1], 0x01010101u, w[1] & 0x04040404u, w[1] & 0x08080808u);
+              #pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float a8 = __fadd_rn(__int_as_float(d[e]), -12582912.0f);
+                const float b8 = __fadd_rn(__int_as_float(d[2 + e]), -12582912.0f);
+                dot[2 * i + e] = __fmaf_rn(c1, a8, __fmaf_rn(c2, b8, c0));
+              }
+            }
+          }
+          uint32_t sc[4][4];
+          #pragma unroll
+          for (int q = 0; q < 4; ++q) lds128(sc[q], st + kBlkOffScale + q * 64 + 16 * t);
+          {
+            uint32_t any = 0;  // a scale of 2 or more has the top exponent bit
+            #pragma unroll
+            for (int q = 0; q < 4; ++q) any |= sc[q][0] | sc[q][1] | sc[q][2] | sc[q][3];
+            if (__any_sync(kFull, (any & 0x40004000u) != 0)) {  // rare: large values
+              int k = 0;
+              #pragma unroll
+              for (int q = 0; q < 4; ++q)
+                #pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  k = max(k, max(static_cast<int>(sc[q][i] & 0x7C00u), static_cast<int>((sc[q][i] >> 16) & 0x7C00u)));
+              k = __reduce_max_sync(kFull, (k >> 10) - 15);  // all scales are below 2^(1 + k)
+              if (k > top_scale) {
+                const float f = ex2(static_cast<float>(top_scale - k));
+                m += static_cast<float>(k - top_scale);
+                top_scale = k;
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  #pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[i][e] = __fmul_rn(acc[i][e], f);
+                }
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) side[e] = __fmul_rn(side[e], f);
+              }
+            }
+          }
+          // exponents of the weights: logit - m + kBase
+          float y[8];
+          {
+            const float off = kBase - m;
+            #pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = __fmaf_rn(dot[j], __uint_as_float(ncr[j]), off);
+          }
+          if (seen != 0xFFFFFFFFu) {
+            const uint32_t mine = seen >> (8 * t);
+            #pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = (mine >> j) & 1u ? y[j] : -INFINITY;
+          }
+          float mx = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+          const float bar = kBase + kTau - static_cast<float>(top_scale);
+          if (__any_sync(kFull, mx > bar) || fresh) {  // rare: raise references
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+            const float rise = fresh || mx > bar ? mx - (bar - kTau) : 0.0f;
+            const float alpha = fresh ? 0.0f : ex2(-rise);
+            m += rise;
+            #pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] -= rise;
+            const float a0 = __shfl_sync(kFull, alpha, 8 * t), a1 = __shfl_sync(kFull, alpha, 8 * t + 4);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[i][0] = __fmul_rn(acc[i][0], a0);
+              acc[i][1] = __fmul_rn(acc[i][1], a1);
+              acc[i][2] = __fmul_rn(acc[i][2], a0);
+              acc[i][3] = __fmul_rn(acc[i][3], a1);
+            }
+            side[0] = __fmul_rn(side[0], a0);
+            side[1] = __fmul_rn(side[1], a1);
+            fresh = false;
+          }
+          uint32_t pw[4];
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) pw[i] = pack_f16(ex2(y[2 * i]), ex2(y[2 * i + 1]));
+          {
+            uint32_t mn[4];
+            lds128(mn, g < 4 ? st + kBlkOffMin + g * 64 + 16 * t : side_row);
+            hmma(side, mn[0], 0u, mn[1], 0u, pw[0], pw[1]);
+            hmma(side, mn[2], 0u, mn[3], 0u, pw[2], pw[3]);
+          }
+          // the codes of pairs 1 and 3 sit four bits higher
+          pw[1] = hmul2(pw[1], 0x2C002C00u);
+          pw[3] = hmul2(pw[3], 0x2C002C00u);
+          // ---- P.V, value group by value group (32 channels: rows of two products)
+          #pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t cw[4], wt[4], rest[4];
+            ldsm_x4(cw, st + kBlkOffCodes + (32 * q + lane) * 16);  // rows g, g + 8, g + 16, g + 24; word t
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              wt[i] = hmul2(pw[i], sc[q][i]);
+              if (kFine) rest[i] = hfma2(pw[i], sc[q][i], wt[i] ^ 0x80008000u);
+            }
+            #pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t lo = cw[2 * u], hi = cw[2 * u + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+              const uint32_t a0 = lo & 0x000F000Fu, a1 = hi & 0x000F000Fu, a2 = lo & 0x00F000F0u, a3 = hi & 0x00F000F0u;
+              const uint32_t b0 = lo8 & 0x000F000Fu, b1 = hi8 & 0x000F000Fu, b2 = lo8 & 0x00F000F0u, b3 = hi8 & 0x00F000F0u;
+              hmma(acc[2 * q + u], a0, a1, a2, a3, wt[0], wt[1]);
+              hmma(acc[2 * q + u], b0, b1, b2, b3, wt[2], wt[3]);
+              if (kFine) {
+                hmma(acc[2 * q + u], a0, a1, a2, a3, rest[0], rest[1]);
+                hmma(acc[2 * q + u], b0, b1, b2, b3, rest[2], rest[3]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        // ---- the stage's next block
+        if (ahead.in + ahead.left > 0 && !gave_up) issue(stage);
+        else if (gave_up) absent |= 1u << stage;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+      }
+      if (fresh) m = kNoRef;
+      cur.left -= count;
+
+      if (starts && ends) {  // all of it: finished here
+        const int64_t qrow = static_cast<int64_t>(cur.b) * p.Hq + static_cast<int64_t>(cur.h) * G;
+        if (p.rows) {
+          put_piece(p.rows + qrow * kRow);
+        } else {
+          #pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int hd = 2 * t + e;
+            const float den = __shfl_sync(kFull, side[e], 16 + t);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float lo = value(i, e, 0), hi = value(i, e, 1);
+              if (hd < G) {
+                store_out(p.out, p.q_dtype, (qrow + hd) * kD + 16 * i + g, den != 0.0f ? __fdiv_rn(lo, den) : 0.0f);
+                store_out(p.out, p.q_dtype, (qrow + hd) * kD + 16 * i + g + 8, den != 0.0f ? __fdiv_rn(hi, den) : 0.0f);
+              }
+            }
+          }
+        }
+      } else if (cur.left > 0) {  // its end: the run goes on with another segment
+        put_piece(first);
+      } else {
+        last = true;
+      }
+      if (cur.left > 0) {
+        const Seg next = seg[++cur.s];
+        cur.i = 0;
+        cur.b = next.b;
+        cur.h = next.h;
+        cur.nb = next.nb;
+        cur.vis = visible(pl.len[cur.b], p.window, p.sinks);
+      }
+    }
+
+    // ---- the warps' pieces meet: of segment x, warps wf .. wl have one each, in `red` or (an end inside the
+    // warp's run) in `first`
+    __syncthreads();  // the ring is drained, the pieces in `first` are written
+    if (last) put_piece(red + warp * G * kRow);
+    __syncthreads();
+    // for the merge: pieces of the segment that goes on past the range, or of every segment (rows)
+    for (int x = threadIdx.x; x < nseg; x += kThreads) {
+      const Seg sg = seg[x];
+      const bool starts = sg.base >= 0, ends = sg.base + sg.nb <= n;
+      const int pieces = ends ? 1 : pl.owner(a + sg.base + sg.nb - 1) - cta + 1;
+      if (p.rows) {
+        if (starts) p.spread[static_cast<int64_t>(sg.b) * pl.Hkv + sg.h] = make_int2(cta, pieces);
+      } else if (x == nseg - 1 && a + n == r1) {
+        p.spread[cta] = make_int2(sg.b * p.Hq + sg.h * G, starts && !ends ? pieces : 0);
+      }
+    }
+    for (int r = warp; r < nseg * G; r += kWarps) {  // a row (segment, head) per warp, four channels per lane
+      const int x = r / G, hd = r - x * G;
+      const Seg sg = seg[x];
+      const int s = max(sg.base, 0), e = min(sg.base + sg.nb, n);
+      const int wf = run_owner(s), wl = run_owner(e - 1);
+      const bool starts = sg.base >= 0, ends = sg.base + sg.nb <= n;
+      if (wf == wl && starts && ends) continue;  // finished by its warp
+      const bool inside = e < run_begin(wl + 1);  // the last piece is in `first`
+      const float* tail = p.first + ((static_cast<int64_t>(cta) * kWarps + wl) * G + hd) * kRow;
+      float2 head = make_float2(kNoRef, 0.0f);  // lane w: piece w's m and l
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (lane >= wf && lane <= wl) head = *reinterpret_cast<const float2*>(red + (lane * G + hd) * kRow);
+      if (inside) {
+        if (lane == wl) head = *reinterpret_cast<const float2*>(tail);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = tail[2 + lane + 32 * i];
+      }
+      float M = head.x;
+      #pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+      M = __shfl_sync(kFull, M, 0);  // lanes 0 .. 15 hold the pieces
+      const float f = ex2(head.x - M);
+      float num[4] = {0.0f, 0.0f, 0.0f, 0.0f}, den = 0.0f;
+      #pragma unroll 4
+      for (int w = wf; w <= wl; ++w) {
+        const float fw = __shfl_sync(kFull, f, w), lw = __shfl_sync(kFull, head.y, w);
+        const float* o = red + (w * G + hd) * kRow + 2 + lane;
+        const bool in_first = inside && w == wl;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) num[i] = __fmaf_rn(fw, in_first ? v[i] : o[32 * i], num[i]);
+        den = __fmaf_rn(fw, lw, den);
+      }
+      const int64_t qrow = static_cast<int64_t>(sg.b) * p.Hq + static_cast<int64_t>(sg.h) * G + hd;
+      if (starts && ends && !p.rows) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) store_out(p.out, p.q_dtype, qrow * kD + lane + 32 * i, den != 0.0f ? __fdiv_rn(num[i], den) : 0.0f);
+      } else {
+        float* row = starts && ends ? p.rows + qrow * kRow
+                                    : p.part + ((static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * G + hd) * kRow;
+        if (lane == 0) *reinterpret_cast<float2*>(row) = make_float2(M, den);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) row[2 + lane + 32 * i] = num[i];
+      }
+    }
+    a += n;
+    if (a < r1) {  // the next round's copies land where the pieces were
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();
+    }
+  }
+  if (gave_up && lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_TIMEOUT);
+}
+
+}  // namespace paged
+}  // namespace kv1b

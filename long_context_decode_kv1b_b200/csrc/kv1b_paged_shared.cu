@@ -21,7 +21,7 @@
 //
 // A tile of 128 tokens x 256 rows costs 512 + 1,024 clocks of products and 32,768 exponentials, 2,048
 // clocks at 16 a clock: the exponentials bound it.
-#include "kv1b_paged_device.cuh"
+#include "kv1b_paged_attend.cuh"
 
 namespace kv1b {
 namespace paged {
@@ -48,7 +48,8 @@ constexpr int kShV = kShK + kBuf * kKBytes;
 constexpr int kShRaw = kShV + kBuf * kVBytes;
 constexpr int kShNc = kShRaw + kRaw * kRawBytes;     // f32 [kBuf][2][128]: nc, nc I1
 constexpr int kShMask = kShNc + kBuf * 2 * kTile * 4;  // u32 [kBuf][4]: tokens seen
-constexpr int kShSmem = kShMask + kBuf * 16 + 1024;    // and the alignment of the base
+constexpr int kShFactors = kShMask + kBuf * 16;        // f32 [256][2]
+constexpr int kShSmem = kShFactors + 256 * 8 + 1024;   // and the alignment of the base
 static_assert(kRawBytes % 128 == 0 && kShSmem <= 226 * 1024, "shared memory");
 
 // ---- tensor memory and products
@@ -126,39 +127,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N]) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ---------------------------------------------------------------------------------------------
-// Query rows as f8 codes in the order of the expanded signs (channel 32 w + 8 j + r at byte 32 w + 4 r + j),
-// and each row's two factors of the logit.  One warp per row.
-__global__ void __launch_bounds__(256) paged_query_codes_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // [sequence][q head]
-  if (row >= static_cast<int64_t>(p.B) * p.Hq) return;
-  const QueryPrep qp = query_prep_warp(p.q, row * kD, p.q_dtype, p.c.signs);
-  const int b = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - static_cast<int64_t>(b) * p.Hq);
-  const int h = hq / G, g = hq - h * G;
-  const int64_t at = static_cast<int64_t>(h) * s.R + static_cast<int64_t>(b) * G + g;
-  const int w = lane >> 3;  // word of the lane's four channels 4 lane + r
-  #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int c = 4 * (lane & 7) + r;  // channel within the word
-    uint32_t v = 0;
-    #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t word = w == 0 ? qp.planes[j][0] : (w == 1 ? qp.planes[j][1] : (w == 2 ? qp.planes[j][2] : qp.planes[j][3]));
-      v |= ((word >> c) & 1u) << j;
-    }
-    const int e = 31 - __clz(v | 1u);
-    const uint32_t f8 = v == 0 ? 0u : static_cast<uint32_t>((7 + e) << 3) | ((v << (3 - e)) & 7u);
-    s.codes[at * kD + 32 * w + 4 * (c & 7) + (c >> 3)] = static_cast<uint8_t>(f8);
-  }
-  if (lane == 0) {
-    const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
-    s.factors[at] = make_float2(__fmul_rn(qp.delta, qs), __fmul_rn(qp.vl, qs));
-  }
-}
-
 __device__ __forceinline__ int prefix_tokens(const PagedAttendParams& p, bool report) {
   const int64_t top = static_cast<int64_t>(p.max_prefix_pages) << (p.c.bpp_shift + 5);
   const int n = __ldg(p.prefix_len);
@@ -202,12 +170,11 @@ __device__ __forceinline__ float row_weights(const uint32_t (&x)[2][32], const f
   return __fadd_rn(s0, s1);
 }
 
-__global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const PagedAttendParams p, const PagedSharedParams s) {
-  extern __shared__ uint8_t smem_raw[];
+// Unit u of the prefix's part.
+__device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const PagedSharedParams& s, const int G, const int u, uint8_t* smem) {
   __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[kBuf], kv_empty[kBuf];
   __shared__ __align__(8) uint64_t s_full[2], turn[2], pv_done[2][2];
   __shared__ uint32_t s_tmem, s_absent[kRaw];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // the warp as a uniform value
 
@@ -224,7 +191,6 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
   pdl_launch_dependents();
 
   // unit: kv-head, row tile, split
-  const int u = blockIdx.x;
   const int split = u % s.splits, hr = u / s.splits;
   const int rt = hr % s.row_tiles, h = hr / s.row_tiles;
   const int n = prefix_tokens(p, u == 0 && threadIdx.x == 0);
@@ -242,14 +208,44 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
   auto tile_of = [&](int j) { return two ? j >> 1 : j; };
   auto half_of = [&](int w, int j) { return two ? j & 1 : w; };
 
+  float2* const factors = reinterpret_cast<float2*>(smem + kShFactors);
   if (warp == 0) tmem_alloc(&s_tmem);
-  {  // the rows' codes, swizzled; zeros behind the last row
+  {  // The rows' codes as f8 in the order of the expanded signs (channel 32 w + 8 j + r at byte 32 w + 4 r + j),
+     // swizzled, and their two factors of the logit; zeros behind the last row.  Two rows of a warp at a time.
     const int rows = two ? 256 : 128;
-    for (int e = threadIdx.x; e < rows * 8; e += kShThreads) {
-      const int r = e >> 3, c = e & 7, row = rt * rows + r;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (row < s.R) v = *reinterpret_cast<const uint4*>(s.codes + (static_cast<int64_t>(h) * s.R + row) * kD + 16 * c);
-      *reinterpret_cast<uint4*>(smem + kShQ + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+    const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
+    #pragma unroll 1
+    for (int r0 = 2 * warp; r0 < rows; r0 += 2 * (kShThreads / 32)) {
+      float x[2][4];
+      #pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = rt * rows + r0 + i;
+        x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
+        if (row < s.R) load4(p.q, (static_cast<int64_t>(row / G) * p.Hq + static_cast<int64_t>(h) * G + row % G) * kD + 4 * lane, p.q_dtype, x[i]);
+      }
+      if (rt * rows + r0 >= s.R) {  // neither is there
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          *reinterpret_cast<uint32_t*>(smem + kShQ + (r0 + i) * 128 + 4 * lane) = 0u;
+          if (lane == 0) factors[r0 + i] = make_float2(0.0f, 0.0f);
+        }
+        continue;
+      }
+      #pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + i;
+        int code[4];
+        float vl, dl;
+        query_quantise(x[i], p.c.signs, code, &vl, &dl);
+        uint8_t* at = smem + kShQ + r * 128 + (((2 * (lane >> 3) + (lane & 1)) ^ (r & 7)) << 4) + ((lane & 7) >> 1);
+        #pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t v = static_cast<uint32_t>(code[c]);
+          const int e = 31 - __clz(v | 1u);
+          at[4 * c] = static_cast<uint8_t>(v == 0 ? 0u : static_cast<uint32_t>((7 + e) << 3) | ((v << (3 - e)) & 7u));
+        }
+        if (lane == 0) factors[r] = make_float2(__fmul_rn(dl, qs), __fmul_rn(vl, qs));
+      }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -272,8 +268,7 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
     const int row = rt * (two ? 256 : 128) + (two ? w * 128 : 0) + r;
     const bool warp_rows = row - lane < s.R;  // a warp without rows only keeps the barriers going
     const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 256, tO = tS + 128;
-    float2 f = make_float2(0.0f, 0.0f);
-    if (row < s.R) f = s.factors[static_cast<int64_t>(h) * s.R + row];
+    const float2 f = factors[(two ? w * 128 : 0) + r];
     const uint64_t fa = pair(f.x, f.x), fb = pair(f.y, f.y);
     float m = 0.0f, l = 0.0f;
     bool have = false;  // a finite logit has set m
@@ -545,6 +540,19 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_prefix_kernel(const Paged
   if (warp == 0) tmem_free(tmem);
 }
 
+// The prefix's units, then the CTAs of the sequences' own tokens: where the prefix leaves SMs idle the two
+// parts run side by side.  (Four launches one after another, the queries' codes first: 37 instead of @SMALL@ us for
+// 4 sequences of 61 tokens behind 1,000.)
+template <bool kFine>
+__global__ void __launch_bounds__(kShThreads, 1) paged_shared_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G,
+                                                                      const int units) {
+  static_assert(kShThreads == kThreads && kSmem <= kShSmem, "one launch for both parts");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  if (static_cast<int>(blockIdx.x) < units) prefix_cta(p, s, G, blockIdx.x, smem);
+  else attend_cta<kFine>(p, G, blockIdx.x - units, smem);
+}
+
 // One (sequence, kv-head, query head) per block: the sequence's own pieces and the prefix's.
 __global__ void __launch_bounds__(128) paged_shared_merge_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G) {
   __shared__ float2 s_head[kMaxPieces];
@@ -576,16 +584,13 @@ __global__ void __launch_bounds__(128) paged_shared_merge_kernel(const PagedAtte
 using namespace kv1b;
 
 cudaError_t kv1b_launch_paged_shared(const PagedAttendParams& p, const PagedSharedParams& s, int32_t G, cudaStream_t stream) {
-  static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = configure_smem(reinterpret_cast<const void*>(paged::paged_prefix_kernel), paged::kShSmem, &configured);
+  static std::atomic<unsigned long long> configured{0}, configured_fine{0};
+  const bool fine = p.q_dtype == KV1B_DTYPE_F16;
+  const auto kernel = fine ? paged::paged_shared_kernel<true> : paged::paged_shared_kernel<false>;
+  cudaError_t e = configure_smem(reinterpret_cast<const void*>(kernel), paged::kShSmem, fine ? &configured_fine : &configured);
   if (e != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(p.B) * p.Hq;
-  e = launch_pdl(paged::paged_query_codes_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p, s, G);
-  if (e != cudaSuccess) return e;
-  const unsigned units = static_cast<unsigned>(p.c.Hkv) * s.row_tiles * s.splits;
-  e = launch_pdl(paged::paged_prefix_kernel, dim3(units), dim3(paged::kShThreads), paged::kShSmem, stream, p, s);
-  if (e != cudaSuccess) return e;
-  e = kv1b_launch_paged_attend(p, G, stream);
+  const int units = p.c.Hkv * s.row_tiles * s.splits;
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(units + p.ncta)), dim3(paged::kShThreads), paged::kShSmem, stream, p, s, G, units);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged::paged_shared_merge_kernel, dim3(static_cast<unsigned>(p.B) * p.c.Hkv, G), dim3(128), 0, stream, p, s, G);
 }
