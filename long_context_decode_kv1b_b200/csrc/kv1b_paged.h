@@ -71,17 +71,23 @@ struct PagedAttendParams {
   int32_t max_pages;
   const int32_t* lengths;
   int32_t window, sinks;
+  int32_t packed;          // first sequences of the plan that are the shared prefix, each for up to 8 rows of every
+                           // kv-head's matrix (below); then the B sequences' own tokens
   const int32_t* prefix_pages;  // optional shared prefix: its pages and (device) token count
   const int32_t* prefix_len;
   int32_t max_prefix_pages;
   void* out;               // q_dtype [B][Hq][128]
   float* part;             // [ctas][2][G][2 + 128]
   float* first;            // [ctas][16 warps][G][2 + 128]: ends of segments inside a warp's run
-  float* rows;             // null, or [B][Hq][2 + 128]: whole segments leave (m, l, o) here, none is normalised
+  float* rows;             // null, or [B][Hq][2 + 128] and, packed, [Hkv][B G][2 + 128]: whole segments leave
+                           // (m, l, o) here, none is normalised
   int2* spread;            // [ctas] first output row and pieces of the segment a range boundary cuts, or with
-                           // rows [B][Hkv] first CTA and pieces of each segment; pieces 0: none
+                           // rows [packed + B][Hkv] first CTA and pieces of each segment; pieces 0: none
   int32_t ncta;
+  int32_t min_units;       // blocks and what segments count besides (kSegUnits each) that a CTA takes at least
 };
+
+constexpr int kPackedRows = 32;  // rows of a kv-head up to which the attend's kernel takes the prefix
 
 // The queries of a kv-head as the rows of one matrix: R = B G rows, row b G + g.
 struct PagedSharedParams {

@@ -195,16 +195,36 @@ kv1b::PagedSharedParams shared_plan(int32_t Hkv, int32_t G, int32_t num_seqs, in
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The buffers of a shared call in its workspace, behind those of the attend; bytes in all.
-size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int32_t Hkv, int32_t G, size_t attend_bytes, uint8_t* ws) {
+// Few rows of a kv-head are served by the attend's kernel, eight at a time, the prefix once for each eight.
+int packed_groups(int32_t rows) { return rows <= kv1b::kPackedRows ? (rows + 7) / 8 : 0; }
+
+// The buffers of a shared call in its workspace; bytes in all.
+size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int32_t Hkv, int32_t G, uint8_t* ws) {
   const size_t rows = static_cast<size_t>(Hkv) * s->R, row = kv1b::kPartStride * 4;
-  size_t at = attend_bytes;
-  if (p) p->rows = reinterpret_cast<float*>(ws + at);
-  at += up256(rows * row);
-  if (p) p->spread = reinterpret_cast<int2*>(ws + at);
-  at += up256(static_cast<size_t>(Hkv) * (s->R / G) * 8);
-  s->pieces = reinterpret_cast<float*>(ws + at);
-  return at + up256(static_cast<size_t>(Hkv) * s->row_tiles * s->splits * 256 * row);
+  const size_t packed = packed_groups(s->R), n = packed ? 8 : G;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* const here = ws + at;
+    at += up256(bytes);
+    return here;
+  };
+  uint8_t* const part = take(static_cast<size_t>(num_sms()) * 2 * n * row);
+  uint8_t* const first = take(static_cast<size_t>(num_sms()) * 16 * n * row);
+  uint8_t* const whole = take((packed ? 2 : 1) * rows * row);
+  uint8_t* const spread = take(static_cast<size_t>(Hkv) * (packed + s->R / G) * 8);
+  uint8_t* const pieces = take(packed ? 0 : static_cast<size_t>(Hkv) * s->row_tiles * s->splits * 256 * row);
+  if (p) {
+    p->packed = static_cast<int32_t>(packed);
+    // Behind the prefix's CTAs, which take nearly every SM, few CTAs do better than short ones: 56 against 66 us
+    // for 64 rows a kv-head over 30,000 tokens; with the SMs to themselves, 20 against 26 us the other way.
+    if (!packed) p->min_units = 64;
+    p->part = reinterpret_cast<float*>(part);
+    p->first = reinterpret_cast<float*>(first);
+    p->rows = reinterpret_cast<float*>(whole);
+    p->spread = reinterpret_cast<int2*>(spread);
+    s->pieces = reinterpret_cast<float*>(pieces);
+  }
+  return at;
 }
 
 }  // namespace
@@ -212,12 +232,11 @@ size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int3
 size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_seqs, int32_t num_q_heads,
                                          int32_t max_prefix_pages) {
   if (num_seqs < 1 || num_seqs > KV1B_PAGED_MAX_SEQS || max_prefix_pages < 1) return 0;
-  const size_t attend_bytes = kv1b_paged_attend_workspace_bytes(cache, num_q_heads);
-  if (attend_bytes == 0 || table_check(cache, 1, 0, 1, max_prefix_pages) != KV1B_OK) return 0;
+  if (!paged_ok(cache) || heads_check(cache, num_q_heads) != KV1B_OK || table_check(cache, 1, 0, 1, max_prefix_pages) != KV1B_OK) return 0;
   const int32_t G = num_q_heads / cache->num_kv_heads;
   kv1b::PagedSharedParams s =
       shared_plan(cache->num_kv_heads, G, num_seqs, static_cast<int64_t>(max_prefix_pages) * cache->page_tokens);
-  return shared_carve(&s, nullptr, cache->num_kv_heads, G, attend_bytes, nullptr);
+  return shared_carve(&s, nullptr, cache->num_kv_heads, G, nullptr);
 }
 
 static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
@@ -234,8 +253,8 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(page_table, 4) || !aligned(lengths, 4) ||
       !aligned(prefix_pages, 4) || !aligned(prefix_length, 4))
     return KV1B_ERR_MISALIGNED;
-  const size_t attend_bytes = kv1b_paged_attend_workspace_bytes(cache, num_q_heads);
-  if (ws_bytes < (prefix_pages ? kv1b_paged_shared_workspace_bytes(cache, num_seqs, num_q_heads, max_prefix_pages) : attend_bytes))
+  if (ws_bytes < (prefix_pages ? kv1b_paged_shared_workspace_bytes(cache, num_seqs, num_q_heads, max_prefix_pages)
+                               : kv1b_paged_attend_workspace_bytes(cache, num_q_heads)))
     return KV1B_ERR_WORKSPACE;
   kv1b::PagedAttendParams p;
   memset(&p, 0, sizeof(p));
@@ -256,6 +275,7 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   p.max_prefix_pages = max_prefix_pages;
   p.out = out;
   p.ncta = num_sms();
+  p.min_units = 16;
   p.part = static_cast<float*>(ws);
   p.first = p.part + static_cast<size_t>(p.ncta) * 2 * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride;
   p.spread = reinterpret_cast<int2*>(p.first + static_cast<size_t>(p.ncta) * 16 * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride);
@@ -263,7 +283,7 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   if (!prefix_pages) return cuda_status(kv1b_launch_paged_attend(p, G, static_cast<cudaStream_t>(stream)));
   kv1b::PagedSharedParams s =
       shared_plan(cache->num_kv_heads, G, num_seqs, static_cast<int64_t>(max_prefix_pages) * cache->page_tokens);
-  shared_carve(&s, &p, cache->num_kv_heads, G, attend_bytes, static_cast<uint8_t*>(ws));
+  shared_carve(&s, &p, cache->num_kv_heads, G, static_cast<uint8_t*>(ws));
   return cuda_status(kv1b_launch_paged_shared(p, s, G, static_cast<cudaStream_t>(stream)));
 }
 

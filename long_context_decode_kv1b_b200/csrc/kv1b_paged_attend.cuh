@@ -43,20 +43,21 @@ constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 
-constexpr int kQuerySlots = 128;  // prepared query rows a round holds
+constexpr int kQuerySlots = 256;  // prepared query rows a round holds
 constexpr int kMaxSegs = 64;      // segments a round holds
 
 // a segment of a round, in blocks from the round's start
 struct Seg {
   int base, nb;  // first block (below 0 where the CTA's range begins inside the segment), blocks
   int b, h;
+  int k;         // place of b among the sequences that see a block
 };
 
 constexpr int kOffPre = kWarps * kStages * kBlkBytes;            // u32 [kMaxSeqs + 1] blocks before each sequence
 constexpr int kOffLen = kOffPre + (kMaxSeqs + 4) * 4;            // i32 [kMaxSeqs]
 constexpr int kOffSome = kOffLen + kMaxSeqs * 4;                 // u16 [kMaxSeqs]
 constexpr int kOffSeg = kOffSome + kMaxSeqs * 2;                 // Seg [kMaxSegs]
-constexpr int kOffPlane = kOffSeg + kMaxSegs * 16;               // u32 [kQuerySlots][4 planes][4]
+constexpr int kOffPlane = kOffSeg + kMaxSegs * 32;               // u32 [kQuerySlots][4 planes][4]
 constexpr int kOffConst = kOffPlane + kQuerySlots * 64;          // f32 [kQuerySlots][4]: c1, c2, c0
 constexpr int kOffRows = kOffConst + kQuerySlots * 16;           // f16 [2][8]: ones, zeros
 constexpr int kOffSigns = kOffRows + 32;                         // f32 [3][128]
@@ -85,7 +86,8 @@ struct Ahead {
     vis = visible(pl.len[b], p.window, p.sinks);
   }
   __device__ __forceinline__ void look_up(const PagedAttendParams& p) {
-    page = __ldg(p.table + b * p.table_stride + (own_block(vis, i) >> p.c.bpp_shift));
+    const int32_t* list = b < p.packed ? p.prefix_pages : p.table + (b - p.packed) * p.table_stride;
+    page = __ldg(list + (own_block(vis, i) >> p.c.bpp_shift));
   }
   __device__ __forceinline__ void next_stretch(const Seg* seg, const Plan& pl, const PagedAttendParams& p) {
     const int blk = own_block(vis, i), off = blk & ((1 << p.c.bpp_shift) - 1);
@@ -116,9 +118,26 @@ __device__ __forceinline__ int next_edge(const Visible& v, int i, int nb) {
 constexpr float kCodeUnit = 16777216.0f;  // codes enter the products as binary16 subnormals, units of 2^-24
 
 // kFine: the weights of the codes in two binary16 parts (fp16 results); one part is enough for bf16.
+// The query heads of kv-head h that sequence b of the plan serves: G, or up to 8 rows b G' + g of the batch.
+struct Heads {
+  int V, G, Hq, B;
+  __device__ __forceinline__ int count(int b) const { return b < V ? min(8, B * G - 8 * b) : G; }
+  // row of q and out of head i
+  __device__ __forceinline__ int64_t query(int b, int h, int i) const {
+    const int r = 8 * b + i;
+    return b < V ? static_cast<int64_t>(r / G) * Hq + h * G + r % G : static_cast<int64_t>(b - V) * Hq + h * G + i;
+  }
+  // row of p.rows of head 0
+  __device__ __forceinline__ int64_t row(int b, int h) const {
+    return b < V ? static_cast<int64_t>(B) * Hq + static_cast<int64_t>(h) * B * G + 8 * b : static_cast<int64_t>(b - V) * Hq + h * G;
+  }
+};
+
 // `cta` of p.ncta, kThreads threads, kSmem bytes at `smem` (128-byte aligned).
 template <bool kFine>
-__device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int G, const int cta, uint8_t* smem) {
+__device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int G_, const int cta, uint8_t* smem) {
+  const Heads heads = {p.packed, G_, p.Hq, p.B};
+  const int G = p.packed ? 8 : G_;  // rows that a segment may have
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint32_t* pre = reinterpret_cast<uint32_t*>(smem + kOffPre);
@@ -139,11 +158,11 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
   const Plan pl = make_plan<kThreads>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), p.ncta, cta == 0);
 
   // sequences that see nothing: zeros
-  for (int b = p.rows ? p.B : cta; b < p.B; b += p.ncta)
+  for (int b = p.rows ? p.B : cta; b < p.B; b += p.ncta)  // (none are packed here)
     if (pre[b + 1] == pre[b])
       for (int e = threadIdx.x; e < p.Hq * kD; e += kThreads) store_out(p.out, p.q_dtype, static_cast<int64_t>(b) * p.Hq * kD + e, 0.0f);
   if (p.rows)
-    for (int64_t i = static_cast<int64_t>(cta) * kThreads + threadIdx.x; i < static_cast<int64_t>(p.B) * pl.Hkv;
+    for (int64_t i = static_cast<int64_t>(cta) * kThreads + threadIdx.x; i < static_cast<int64_t>(pl.B) * pl.Hkv;
          i += static_cast<int64_t>(p.ncta) * kThreads) {
       const int b = static_cast<int>(i / pl.Hkv);
       if (pre[b + 1] == pre[b]) p.spread[i] = make_int2(0, 0);
@@ -153,7 +172,11 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     return;
   }
 
-  const int64_t r0 = pl.begin(cta), r1 = pl.begin(cta + 1);  // never empty: n is at most S
+  const int64_t r0 = pl.begin(cta), r1 = pl.begin(cta + 1);
+  if (r0 == r1) {  // within what a segment counts besides its blocks
+    if (threadIdx.x == 0 && !p.rows) p.spread[cta] = make_int2(0, 0);
+    return;
+  }
   const uint32_t ring = smem_u32(smem) + warp * kStages * kBlkBytes;
   const int max_segs = min(kMaxSegs, kQuerySlots / G);
   const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
@@ -171,19 +194,18 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       int lo = 0, hi = pl.nsome;  // the sequence of block a: largest lo with Hkv pre[some[lo]] <= a
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (static_cast<int64_t>(pre[pl.some[mid]]) * pl.Hkv <= a) lo = mid;
+        if (pl.first_block(mid) <= a) lo = mid;
         else hi = mid;
       }
-      const int b0 = pl.some[lo];
-      const int h0 = static_cast<int>(quotient(a - static_cast<int64_t>(pre[b0]) * pl.Hkv, pre[b0 + 1] - pre[b0]));
+      const int h0 = static_cast<int>(quotient(a - pl.first_block(lo), pl.blocks(lo)));
       bool valid = false;
       if (static_cast<int>(threadIdx.x) < max_segs) {
         const int id = h0 + threadIdx.x, k = lo + id / pl.Hkv, h = id % pl.Hkv;
         if (k < pl.nsome) {
-          const int b = pl.some[k], nb = static_cast<int>(pre[b + 1] - pre[b]);
-          const int64_t base = static_cast<int64_t>(pre[b]) * pl.Hkv + static_cast<int64_t>(h) * nb;
+          const int nb = pl.blocks(k);
+          const int64_t base = pl.first_block(k) + static_cast<int64_t>(h) * nb;
           valid = base < r1;
-          if (valid) seg[threadIdx.x] = {static_cast<int>(base - a), nb, b, h};
+          if (valid) seg[threadIdx.x] = {static_cast<int>(base - a), nb, pl.some[k], h, k};
         }
       }
       nseg = __syncthreads_count(valid);
@@ -197,14 +219,26 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     };
     const int w0 = run_begin(warp), w1 = run_begin(warp + 1);
 
-    // the rows of the round's queries: a warp's first two are loaded before the copies fill the memory's queues
+    // the round's rows: those of the packed segments, which come first, then the others'
+    int npacked = 0;
+    if (p.packed)
+      while (npacked < nseg && seg[npacked].b < p.packed) ++npacked;
+    const int nrow = npacked * G + (nseg - npacked) * heads.G;
+    auto slot_of = [&](int r) {  // its segment G + head
+      if (r < npacked * G) return r;
+      const int x = (r - npacked * G) / heads.G;
+      return (npacked + x) * G + r - npacked * G - x * heads.G;
+    };
+    // a warp's first two are loaded before the copies fill the memory's queues
     auto load_row = [&](int r, float (&x)[4]) {
-      const Seg sg = seg[r / G];
-      load4(p.q, (static_cast<int64_t>(sg.b) * p.Hq + static_cast<int64_t>(sg.h) * G + r % G) * kD + 4 * lane, p.q_dtype, x);
+      const int s = slot_of(r);
+      const Seg sg = seg[s / G];
+      const int i = min(s % G, heads.count(sg.b) - 1);  // a row that is not there: the last one again, unused
+      load4(p.q, heads.query(sg.b, sg.h, i) * kD + 4 * lane, p.q_dtype, x);
     };
     float q0[4], q1[4];
-    if (warp < nseg * G) load_row(warp, q0);
-    if (warp + kWarps < nseg * G) load_row(warp + kWarps, q1);
+    if (warp < nrow) load_row(warp, q0);
+    if (warp + kWarps < nrow) load_row(warp + kWarps, q1);
 
     // ---- copy side: `ahead` walks kStages blocks in front of the compute
     Ahead ahead;
@@ -235,11 +269,12 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     }
 
     // ---- the round's queries
-    for (int r = warp; r < nseg * G; r += kWarps) {
-      if (r >= 2 * kWarps) load_row(r, q0);
+    for (int r0 = warp; r0 < nrow; r0 += kWarps) {
+      if (r0 >= 2 * kWarps) load_row(r0, q0);
       const QueryPrep qp = query_prep_values(q0, signs);
       #pragma unroll
       for (int j = 0; j < 4; ++j) q0[j] = q1[j];
+      const int r = slot_of(r0);
       if (lane == 0) {
         #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -262,15 +297,16 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     };
     // the warp's sums of a segment to a piece [head][kRow]
     auto put_piece = [&](float* w) {
-      if (t == 0 && g < G) w[g * kRow] = m;
+      const int n_heads = heads.count(cur.b);
+      if (t == 0 && g < n_heads) w[g * kRow] = m;
       #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int hd = 2 * t + e;
-        if (g == 4 && hd < G) w[hd * kRow + 1] = side[e];
+        if (g == 4 && hd < n_heads) w[hd * kRow + 1] = side[e];
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float lo = value(i, e, 0), hi = value(i, e, 1);
-          if (hd < G) {
+          if (hd < n_heads) {
             w[hd * kRow + 2 + 16 * i + g] = lo;
             w[hd * kRow + 2 + 16 * i + g + 8] = hi;
           }
@@ -286,7 +322,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       float4 cc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       {
         uint32_t pw[4] = {0u, 0u, 0u, 0u};
-        if (g < G) {
+        if (g < heads.count(cur.b)) {
           #pragma unroll
           for (int j = 0; j < 4; ++j) pw[j] = planes[((cur.s * G + g) * 4 + j) * 4 + t];
           cc = consts[cur.s * G + g];
@@ -476,9 +512,9 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       cur.left -= count;
 
       if (starts && ends) {  // all of it: finished here
-        const int64_t qrow = static_cast<int64_t>(cur.b) * p.Hq + static_cast<int64_t>(cur.h) * G;
+        const int64_t qrow = heads.query(cur.b, cur.h, 0);
         if (p.rows) {
-          put_piece(p.rows + qrow * kRow);
+          put_piece(p.rows + heads.row(cur.b, cur.h) * kRow);
         } else {
           #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -518,16 +554,17 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     for (int x = threadIdx.x; x < nseg; x += kThreads) {
       const Seg sg = seg[x];
       const bool starts = sg.base >= 0, ends = sg.base + sg.nb <= n;
-      const int pieces = ends ? 1 : pl.owner(a + sg.base + sg.nb - 1) - cta + 1;
+      const int pieces = ends ? 1 : pl.owner(sg.k, sg.h, sg.nb - 1) - cta + 1;
       if (p.rows) {
         if (starts) p.spread[static_cast<int64_t>(sg.b) * pl.Hkv + sg.h] = make_int2(cta, pieces);
       } else if (x == nseg - 1 && a + n == r1) {
-        p.spread[cta] = make_int2(sg.b * p.Hq + sg.h * G, starts && !ends ? pieces : 0);
+        p.spread[cta] = make_int2(static_cast<int>(heads.query(sg.b, sg.h, 0)), starts && !ends ? pieces : 0);
       }
     }
-    for (int r = warp; r < nseg * G; r += kWarps) {  // a row (segment, head) per warp, four channels per lane
-      const int x = r / G, hd = r - x * G;
+    for (int r = warp; r < nrow; r += kWarps) {  // a row (segment, head) per warp, four channels per lane
+      const int x = slot_of(r) / G, hd = slot_of(r) - x * G;
       const Seg sg = seg[x];
+      if (hd >= heads.count(sg.b)) continue;
       const int s = max(sg.base, 0), e = min(sg.base + sg.nb, n);
       const int wf = run_owner(s), wl = run_owner(e - 1);
       const bool starts = sg.base >= 0, ends = sg.base + sg.nb <= n;
@@ -557,12 +594,12 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
         for (int i = 0; i < 4; ++i) num[i] = __fmaf_rn(fw, in_first ? v[i] : o[32 * i], num[i]);
         den = __fmaf_rn(fw, lw, den);
       }
-      const int64_t qrow = static_cast<int64_t>(sg.b) * p.Hq + static_cast<int64_t>(sg.h) * G + hd;
+      const int64_t qrow = heads.query(sg.b, sg.h, hd);
       if (starts && ends && !p.rows) {
         #pragma unroll
         for (int i = 0; i < 4; ++i) store_out(p.out, p.q_dtype, qrow * kD + lane + 32 * i, den != 0.0f ? __fdiv_rn(num[i], den) : 0.0f);
       } else {
-        float* row = starts && ends ? p.rows + qrow * kRow
+        float* row = starts && ends ? p.rows + (heads.row(sg.b, sg.h) + hd) * kRow
                                     : p.part + ((static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * G + hd) * kRow;
         if (lane == 0) *reinterpret_cast<float2*>(row) = make_float2(M, den);
         #pragma unroll

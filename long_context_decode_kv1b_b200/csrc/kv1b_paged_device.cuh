@@ -11,7 +11,7 @@ constexpr float kTau = 8.0f;    // a logit may pass the reference by 2^8 before 
 constexpr float kBase = 7.0f;   // weights are 2^7 at the reference: at most 2^15 < 65504
 constexpr float kNoRef = -1e30f;
 constexpr int kRow = 2 + kD;    // partial row: m (log2 units), l, o[128]
-constexpr int kMinBlocks = 16;  // blocks a CTA of the split takes at least
+constexpr int kSegUnits = 8;    // what a segment counts besides its blocks
 constexpr int kMaxSeqs = KV1B_PAGED_MAX_SEQS;
 constexpr int kWaitTries = 4096;
 
@@ -146,7 +146,7 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float
 }
 
 // ---------------------------------------------------------------------------------------------
-// The work plan, computed alike by every CTA of both kernels from the device lengths.
+// The work plan, computed alike by every CTA from the device lengths.
 struct Visible {
   int blocks;       // blocks seen
   int skip_from;    // blocks [0, skip_from) and from skip_to on are seen
@@ -173,33 +173,39 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return a / b;
 }
 
+// The segments in order, each of as many units as it has blocks and kSegUnits more for its start and end
+// (queries, a piece or a result), cut into n equal ranges of units.
 struct Plan {
-  const uint32_t* pre;  // [B + 1] blocks of one kv-head before each sequence
+  const uint32_t* pre;   // [B + 1] blocks of one kv-head before each sequence
   const int* len;
-  const uint16_t* some; // [nsome] the sequences that see a block, in order (only where asked for)
+  const uint16_t* some;  // [nsome] the sequences that see a block, in order
   int nsome;
-  int B, Hkv, n;        // n: CTAs with work
-  int64_t S;            // blocks in all
-  int64_t q;            // S / n: the first `rem` ranges are one block longer
+  int B, Hkv, n;         // n: CTAs with work
+  int64_t S;             // blocks in all
+  int64_t q;             // units / n: the first `rem` ranges are one unit longer
   int rem;
-  __device__ __forceinline__ int64_t begin(int c) const { return c * q + (c < rem ? c : rem); }
-  __device__ __forceinline__ int owner(int64_t r) const {  // the CTA whose range holds block r: begin(c) <= r < begin(c + 1)
-    const int64_t longer = rem * (q + 1);
-    return r < longer ? static_cast<int>(quotient(r, q + 1)) : rem + static_cast<int>(quotient(r - longer, q));
-  }
-  // segment of block r: sequence, head, first block
-  __device__ __forceinline__ void locate(int64_t r, int* b, int* h, int64_t* base) const {
-    int lo = 0, hi = B;  // largest lo with Hkv * pre[lo] <= r
+  __device__ __forceinline__ int blocks(int k) const { return static_cast<int>(pre[some[k] + 1] - pre[some[k]]); }
+  __device__ __forceinline__ int64_t first_block(int k) const { return static_cast<int64_t>(pre[some[k]]) * Hkv; }
+  __device__ __forceinline__ int64_t first_unit(int k) const { return (pre[some[k]] + static_cast<int64_t>(kSegUnits) * k) * Hkv; }
+  // first block of range c: a segment's kSegUnits come before its blocks
+  __device__ __forceinline__ int64_t begin(int c) const {
+    if (c >= n) return S;
+    const int64_t u = c * q + (c < rem ? c : rem);
+    int lo = 0, hi = nsome;  // largest lo with first_unit(lo) <= u
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (static_cast<int64_t>(pre[mid]) * Hkv <= r) lo = mid;
+      if (first_unit(mid) <= u) lo = mid;
       else hi = mid;
     }
-    const int64_t s0 = static_cast<int64_t>(pre[lo]) * Hkv;
-    const int nb = static_cast<int>(pre[lo + 1] - pre[lo]);
-    *b = lo;
-    *h = static_cast<int>(quotient(r - s0, nb));
-    *base = s0 + static_cast<int64_t>(*h) * nb;
+    const int nb = blocks(lo);
+    const int64_t in = u - first_unit(lo), h = quotient(in, nb + kSegUnits);
+    const int64_t i = in - h * (nb + kSegUnits) - kSegUnits;
+    return first_block(lo) + h * nb + (i > 0 ? i : 0);
+  }
+  // the range that holds block i of head h of sequence some[k]
+  __device__ __forceinline__ int owner(int k, int h, int i) const {
+    const int64_t u = first_unit(k) + static_cast<int64_t>(h) * (blocks(k) + kSegUnits) + kSegUnits + i, longer = rem * (q + 1);
+    return u < longer ? static_cast<int>(quotient(u, q + 1)) : rem + static_cast<int>(quotient(u - longer, q));
   }
 };
 
@@ -207,7 +213,8 @@ struct Plan {
 template <int THREADS>
 __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* pre, int* len, uint16_t* some, int ncta, bool report) {
   __shared__ uint64_t s_tot[THREADS / 32];  // blocks, and sequences with some << 40
-  const int per = (p.B + THREADS - 1) / THREADS;
+  const int nseq = p.packed + p.B;
+  const int per = (nseq + THREADS - 1) / THREADS;
   const int page_shift = p.c.bpp_shift + 5;
   const int64_t most = static_cast<int64_t>(p.max_pages) << page_shift;
   Plan pl;
@@ -216,10 +223,12 @@ __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* 
   uint64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = b0 + i;
-    if (b >= p.B) break;
-    const int n = __ldg(p.lengths + b);
-    bad |= n < 0 || n > most;
-    const int nn = n < 0 ? 0 : static_cast<int>(n > most ? most : n);
+    if (b >= nseq) break;
+    const bool own = b >= p.packed;
+    const int64_t top = own ? most : static_cast<int64_t>(p.max_prefix_pages) << page_shift;
+    const int n = own ? __ldg(p.lengths + b - p.packed) : __ldg(p.prefix_len);
+    bad |= n < 0 || n > top;
+    const int nn = n < 0 ? 0 : static_cast<int>(n > top ? top : n);
     len[b] = nn;
     const int blocks = visible(nn, p.window, p.sinks).blocks;
     mine += static_cast<uint64_t>(blocks) | (blocks > 0 ? 1ull << 40 : 0ull);
@@ -241,26 +250,27 @@ __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* 
   }
   for (int i = 0; i < per; ++i) {
     const int b = b0 + i;
-    if (b >= p.B) break;
+    if (b >= nseq) break;
     pre[b] = static_cast<uint32_t>(at);
     const int blocks = visible(len[b], p.window, p.sinks).blocks;
-    if (some && blocks > 0) some[at >> 40] = static_cast<uint16_t>(b);
+    if (blocks > 0) some[at >> 40] = static_cast<uint16_t>(b);
     at += static_cast<uint64_t>(blocks) | (blocks > 0 ? 1ull << 40 : 0ull);
   }
   const uint32_t total_blocks = static_cast<uint32_t>(total);
-  if (threadIdx.x == 0) pre[p.B] = total_blocks;
+  if (threadIdx.x == 0) pre[nseq] = total_blocks;
   __syncthreads();
   pl.pre = pre;
   pl.len = len;
   pl.some = some;
   pl.nsome = static_cast<int>(total >> 40);
-  pl.B = p.B;
+  pl.B = nseq;
   pl.Hkv = p.c.Hkv;
   pl.S = static_cast<int64_t>(total_blocks) * p.c.Hkv;
-  const int64_t want = (pl.S + kMinBlocks - 1) / kMinBlocks;
+  const int64_t units = pl.S + static_cast<int64_t>(kSegUnits) * pl.nsome * pl.Hkv;
+  const int64_t want = (units + p.min_units - 1) / p.min_units;
   pl.n = static_cast<int>(want < 1 ? 1 : (want < ncta ? want : ncta));
-  pl.q = quotient(pl.S, pl.n);
-  pl.rem = static_cast<int>(pl.S - pl.q * pl.n);
+  pl.q = quotient(units, pl.n);
+  pl.rem = static_cast<int>(units - pl.q * pl.n);
   return pl;
 }
 

@@ -211,28 +211,28 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
   float2* const factors = reinterpret_cast<float2*>(smem + kShFactors);
   if (warp == 0) tmem_alloc(&s_tmem);
   {  // The rows' codes as f8 in the order of the expanded signs (channel 32 w + 8 j + r at byte 32 w + 4 r + j),
-     // swizzled, and their two factors of the logit; zeros behind the last row.  Two rows of a warp at a time.
+     // swizzled, and their two factors of the logit; zeros behind the last row.  Four rows of a warp at a time.
     const int rows = two ? 256 : 128;
     const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
     #pragma unroll 1
-    for (int r0 = 2 * warp; r0 < rows; r0 += 2 * (kShThreads / 32)) {
-      float x[2][4];
+    for (int r0 = 4 * warp; r0 < rows; r0 += 4 * (kShThreads / 32)) {
+      float x[4][4];
       #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const int row = rt * rows + r0 + i;
         x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
         if (row < s.R) load4(p.q, (static_cast<int64_t>(row / G) * p.Hq + static_cast<int64_t>(h) * G + row % G) * kD + 4 * lane, p.q_dtype, x[i]);
       }
-      if (rt * rows + r0 >= s.R) {  // neither is there
+      if (rt * rows + r0 >= s.R) {  // none is there
         #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
           *reinterpret_cast<uint32_t*>(smem + kShQ + (r0 + i) * 128 + 4 * lane) = 0u;
           if (lane == 0) factors[r0 + i] = make_float2(0.0f, 0.0f);
         }
         continue;
       }
       #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const int r = r0 + i;
         int code[4];
         float vl, dl;
@@ -560,22 +560,42 @@ __global__ void __launch_bounds__(128) paged_shared_merge_kernel(const PagedAtte
   pdl_wait();
   const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x - b * p.c.Hkv, g = blockIdx.y;
   const int64_t out_row = static_cast<int64_t>(b) * p.Hq + static_cast<int64_t>(h) * G + g;
-  const int2 own = p.spread[blockIdx.x];  // first CTA, pieces
-  const float* own0 = own.y == 1 ? p.rows + out_row * kRow : p.part + ((static_cast<int64_t>(own.x) * 2 + 1) * G + g) * kRow;
-  const float* own1 = p.part + ((static_cast<int64_t>(own.x) * 2) * G + g) * kRow;
-  const int64_t step = 2LL * G * kRow;
-  const int r = b * G + g, rows = s.two ? 256 : 128, rt = r / rows, in = r - rt * rows;
-  // the token ranges with tiles are the same number of pieces each: all of them, or as many as there are
-  // tiles; where two lanes share a range's tiles, one tile is the first lane's
+  const int stride = p.packed ? 8 : G;  // rows of a piece
+  // pieces of a segment of the plan: one row of p.rows, or slot 1 of its first CTA and slot 0 of the others
+  struct Seg {
+    const float *first, *rest;
+    int n;
+  };
+  auto segment = [&](int seq, int64_t row, int i) {
+    const int2 at = p.spread[static_cast<int64_t>(seq) * p.c.Hkv + h];
+    Seg s;
+    s.n = at.y;
+    s.first = at.y == 1 ? p.rows + row * kRow : p.part + ((static_cast<int64_t>(at.x) * 2 + 1) * stride + i) * kRow;
+    s.rest = p.part + (static_cast<int64_t>(at.x) * 2 * stride + i) * kRow;
+    return s;
+  };
+  const int64_t step = 2LL * stride * kRow;
+  const Seg own = segment(p.packed + b, out_row, g);
+  const int r = b * G + g;
+  auto own_piece = [&](int i) { return i == 0 ? own.first : own.rest + i * step; };
+  if (p.packed) {
+    const Seg pre = segment(r >> 3, static_cast<int64_t>(p.B) * p.Hq + static_cast<int64_t>(h) * p.B * G + r, r & 7);
+    merge_pieces(own.n + pre.n,
+                 [&](int i) { return i < own.n ? own_piece(i) : (i == own.n ? pre.first : pre.rest + (i - own.n) * step); }, s_head, s_max,
+                 p.out, p.q_dtype, out_row * kD);
+    return;
+  }
+  const int rows = s.two ? 256 : 128, rt = r / rows, in = r - rt * rows;
+  // each token range has the same number of pieces; those without a tile are empty
   const int nt = (prefix_tokens(p, false) + kTile - 1) / kTile;
   const float* base = s.pieces + ((static_cast<int64_t>(h) * s.row_tiles + rt) * s.splits * 256 + in) * kRow;
   const int per = s.two ? 1 : 2;
   auto piece = [&](int i) -> const float* {
-    if (i < own.y) return i == 0 ? own0 : own1 + i * step;
-    i -= own.y;
+    if (i < own.n) return own_piece(i);
+    i -= own.n;
     return base + (per == 1 ? static_cast<int64_t>(i) * 256 : static_cast<int64_t>(i >> 1) * 256 + (i & 1) * 128) * kRow;
   };
-  merge_pieces(own.y + (nt > 0 ? s.splits * per : 0), piece, s_head, s_max, p.out, p.q_dtype, out_row * kD);
+  merge_pieces(own.n + (nt > 0 ? s.splits * per : 0), piece, s_head, s_max, p.out, p.q_dtype, out_row * kD);
 }
 
 }  // namespace paged
@@ -589,7 +609,7 @@ cudaError_t kv1b_launch_paged_shared(const PagedAttendParams& p, const PagedShar
   const auto kernel = fine ? paged::paged_shared_kernel<true> : paged::paged_shared_kernel<false>;
   cudaError_t e = configure_smem(reinterpret_cast<const void*>(kernel), paged::kShSmem, fine ? &configured_fine : &configured);
   if (e != cudaSuccess) return e;
-  const int units = p.c.Hkv * s.row_tiles * s.splits;
+  const int units = p.packed ? 0 : p.c.Hkv * s.row_tiles * s.splits;
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(units + p.ncta)), dim3(paged::kShThreads), paged::kShSmem, stream, p, s, G, units);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged::paged_shared_merge_kernel, dim3(static_cast<unsigned>(p.B) * p.c.Hkv, G), dim3(128), 0, stream, p, s, G);

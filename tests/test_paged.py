@@ -341,6 +341,9 @@ SHARED = [
     (500, [31] * 40, 128, 1, 4),       # more rows than one 128-row tile
     (257, [9] * 33, 256, 2, 8),
     (130, [17] * 300, 32, 1, 1),
+    (2100, [70, 0, 5, 33], 64, 3, 8),  # as many rows as the plain kernel packs
+    (900, [20] * 11, 64, 2, 3),         # one more than that
+    (1500, [3] * 16, 128, 1, 8),        # a full 128-row tile
 ]
 
 
