@@ -95,6 +95,8 @@ struct PagedSharedParams {
   int32_t two;             // a CTA's two lanes hold 256 rows, or 128 rows twice
   int32_t row_tiles;       // of 256 or 128 rows
   int32_t splits;          // token ranges
+  uint8_t* codes;          // [Hkv][R][128] f8
+  float2* factors;         // [Hkv][R]
   float* pieces;           // [Hkv][row_tiles][splits][2][128][2 + 128]
 };
 

@@ -213,6 +213,8 @@ size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int3
   uint8_t* const whole = take((packed ? 2 : 1) * rows * row);
   uint8_t* const spread = take(static_cast<size_t>(Hkv) * (packed + s->R / G) * 8);
   uint8_t* const pieces = take(packed ? 0 : static_cast<size_t>(Hkv) * s->row_tiles * s->splits * 256 * row);
+  uint8_t* const codes = take(packed ? 0 : rows * KV1B_HEAD_DIM);
+  uint8_t* const factors = take(packed ? 0 : rows * 8);
   if (p) {
     p->packed = static_cast<int32_t>(packed);
     // Behind the prefix's CTAs, which take nearly every SM, few CTAs do better than short ones: 56 against 66 us
@@ -223,6 +225,8 @@ size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int3
     p->rows = reinterpret_cast<float*>(whole);
     p->spread = reinterpret_cast<int2*>(spread);
     s->pieces = reinterpret_cast<float*>(pieces);
+    s->codes = codes;
+    s->factors = reinterpret_cast<float2*>(factors);
   }
   return at;
 }

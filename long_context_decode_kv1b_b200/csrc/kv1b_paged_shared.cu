@@ -48,8 +48,7 @@ constexpr int kShV = kShK + kBuf * kKBytes;
 constexpr int kShRaw = kShV + kBuf * kVBytes;
 constexpr int kShNc = kShRaw + kRaw * kRawBytes;     // f32 [kBuf][2][128]: nc, nc I1
 constexpr int kShMask = kShNc + kBuf * 2 * kTile * 4;  // u32 [kBuf][4]: tokens seen
-constexpr int kShFactors = kShMask + kBuf * 16;        // f32 [256][2]
-constexpr int kShSmem = kShFactors + 256 * 8 + 1024;   // and the alignment of the base
+constexpr int kShSmem = kShMask + kBuf * 16 + 1024;    // and the alignment of the base
 static_assert(kRawBytes % 128 == 0 && kShSmem <= 226 * 1024, "shared memory");
 
 // ---- tensor memory and products
@@ -127,6 +126,37 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N]) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// ---------------------------------------------------------------------------------------------
+// Query rows as f8 codes in the order of the expanded signs (channel 32 w + 8 j + r at byte 32 w + 4 r + j),
+// and each row's two factors of the logit.  One warp per row, every row once: the CTAs of the prefix's token
+// ranges preparing their 256 rows each took 24 us before their first product.
+__global__ void __launch_bounds__(256) paged_query_codes_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // [sequence][q head]
+  if (row >= static_cast<int64_t>(p.B) * p.Hq) return;
+  float x[4];
+  load4(p.q, row * kD + 4 * lane, p.q_dtype, x);
+  int code[4];
+  float vl, dl;
+  query_quantise(x, p.c.signs, code, &vl, &dl);
+  const int b = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - static_cast<int64_t>(b) * p.Hq);
+  const int h = hq / G, g = hq - h * G;
+  const int64_t at = static_cast<int64_t>(h) * s.R + static_cast<int64_t>(b) * G + g;
+  uint8_t* bytes = s.codes + at * kD + 32 * (lane >> 3) + 16 * (lane & 1) + ((lane & 7) >> 1);  // channel 4 (lane & 7) of word lane / 8
+  #pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t v = static_cast<uint32_t>(code[r]);
+    const int e = 31 - __clz(v | 1u);
+    bytes[4 * r] = static_cast<uint8_t>(v == 0 ? 0u : static_cast<uint32_t>((7 + e) << 3) | ((v << (3 - e)) & 7u));
+  }
+  if (lane == 0) {
+    const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
+    s.factors[at] = make_float2(__fmul_rn(dl, qs), __fmul_rn(vl, qs));
+  }
+}
+
 __device__ __forceinline__ int prefix_tokens(const PagedAttendParams& p, bool report) {
   const int64_t top = static_cast<int64_t>(p.max_prefix_pages) << (p.c.bpp_shift + 5);
   const int n = __ldg(p.prefix_len);
@@ -171,7 +201,7 @@ __device__ __forceinline__ float row_weights(const uint32_t (&x)[2][32], const f
 }
 
 // Unit u of the prefix's part.
-__device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const PagedSharedParams& s, const int G, const int u, uint8_t* smem) {
+__device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const PagedSharedParams& s, const int u, uint8_t* smem) {
   __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[kBuf], kv_empty[kBuf];
   __shared__ __align__(8) uint64_t s_full[2], turn[2], pv_done[2][2];
   __shared__ uint32_t s_tmem, s_absent[kRaw];
@@ -208,44 +238,14 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
   auto tile_of = [&](int j) { return two ? j >> 1 : j; };
   auto half_of = [&](int w, int j) { return two ? j & 1 : w; };
 
-  float2* const factors = reinterpret_cast<float2*>(smem + kShFactors);
   if (warp == 0) tmem_alloc(&s_tmem);
-  {  // The rows' codes as f8 in the order of the expanded signs (channel 32 w + 8 j + r at byte 32 w + 4 r + j),
-     // swizzled, and their two factors of the logit; zeros behind the last row.  Four rows of a warp at a time.
+  {  // the rows' codes, swizzled; zeros behind the last row
     const int rows = two ? 256 : 128;
-    const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
-    #pragma unroll 1
-    for (int r0 = 4 * warp; r0 < rows; r0 += 4 * (kShThreads / 32)) {
-      float x[4][4];
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = rt * rows + r0 + i;
-        x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
-        if (row < s.R) load4(p.q, (static_cast<int64_t>(row / G) * p.Hq + static_cast<int64_t>(h) * G + row % G) * kD + 4 * lane, p.q_dtype, x[i]);
-      }
-      if (rt * rows + r0 >= s.R) {  // none is there
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          *reinterpret_cast<uint32_t*>(smem + kShQ + (r0 + i) * 128 + 4 * lane) = 0u;
-          if (lane == 0) factors[r0 + i] = make_float2(0.0f, 0.0f);
-        }
-        continue;
-      }
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + i;
-        int code[4];
-        float vl, dl;
-        query_quantise(x[i], p.c.signs, code, &vl, &dl);
-        uint8_t* at = smem + kShQ + r * 128 + (((2 * (lane >> 3) + (lane & 1)) ^ (r & 7)) << 4) + ((lane & 7) >> 1);
-        #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t v = static_cast<uint32_t>(code[c]);
-          const int e = 31 - __clz(v | 1u);
-          at[4 * c] = static_cast<uint8_t>(v == 0 ? 0u : static_cast<uint32_t>((7 + e) << 3) | ((v << (3 - e)) & 7u));
-        }
-        if (lane == 0) factors[r] = make_float2(__fmul_rn(dl, qs), __fmul_rn(vl, qs));
-      }
+    for (int e = threadIdx.x; e < rows * 8; e += kShThreads) {
+      const int r = e >> 3, c = e & 7, row = rt * rows + r;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (row < s.R) v = *reinterpret_cast<const uint4*>(s.codes + (static_cast<int64_t>(h) * s.R + row) * kD + 16 * c);
+      *reinterpret_cast<uint4*>(smem + kShQ + r * 128 + ((c ^ (r & 7)) << 4)) = v;
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -268,7 +268,7 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
     const int row = rt * (two ? 256 : 128) + (two ? w * 128 : 0) + r;
     const bool warp_rows = row - lane < s.R;  // a warp without rows only keeps the barriers going
     const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 256, tO = tS + 128;
-    const float2 f = factors[(two ? w * 128 : 0) + r];
+    const float2 f = row < s.R ? s.factors[static_cast<int64_t>(h) * s.R + row] : make_float2(0.0f, 0.0f);
     const uint64_t fa = pair(f.x, f.x), fb = pair(f.y, f.y);
     float m = 0.0f, l = 0.0f;
     bool have = false;  // a finite logit has set m
@@ -541,15 +541,14 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
 }
 
 // The prefix's units, then the CTAs of the sequences' own tokens: where the prefix leaves SMs idle the two
-// parts run side by side.  (Four launches one after another, the queries' codes first: 37 instead of @SMALL@ us for
-// 4 sequences of 61 tokens behind 1,000.)
+// parts run side by side.
 template <bool kFine>
 __global__ void __launch_bounds__(kShThreads, 1) paged_shared_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G,
                                                                       const int units) {
   static_assert(kShThreads == kThreads && kSmem <= kShSmem, "one launch for both parts");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  if (static_cast<int>(blockIdx.x) < units) prefix_cta(p, s, G, blockIdx.x, smem);
+  if (static_cast<int>(blockIdx.x) < units) prefix_cta(p, s, blockIdx.x, smem);
   else attend_cta<kFine>(p, G, blockIdx.x - units, smem);
 }
 
@@ -610,6 +609,11 @@ cudaError_t kv1b_launch_paged_shared(const PagedAttendParams& p, const PagedShar
   cudaError_t e = configure_smem(reinterpret_cast<const void*>(kernel), paged::kShSmem, fine ? &configured_fine : &configured);
   if (e != cudaSuccess) return e;
   const int units = p.packed ? 0 : p.c.Hkv * s.row_tiles * s.splits;
+  if (units) {
+    const int64_t rows = static_cast<int64_t>(p.B) * p.Hq;
+    e = launch_pdl(paged::paged_query_codes_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p, s, G);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(units + p.ncta)), dim3(paged::kShThreads), paged::kShSmem, stream, p, s, G, units);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged::paged_shared_merge_kernel, dim3(static_cast<unsigned>(p.B) * p.c.Hkv, G), dim3(128), 0, stream, p, s, G);
