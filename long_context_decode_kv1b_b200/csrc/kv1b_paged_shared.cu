@@ -273,30 +273,25 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
     float m = 0.0f, l = 0.0f;
     bool have = false;  // a finite logit has set m
     bool cold = true;   // not in all of the warp's rows
-    uint32_t x[2][32];
-    uint2 seen;  // of the job's tokens
-    // Sums of the next job into registers, with the wait in the same straight line: nothing may copy the
-    // registers of a load in flight.  Warps without rows load and store along, in rows that nobody reads.
-    auto load_sums = [&]() {
+    for (int j = 0; j < jobs; ++j) {
+      const int k = tile_of(j), buf = k % kBuf, half = half_of(w, j), slot = j & 1;
+      // The commit of the job's scores covers the products issued before them, P V of job j - 2 among them, so
+      // P's place is free; and the tile's factors and masks were written before the products' warp waited for
+      // the tile.
+      if (!wait(&s_full[w], j & 1)) break;
+      tc_after();
+      // (The wait for a load follows it in a straight line: nothing may copy the registers of a load in
+      // flight.  Warps without rows load and store along, in rows that nobody reads.)
+      uint32_t x[2][32];
       tmem_ld32(x[0], tS);
       tmem_ld32(x[1], tS + 32);
-    };
-    auto sums_loaded = [&](int j) {
-      seen = *(reinterpret_cast<const uint2*>(smem + kShMask) + (tile_of(j) % kBuf) * 2 + half_of(w, j));
+      const uint2 seen = *(reinterpret_cast<const uint2*>(smem + kShMask) + buf * 2 + half);  // the job's tokens
       tmem_ld_wait(x[0]);
       tmem_ld_wait(x[1]);
       tmem_st_wait();
       tc_before();
       __syncwarp();
-      if (elect()) mbar_arrive(&turn[w]);
-    };
-    if (wait(&s_full[w], 0)) {
-      tc_after();
-      load_sums();
-      sums_loaded(0);
-    }
-    for (int j = 0; ok && j < jobs; ++j) {
-      const int k = tile_of(j), buf = k % kBuf, half = half_of(w, j), slot = j & 1;
+      if (elect()) mbar_arrive(&turn[w]);  // S of job j has been read, P of job j - 1 written
       uint32_t pw[32];
       if (!warp_rows) {
         #pragma unroll
@@ -344,18 +339,15 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
         l = __fadd_rn(l, sum);
       }
       if (!ok) break;
-      // The next scores' commit covers the products issued before them, P V of job j - 2 among them, so P's
-      // place is free; and the tile's factors and masks were written before the products' warp waited for
-      // the tile.  The commit follows all four warps' turn j; behind the last job, where no scores come, a
-      // warp waits for that turn itself before it arrives for the next.
-      const bool more = j + 1 < jobs;
-      if (!wait(more ? &s_full[w] : &turn[w], more ? (j + 1) & 1 : j & 1)) break;
-      if (!more && j >= 2 && !wait(&pv_done[w][slot], ((j >> 1) - 1) & 1)) break;
-      tc_after();
-      load_sums();  // behind the last job: once more, unused
       tmem_st16(tS + kHalf + 32 * slot, pw);
       tmem_st16(tS + kHalf + 32 * slot + 16, pw + 16);
-      sums_loaded(more ? j + 1 : j);
+    }
+    // the last P, not before all four warps' last turn
+    if (ok && wait(&turn[w], (jobs - 1) & 1)) {
+      tmem_st_wait();
+      tc_before();
+      __syncwarp();
+      if (elect()) mbar_arrive(&turn[w]);
     }
     // the lane's sums
     if (ok && wait(&pv_done[w][(jobs - 1) & 1], ((jobs - 1) >> 1) & 1)) {
@@ -518,19 +510,20 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
     scores(0);
     for (int j = 0; ok && j <= jobs; ++j) {  // S of job j has been read and P of job j - 1 written
       if (!wait(&turn[w], j & 1)) break;
-      if (j + 1 < jobs) scores(j + 1);
-      if (!ok || j == 0) continue;
-      const int i = j - 1, half = half_of(w, i), slot = i & 1, buf = tile_of(i) % kBuf;
-      tc_after();
-      if (elect()) {
-        const uint64_t b = operand(sb + kShV + buf * kVBytes + half * (kVBytes / 2));
-        #pragma unroll
-        for (int c = 0; c < 4; ++c)  // 16 tokens each
-          mma_f16_ta(tmem + w * 256 + 128, tmem + w * 256 + kHalf + 32 * slot + 8 * c, b + 2 * c, i > 0 || c > 0);
-        tc_commit(&pv_done[w][slot]);
-        if (!two || half == 1) tc_commit(&kv_empty[buf]);
+      if (j > 0) {
+        const int i = j - 1, half = half_of(w, i), slot = i & 1, buf = tile_of(i) % kBuf;
+        tc_after();
+        if (elect()) {
+          const uint64_t b = operand(sb + kShV + buf * kVBytes + half * (kVBytes / 2));
+          #pragma unroll
+          for (int c = 0; c < 4; ++c)  // 16 tokens each
+            mma_f16_ta(tmem + w * 256 + 128, tmem + w * 256 + kHalf + 32 * slot + 8 * c, b + 2 * c, i > 0 || c > 0);
+          tc_commit(&pv_done[w][slot]);
+          if (!two || half == 1) tc_commit(&kv_empty[buf]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if (j + 1 < jobs) scores(j + 1);
     }
   }
   if (!ok && lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_TIMEOUT);
