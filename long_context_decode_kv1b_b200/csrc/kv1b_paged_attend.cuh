@@ -51,6 +51,7 @@ struct Seg {
   int base, nb;  // first block (below 0 where the CTA's range begins inside the segment), blocks
   int b, h;
   int k;         // place of b among the sequences that see a block
+  int skip_from, skip_to, pad;  // Visible
 };
 
 constexpr int kOffPre = kWarps * kStages * kBlkBytes;            // u32 [kMaxSeqs + 1] blocks before each sequence
@@ -66,53 +67,47 @@ constexpr int kOffRed = 0;                                       // f32 [kWarps]
 static_assert(kOffPre % 16 == 0 && kOffRows % 16 == 0 && kWarps * KV1B_MAX_GROUP * kRow * 4 <= kOffPre && kSmem + 2048 <= 227 * 1024, "shared memory");
 
 // Block i of a segment: its place in the sequence.
-__device__ __forceinline__ int own_block(const Visible& v, int j) { return j < v.skip_from ? j : j + (v.skip_to - v.skip_from); }
+__device__ __forceinline__ int own_block(const Seg& g, int i) { return i < g.skip_from ? i : i + (g.skip_to - g.skip_from); }
 
 // The copy side's place in a round's blocks.  Stretches of blocks that lie behind one another in a page
-// are walked by a pointer; the page entry of the next stretch is loaded when one begins.
+// are walked by a pointer; the page entry of the next stretch is loaded when one begins.  What follows from
+// the segment is read from shared memory when it is needed: registers are what the loop is short of.
 struct Ahead {
   const uint8_t* ptr;  // next block, null where the page is not there
   int in;              // blocks of the stretch that are left
   int left;            // blocks of the warp's run behind the stretch
   int s, i;            // segment and block behind the stretch
-  int b, h, nb;
-  Visible vis;
   int page;            // page entry there
-  __device__ __forceinline__ void enter(const Seg* seg, const Plan& pl, const PagedAttendParams& p) {
+  __device__ __forceinline__ void look_up(const Seg& g, const PagedAttendParams& p) {
+    const int32_t* list = g.b < p.packed ? p.prefix_pages : p.table + (g.b - p.packed) * p.table_stride;
+    page = __ldg(list + (own_block(g, i) >> p.c.bpp_shift));
+  }
+  __device__ __forceinline__ void next_stretch(const Seg* seg, const PagedAttendParams& p) {
     const Seg g = seg[s];
-    b = g.b;
-    h = g.h;
-    nb = g.nb;
-    vis = visible(pl.len[b], p.window, p.sinks);
-  }
-  __device__ __forceinline__ void look_up(const PagedAttendParams& p) {
-    const int32_t* list = b < p.packed ? p.prefix_pages : p.table + (b - p.packed) * p.table_stride;
-    page = __ldg(list + (own_block(vis, i) >> p.c.bpp_shift));
-  }
-  __device__ __forceinline__ void next_stretch(const Seg* seg, const Plan& pl, const PagedAttendParams& p) {
-    const int blk = own_block(vis, i), off = blk & ((1 << p.c.bpp_shift) - 1);
+    const int off = own_block(g, i) & ((1 << p.c.bpp_shift) - 1);
     const bool ok = page >= 0 && page < p.c.num_pages;
-    ptr = ok ? p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + h) << p.c.bpp_shift) + off) * kBlkBytes) : nullptr;
+    ptr = ok ? p.c.pages + ((((static_cast<int64_t>(page) * p.c.Hkv + g.h) << p.c.bpp_shift) + off) * kBlkBytes) : nullptr;
     if (!ok && (threadIdx.x & 31) == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
-    in = min(min((1 << p.c.bpp_shift) - off, nb - i), left);
-    if (i < vis.skip_from) in = min(in, vis.skip_from - i);
+    in = min(min((1 << p.c.bpp_shift) - off, g.nb - i), left);
+    if (i < g.skip_from) in = min(in, g.skip_from - i);
     left -= in;
     i += in;
     if (left > 0) {
-      if (i == nb) {
+      if (i == g.nb) {
         ++s;
         i = 0;
-        enter(seg, pl, p);
+        look_up(seg[s], p);
+      } else {
+        look_up(g, p);
       }
-      look_up(p);
     }
   }
 };
 
 // The first block from i on of which the query may see only a part: where the sinks end, where the window
 // begins (the first block of all where there is none), the last one.
-__device__ __forceinline__ int next_edge(const Visible& v, int i, int nb) {
-  return i < v.skip_from ? v.skip_from - 1 : (i == v.skip_from ? i : nb - 1);
+__device__ __forceinline__ int next_edge(const Seg& g, int i) {
+  return i < g.skip_from ? g.skip_from - 1 : (i == g.skip_from ? i : g.nb - 1);
 }
 
 constexpr float kCodeUnit = 16777216.0f;  // codes enter the products as binary16 subnormals, units of 2^-24
@@ -155,7 +150,12 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
   pdl_launch_dependents();
   float* signs = reinterpret_cast<float*>(smem + kOffSigns);
   if (threadIdx.x < KV1B_MAX_ROUNDS * kD) signs[threadIdx.x] = __ldg(p.c.signs + threadIdx.x);
-  const Plan pl = make_plan<kThreads>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), p.ncta, cta == 0);
+  __shared__ Plan pl;
+  {
+    const Plan mine = make_plan<kThreads>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), p.ncta, cta == 0);
+    if (threadIdx.x == 0) pl = mine;
+    __syncthreads();
+  }
 
   // sequences that see nothing: zeros
   for (int b = p.rows ? p.B : cta; b < p.B; b += p.ncta)  // (none are packed here)
@@ -205,7 +205,11 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
           const int nb = pl.blocks(k);
           const int64_t base = pl.first_block(k) + static_cast<int64_t>(h) * nb;
           valid = base < r1;
-          if (valid) seg[threadIdx.x] = {static_cast<int>(base - a), nb, pl.some[k], h, k};
+          if (valid) {
+            const int b = pl.some[k];
+            const Visible v = visible(pl.len[b], p.window, p.sinks);
+            seg[threadIdx.x] = {static_cast<int>(base - a), nb, b, h, k, v.skip_from, v.skip_to, 0};
+          }
         }
       }
       nseg = __syncthreads_count(valid);
@@ -246,7 +250,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     ahead.left = w1 - w0;
     uint32_t absent = 0;  // bit s: stage s holds no block (its page is outside the cache)
     auto issue = [&](int s) {
-      if (ahead.in == 0) ahead.next_stretch(seg, pl, p);
+      if (ahead.in == 0) ahead.next_stretch(seg, p);
       absent = ahead.ptr ? absent & ~(1u << s) : absent | (1u << s);
       if (ahead.ptr) {
         if (lane == 0) block_g2s(ring + s * kBlkBytes, ahead.ptr, &bars[warp][s]);
@@ -254,7 +258,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       }
       --ahead.in;
     };
-    struct { int s, i, left, b, h, nb; Visible vis; } cur = {0, 0, w1 - w0, 0, 0, 0, {0, 0, 0}};
+    struct { int s, i, left; } cur = {0, 0, w1 - w0};
     if (cur.left > 0) {
       int k = 0;  // the segment of block w0
       for (int x = lane; x < nseg; x += 32)
@@ -262,9 +266,9 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       k = __reduce_max_sync(kFull, k);
       ahead.s = k;
       ahead.i = w0 - seg[k].base;
-      ahead.enter(seg, pl, p);
-      ahead.look_up(p);
-      cur = {k, ahead.i, cur.left, ahead.b, ahead.h, ahead.nb, ahead.vis};
+      ahead.look_up(seg[k], p);
+      cur.s = k;
+      cur.i = ahead.i;
       for (int s = 0; s < kStages && ahead.in + ahead.left > 0 && !gave_up; ++s) issue(s);
     }
 
@@ -297,7 +301,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     };
     // the warp's sums of a segment to a piece [head][kRow]
     auto put_piece = [&](float* w) {
-      const int n_heads = heads.count(cur.b);
+      const int n_heads = heads.count(seg[cur.s].b);
       if (t == 0 && g < n_heads) w[g * kRow] = m;
       #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -322,7 +326,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       float4 cc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       {
         uint32_t pw[4] = {0u, 0u, 0u, 0u};
-        if (g < heads.count(cur.b)) {
+        if (g < heads.count(seg[cur.s].b)) {
           #pragma unroll
           for (int j = 0; j < 4; ++j) pw[j] = planes[((cur.s * G + g) * 4 + j) * 4 + t];
           cc = consts[cur.s * G + g];
@@ -346,9 +350,9 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       bool fresh = true;   // no block has set m
       int top_scale = 0;   // weights are 2^-top_scale lower: no scale reaches 2^(1 + top_scale)
       const bool starts = cur.i == 0;
-      const int count = min(cur.left, cur.nb - cur.i);  // blocks of the segment in the warp's run
-      const bool ends = cur.i + count == cur.nb;
-      int edge_at = next_edge(cur.vis, cur.i, cur.nb);
+      const int count = min(cur.left, seg[cur.s].nb - cur.i);  // blocks of the segment in the warp's run
+      const bool ends = cur.i + count == seg[cur.s].nb;
+      int edge_at = next_edge(seg[cur.s], cur.i);
 
       for (int x = cur.i; x < cur.i + count; ++x) {
         const uint32_t st = ring + stage * kBlkBytes;
@@ -361,7 +365,8 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
             // which of the block's tokens the query sees.  Unseen ones: what their places hold (another
             // sequence's remains, infinities) must not reach a product, so their scale, min and norm
             // become zeros and their weights are zero
-            const int len = pl.len[cur.b], tk = own_block(cur.vis, x) * kBlkTok + lane;
+            const Seg& sg = seg[cur.s];
+            const int len = pl.len[sg.b], tk = own_block(sg, x) * kBlkTok + lane;
             const int wstart = (p.window > 0 && len > p.window) ? len - p.window : 0;
             const bool on = tk < len && (tk >= wstart || tk < p.sinks);
             seen = __ballot_sync(kFull, on);
@@ -376,7 +381,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy to the stage
             }
             __syncwarp();
-            edge_at = next_edge(cur.vis, x + 1, cur.nb);
+            edge_at = next_edge(sg, x + 1);
           }
           // ---- scores
           float dot[8];
@@ -403,20 +408,13 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
               }
             }
           }
-          uint32_t sc[4][4];
-          #pragma unroll
-          for (int q = 0; q < 4; ++q) lds128(sc[q], st + kBlkOffScale + q * 64 + 16 * t);
           {
-            uint32_t any = 0;  // a scale of 2 or more has the top exponent bit
-            #pragma unroll
-            for (int q = 0; q < 4; ++q) any |= sc[q][0] | sc[q][1] | sc[q][2] | sc[q][3];
-            if (__any_sync(kFull, (any & 0x40004000u) != 0)) {  // rare: large values
-              int k = 0;
-              #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  k = max(k, max(static_cast<int>(sc[q][i] & 0x7C00u), static_cast<int>((sc[q][i] >> 16) & 0x7C00u)));
+            // the block's 128 scales, four a lane: one of 2 or more has the top exponent bit
+            uint32_t w0, w1;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(st + kBlkOffScale + 8 * lane) : "memory");
+            if (__any_sync(kFull, ((w0 | w1) & 0x40004000u) != 0)) {  // rare: large values
+              int k = max(max(static_cast<int>(w0 & 0x7C00u), static_cast<int>((w0 >> 16) & 0x7C00u)),
+                          max(static_cast<int>(w1 & 0x7C00u), static_cast<int>((w1 >> 16) & 0x7C00u)));
               k = __reduce_max_sync(kFull, (k >> 10) - 15);  // all scales are below 2^(1 + k)
               if (k > top_scale) {
                 const float f = ex2(static_cast<float>(top_scale - k));
@@ -444,7 +442,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
             #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] = (mine >> j) & 1u ? y[j] : -INFINITY;
           }
-          float mx = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+          float mx = fmaxf(max3(max3(y[0], y[1], y[2]), y[3], y[4]), max3(y[5], y[6], y[7]));
           const float bar = kBase + kTau - static_cast<float>(top_scale);
           if (__any_sync(kFull, mx > bar) || fresh) {  // rare: raise references
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
@@ -481,12 +479,13 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
           // ---- P.V, value group by value group (32 channels: rows of two products)
           #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t cw[4], wt[4], rest[4];
+            uint32_t cw[4], sc[4], wt[4], rest[4];
+            lds128(sc, st + kBlkOffScale + q * 64 + 16 * t);
             ldsm_x4(cw, st + kBlkOffCodes + (32 * q + lane) * 16);  // rows g, g + 8, g + 16, g + 24; word t
             #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              wt[i] = hmul2(pw[i], sc[q][i]);
-              if (kFine) rest[i] = hfma2(pw[i], sc[q][i], wt[i] ^ 0x80008000u);
+              wt[i] = hmul2(pw[i], sc[i]);
+              if (kFine) rest[i] = hfma2(pw[i], sc[i], wt[i] ^ 0x80008000u);
             }
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -512,9 +511,10 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       cur.left -= count;
 
       if (starts && ends) {  // all of it: finished here
-        const int64_t qrow = heads.query(cur.b, cur.h, 0);
+        const Seg& sg = seg[cur.s];
+        const int64_t qrow = heads.query(sg.b, sg.h, 0);
         if (p.rows) {
-          put_piece(p.rows + heads.row(cur.b, cur.h) * kRow);
+          put_piece(p.rows + heads.row(sg.b, sg.h) * kRow);
         } else {
           #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -536,12 +536,8 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
         last = true;
       }
       if (cur.left > 0) {
-        const Seg next = seg[++cur.s];
+        ++cur.s;
         cur.i = 0;
-        cur.b = next.b;
-        cur.h = next.h;
-        cur.nb = next.nb;
-        cur.vis = visible(pl.len[cur.b], p.window, p.sinks);
       }
     }
 
@@ -581,8 +577,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       }
       float M = head.x;
       #pragma unroll
-      for (int o = 8; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-      M = __shfl_sync(kFull, M, 0);  // lanes 0 .. 15 hold the pieces
+      for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
       const float f = ex2(head.x - M);
       float num[4] = {0.0f, 0.0f, 0.0f, 0.0f}, den = 0.0f;
       #pragma unroll 4
