@@ -78,7 +78,7 @@ struct PagedAttendParams {
   int32_t max_prefix_pages;
   void* out;               // q_dtype [B][Hq][128]
   float* part;             // [ctas][2][G][2 + 128]
-  float* first;            // [ctas][16 warps][G][2 + 128]: ends of segments inside a warp's run
+  float* first;            // [ctas][kAttendWarps][G][2 + 128]: ends of segments inside a warp's run
   float* rows;             // null, or [B][Hq][2 + 128] and, packed, [Hkv][B G][2 + 128]: whole segments leave
                            // (m, l, o) here, none is normalised
   int2* spread;            // [ctas] first output row and pieces of the segment a range boundary cuts, or with
@@ -87,6 +87,7 @@ struct PagedAttendParams {
   int32_t min_units;       // blocks and what segments count besides (kSegUnits each) that a CTA takes at least
 };
 
+constexpr int kAttendWarps = 12;  // of a CTA of the attend's kernel
 constexpr int kPackedRows = 32;  // rows of a kv-head up to which the attend's kernel takes the prefix
 
 // The queries of a kv-head as the rows of one matrix: R = B G rows, row b G + g.

@@ -165,7 +165,7 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
 size_t kv1b_paged_attend_workspace_bytes(const kv1b_paged_t* cache, int32_t num_q_heads) {
   if (!paged_ok(cache) || heads_check(cache, num_q_heads) != KV1B_OK) return 0;
   const size_t G = num_q_heads / cache->num_kv_heads;
-  const size_t n = static_cast<size_t>(num_sms()) * ((2 + 16) * G * kv1b::kPartStride * 4 + 8);  // part, first, spread
+  const size_t n = static_cast<size_t>(num_sms()) * ((2 + kv1b::kAttendWarps) * G * kv1b::kPartStride * 4 + 8);  // part, first, spread
   return (n + 255) / 256 * 256;
 }
 
@@ -209,7 +209,7 @@ size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int3
     return here;
   };
   uint8_t* const part = take(static_cast<size_t>(num_sms()) * 2 * n * row);
-  uint8_t* const first = take(static_cast<size_t>(num_sms()) * 16 * n * row);
+  uint8_t* const first = take(static_cast<size_t>(num_sms()) * kv1b::kAttendWarps * n * row);
   uint8_t* const whole = take((packed ? 2 : 1) * rows * row);
   uint8_t* const spread = take(static_cast<size_t>(Hkv) * (packed + s->R / G) * 8);
   uint8_t* const pieces = take(packed ? 0 : static_cast<size_t>(Hkv) * s->row_tiles * s->splits * 256 * row);
@@ -282,7 +282,7 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   p.min_units = 16;
   p.part = static_cast<float*>(ws);
   p.first = p.part + static_cast<size_t>(p.ncta) * 2 * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride;
-  p.spread = reinterpret_cast<int2*>(p.first + static_cast<size_t>(p.ncta) * 16 * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride);
+  p.spread = reinterpret_cast<int2*>(p.first + static_cast<size_t>(p.ncta) * kv1b::kAttendWarps * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride);
   const int32_t G = num_q_heads / cache->num_kv_heads;
   if (!prefix_pages) return cuda_status(kv1b_launch_paged_attend(p, G, static_cast<cudaStream_t>(stream)));
   kv1b::PagedSharedParams s =

@@ -31,6 +31,8 @@
 // Range: p = 2^(x - m + kBase) <= 2^15 and scale < 2 keep p scale finite; a block with a larger scale lowers
 // the weights by its power of two.  A weight keeps 11 bits down to 2^-21 of the reference.
 //
+// 12 warps: their 168 registers hold the loop's sums, operands and addresses, where 16 warps' 128 spilled; 8 warps
+// of 255 hid less of the products' latency (178, 190 and 222 us for 1M tokens x 8 heads).
 // 609 warp instructions a block (values expanded to binary16 by fma, a page entry and an address per
 // block) became about 330: the issue slots were 64 % busy at 243 us for 1M tokens x 8 heads.
 #pragma once
@@ -39,9 +41,9 @@
 namespace kv1b {
 namespace paged {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = kAttendWarps;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 
 constexpr int kQuerySlots = 256;  // prepared query rows a round holds
 constexpr int kMaxSegs = 64;      // segments a round holds
@@ -149,7 +151,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
   pdl_wait();
   pdl_launch_dependents();
   float* signs = reinterpret_cast<float*>(smem + kOffSigns);
-  if (threadIdx.x < KV1B_MAX_ROUNDS * kD) signs[threadIdx.x] = __ldg(p.c.signs + threadIdx.x);
+  for (int i = threadIdx.x; i < KV1B_MAX_ROUNDS * kD; i += kThreads) signs[i] = __ldg(p.c.signs + i);
   __shared__ Plan pl;
   {
     const Plan mine = make_plan<kThreads>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), p.ncta, cta == 0);

@@ -538,11 +538,16 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
 template <bool kFine>
 __global__ void __launch_bounds__(kShThreads, 1) paged_shared_kernel(const PagedAttendParams p, const PagedSharedParams s, const int G,
                                                                       const int units) {
-  static_assert(kShThreads == kThreads && kSmem <= kShSmem, "one launch for both parts");
+  static_assert(kThreads == 384 && kShThreads == 512 && kSmem <= kShSmem, "one launch for both parts");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   if (static_cast<int>(blockIdx.x) < units) prefix_cta(p, s, blockIdx.x, smem);
-  else attend_cta<kFine>(p, G, blockIdx.x - units, smem);
+  else if (threadIdx.x < kThreads) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(160));  // 3 x 160 + 32 = 4 x 128
+    attend_cta<kFine>(p, G, blockIdx.x - units, smem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(32));
+  }
 }
 
 // One (sequence, kv-head, query head) per block: the sequence's own pieces and the prefix's.
