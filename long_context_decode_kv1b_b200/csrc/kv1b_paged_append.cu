@@ -174,7 +174,7 @@ __device__ __forceinline__ uint64_t products(uint64_t a, uint64_t b) {
 // Query rows [h0, h1) of token t by the calling warp, a row by 16 lanes.  A lane holds four pairs of each of
 // its rows, so that nothing is exchanged (channels a .. a + 3 and b .. b + 3: a row's pairs in order, then what
 // is not turned); the token's factors are read once for all rows, sixteen of which are in flight.
-template <int DT>
+template <int DT, bool INTERLEAVED>
 __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t, int h0, int h1) {
   typedef typename Elem<DT>::T E;
   typedef typename Four<DT>::Raw Raw;
@@ -189,7 +189,7 @@ __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t
       return;
     }
     if (in) {
-      if (!p.interleaved) a = first, b = first + half;
+      if (!INTERLEAVED) a = first, b = first + half;
       #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float* row = factor_row(p, ps, first + i) + first + i;
@@ -202,7 +202,7 @@ __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t
   E* out = static_cast<E*>(p.q_out) + t * p.qo_st;
   constexpr int kSteps = 8;  // two rows each
   #pragma unroll 1
-  for (int h = h0 + (lane >> 4); h < h1; h += 2 * kSteps) {
+  for (int left = h1 - h0, h = h0 + (lane >> 4); left > 0; left -= 2 * kSteps, h += 2 * kSteps) {  // alike for both rows' lanes
     Raw ra[kSteps], rb[kSteps];
     #pragma unroll
     for (int k = 0; k < kSteps; ++k) {  // behind the last row: it again
@@ -212,32 +212,23 @@ __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t
     }
     #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
-      if (h + 2 * k >= h1) break;
-      if (in) {
-        float x[8];
-        Four<DT>::get(ra[k], x);
-        Four<DT>::get(rb[k], x + 4);
-        const uint64_t c0 = pair(cs[0], cs[1]), c1 = pair(cs[2], cs[3]);
-        const uint64_t s0 = pair(sn[0], sn[1]), s1 = pair(sn[2], sn[3]), n0 = pair(-sn[0], -sn[1]), n1 = pair(-sn[2], -sn[3]);
-        if (p.interleaved) {
-          const uint64_t u0 = pair(x[0], x[2]), v0 = pair(x[1], x[3]), u1 = pair(x[4], x[6]), v1 = pair(x[5], x[7]);
-          unpair(add2(products(u0, c0), products(v0, n0)), x[0], x[2]);
-          unpair(add2(products(v0, c0), products(u0, s0)), x[1], x[3]);
-          unpair(add2(products(u1, c1), products(v1, n1)), x[4], x[6]);
-          unpair(add2(products(v1, c1), products(u1, s1)), x[5], x[7]);
-        } else {
-          const uint64_t u0 = pair(x[0], x[1]), v0 = pair(x[4], x[5]), u1 = pair(x[2], x[3]), v1 = pair(x[6], x[7]);
-          unpair(add2(products(u0, c0), products(v0, n0)), x[0], x[1]);
-          unpair(add2(products(v0, c0), products(u0, s0)), x[4], x[5]);
-          unpair(add2(products(u1, c1), products(v1, n1)), x[2], x[3]);
-          unpair(add2(products(v1, c1), products(u1, s1)), x[6], x[7]);
-        }
-        ra[k] = Four<DT>::put(x);
-        rb[k] = Four<DT>::put(x + 4);
+      float x[8];
+      Four<DT>::get(ra[k], x);
+      Four<DT>::get(rb[k], x + 4);
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) {  // pair i: its members in x
+        float& u = x[INTERLEAVED ? 2 * i : i];
+        float& v = x[INTERLEAVED ? 2 * i + 1 : 4 + i];
+        const float un = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
+        v = __fadd_rn(__fmul_rn(v, cs[i]), __fmul_rn(u, sn[i]));
+        u = un;
       }
-      E* row = out + (h + 2 * k) * p.qo_sh;
-      *reinterpret_cast<Raw*>(row + a) = ra[k];
-      *reinterpret_cast<Raw*>(row + b) = rb[k];
+      const Raw ta = Four<DT>::put(x), tb = Four<DT>::put(x + 4);
+      if (h + 2 * k < h1) {  // what is not turned goes through as it is
+        E* row = out + (h + 2 * k) * p.qo_sh;
+        *reinterpret_cast<Raw*>(row + a) = in ? ta : ra[k];
+        *reinterpret_cast<Raw*>(row + b) = in ? tb : rb[k];
+      }
     }
   }
 }
@@ -516,7 +507,7 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(32 * Prefill<DT>::kWarps, 20 / Prefill<DT>::kWarps) paged_append_prefill_kernel(const PagedAppendParams p, const int64_t kv_blocks,
+__global__ void __launch_bounds__(32 * Prefill<DT>::kWarps, 20 / Prefill<DT>::kWarps) paged_append_prefill_kernel(const PagedAppendParams p, const uint32_t kv_share,
                                                                                        const int heads_per_warp) {
   typedef typename Elem<DT>::T T;
   typedef Prefill<DT> F;
@@ -526,17 +517,19 @@ __global__ void __launch_bounds__(32 * Prefill<DT>::kWarps, 20 / Prefill<DT>::kW
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tau = lane >> 2, j = lane & 3;
   // Blocks of keys and values, which are bound by their instructions, and blocks of queries, by memory,
-  // are spread evenly among one another: both kinds run on every SM at all times.
-  const int64_t u = blockIdx.x, kv0 = u * kv_blocks / gridDim.x;
-  if ((u + 1) * kv_blocks / gridDim.x == kv0) {
-    const int chunks = (p.Hq + kQueryHeads - 1) / kQueryHeads;
-    const int64_t unit = (u - kv0) * F::kWarps + warp, t = unit / chunks;
-    if (t >= p.T || t >= __ldg(p.cu + p.B)) return;
+  // are spread evenly among one another: both kinds run on every SM at all times.  kv_share is the keys' share
+  // of the blocks in units of 2^-32, rounded up (0: all), and block u theirs where its multiple passes a whole.
+  const uint32_t u = blockIdx.x, kv0 = kv_share ? __umulhi(u, kv_share) : u;
+  if (kv_share && __umulhi(u + 1, kv_share) == kv0) {
+    const uint32_t chunks = (p.Hq + kQueryHeads - 1) / kQueryHeads;
+    const uint32_t unit = (u - kv0) * F::kWarps + warp, t = unit / chunks;
+    if (t >= static_cast<uint32_t>(p.T) || static_cast<int>(t) >= __ldg(p.cu + p.B)) return;
     const int h0 = static_cast<int>(unit - t * chunks) * kQueryHeads;
-    query_rows<DT>(p, t, h0, min(h0 + kQueryHeads, p.Hq));
+    if (p.interleaved) query_rows<DT, true>(p, t, h0, min(h0 + kQueryHeads, p.Hq));
+    else query_rows<DT, false>(p, t, h0, min(h0 + kQueryHeads, p.Hq));
     return;
   }
-  const int head_chunks = (p.c.Hkv + heads_per_warp - 1) / heads_per_warp;
+  const uint32_t head_chunks = (p.c.Hkv + heads_per_warp - 1) / heads_per_warp;
   const int gi = static_cast<int>(kv0 / head_chunks) * F::kWarps + warp;
   if (gi >= p.groups) return;
   int h = static_cast<int>(kv0 % head_chunks) * heads_per_warp;
@@ -796,8 +789,9 @@ static cudaError_t launch_prefill(const PagedAppendParams& p, int heads, cudaStr
   constexpr int kWarps = paged::Prefill<DT>::kWarps;
   const int64_t kv_blocks = static_cast<int64_t>((p.groups + kWarps - 1) / kWarps) * ((p.c.Hkv + heads - 1) / heads);
   const int64_t rows = p.q ? static_cast<int64_t>(p.T) * ((p.Hq + paged::kQueryHeads - 1) / paged::kQueryHeads) : 0;
-  const dim3 grid(static_cast<unsigned>(kv_blocks + (rows + kWarps - 1) / kWarps));
-  return launch_pdl(paged::paged_append_prefill_kernel<DT>, grid, dim3(32 * kWarps), 0, stream, p, kv_blocks, heads);
+  const int64_t blocks = kv_blocks + (rows + kWarps - 1) / kWarps;  // below 2^30: the API limits the rows
+  const uint32_t kv_share = blocks == kv_blocks ? 0u : static_cast<uint32_t>(((kv_blocks << 32) + blocks - 1) / blocks);
+  return launch_pdl(paged::paged_append_prefill_kernel<DT>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), 0, stream, p, kv_share, heads);
 }
 
 cudaError_t kv1b_launch_paged_append(const PagedAppendParams& p, cudaStream_t stream) {
