@@ -384,7 +384,7 @@ int kv1b_paged_signs(float* signs, uint64_t seed, int32_t rounds, int32_t* d_sta
  * rope: NULL for none; positions: i32, token row t on axis a at positions[a*pos_stride + t].
  * q, q_out: NULL, or the queries (element (t, h, c) at q[t*q_stride_t + h*q_stride_h + c], h <
  *   num_q_heads) and where their turned rows go, in `dtype` (copied when rope is NULL; q_out may be q
- *   with the same strides).
+ *   with the same strides; its rows may not overlap).
  * Encoded as kv1b_encode_append, except that values are first limited to +-65504 (NaN to 0) and a
  * group's scale is one binary16 step lower where min + 15 scale would pass 65504.
  * Skipped, with KV1B_STATUS_BAD_INDEX: tokens whose page is outside [0, num_pages) or past max_pages,

@@ -132,6 +132,7 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
   if (q || q_out) {
     if (!q || !q_out || q_stride_t < 0 || q_stride_h < 0 || qo_stride_t < 0 || qo_stride_h < 0) return KV1B_ERR_INVALID_ARG;
     if (num_q_heads < 1 || num_q_heads > KV1B_PAGED_MAX_HEADS) return KV1B_ERR_INVALID_ARG;
+    if ((num_tokens > 1 && qo_stride_t < KV1B_HEAD_DIM) || (num_q_heads > 1 && qo_stride_h < KV1B_HEAD_DIM)) return KV1B_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(q_out, 16) || q_stride_t % 4 || q_stride_h % 4 || qo_stride_t % 4 || qo_stride_h % 4)
       return KV1B_ERR_MISALIGNED;
     p.q = q;

@@ -609,7 +609,10 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       __syncthreads();
     }
   }
-  if (gave_up && lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_TIMEOUT);
+  if (gave_up) {
+    if (lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_TIMEOUT);
+    for (int s = 0; s < kStages; ++s) mbar_wait(&bars[warp][s], (phases >> s) & 1u, 64);  // a copy that is still under way
+  }
 }
 
 }  // namespace paged

@@ -473,6 +473,28 @@ def test_agrees_with_the_contiguous_cache():
     assert np.abs(ref.to_np(out) - a).max() <= (1e-3 + 3 * 2.0 ** -11 + eps / 2) * np.abs(a).max() * 4
 
 
+def test_tables_that_are_views():
+    # rows of a wider table, lengths and starts out of the middle of longer vectors
+    lengths, page = [70, 33, 128], 32
+    cache, signs, table, pre = filled(lengths, page, 2, 90, prefix=50)
+    wide = torch.full((3, 11), -7, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + table.shape[1]] = dev(table)
+    many = torch.full((8,), -1, dtype=torch.int32, device="cuda")
+    many[3:6] = dev(lengths, torch.int32)
+    q = torch.randn((3, 4, 128), device="cuda", dtype=torch.float16)
+    tab, n = wide[:, 2:2 + table.shape[1]], many[3:6]
+    check_attend(cache.attend(q, SCALE, tab, n), q, cache, signs, SCALE, table, lengths)
+    out = cache.attend_shared(q, SCALE, dev(pre), dev([50], torch.int32), tab, n)
+    check_attend(out, q, cache, signs, SCALE, table, lengths, prefix=(pre, 50))
+    k = torch.randn((3, 2, 128), device="cuda", dtype=torch.float16)
+    before = cache.pages.cpu().numpy()
+    start = [x - 1 for x in lengths]
+    many[3:6] = dev(start, torch.int32)
+    cache.append(k, k, tab, many[3:6], dev([0, 1, 2, 3], torch.int32))
+    same_bytes(cache.pages.cpu().numpy(), ref.append(before, ref.to_np(k), ref.to_np(k), table, start, [0, 1, 2, 3], signs))
+    assert cache.status() == 0
+
+
 def test_another_stream_and_default_results():
     lengths = [300, 40]
     cache, signs, table, _ = filled(lengths, 64, 2, 77)

@@ -70,8 +70,9 @@ APPEND = dict(cache=None, k=P, v=P, dtype=1, num_tokens=4, kst=256, ksh=128, vst
     (dict(k=P + 8), -4), (dict(ksh=130), -4), (dict(cu=P + 2), -4), (dict(num_tokens=(1 << 28) + 1), -2),
     (dict(max_pages=1 << 29, tstride=1 << 29), -2),
     (dict(q=P), -1), (dict(qo=P), -1), (dict(q=P, qo=P, hq=0), -1), (dict(q=P, qo=P, hq=1025), -1),
-    (dict(q=P, qo=P, hq=8, qs0=1026, qs1=128, os0=1024, os1=128), -4), (dict(q=P + 4, qo=P, hq=8), -4),
-    (dict(q=P, qo=P, hq=1000, num_tokens=1 << 27), -2),
+    (dict(q=P, qo=P, hq=8, qs0=1026, qs1=128, os0=1024, os1=128), -4), (dict(q=P + 4, qo=P, hq=8, os0=1024, os1=128), -4),
+    (dict(q=P, qo=P, hq=8, qs0=1024, qs1=128, os0=0, os1=128), -1), (dict(q=P, qo=P, hq=8, qs0=1024, qs1=128, os0=1024, os1=64), -1),
+    (dict(q=P, qo=P, hq=1000, num_tokens=1 << 27, os0=128000, os1=128), -2),
     (dict(rope=dict(), pos=None), -1), (dict(rope=dict(cos_sin=None), pos=P), -1), (dict(rope=dict(rot_dim=0), pos=P), -1),
     (dict(rope=dict(rot_dim=130), pos=P), -1), (dict(rope=dict(rot_dim=12, sections=(ctypes.c_int32 * 3)(6, 0, 0)), pos=P), -2),
     (dict(rope=dict(axes=4), pos=P), -1), (dict(rope=dict(axes=0), pos=P), -1),
