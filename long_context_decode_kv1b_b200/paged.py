@@ -180,7 +180,7 @@ class PagedCache:
                 raise ValueError("q must be [tokens, q heads, 128] of k's type with unit channel stride")
             self._on_device(q, "q")
             if q_out is None:
-                q_out = torch.empty((T, hq, HEAD_DIM), dtype=q.dtype, device=self.device)
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
             elif q_out.shape != q.shape or q_out.dtype is not q.dtype or q_out.stride(2) != 1 or q_out.get_device() != index:
                 raise ValueError("q_out must have q's shape, type and device, unit channel stride")
             qp, qo = q.data_ptr(), q_out.data_ptr()
@@ -208,7 +208,7 @@ class PagedCache:
         if rows != B or lengths.shape[0] != B:
             raise ValueError("q, page_table and lengths disagree on the number of sequences")
         if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=self.device)
+            out = torch.empty_like(q)
         elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous() or out.get_device() != self._index:
             raise ValueError("out must be a contiguous tensor of q's shape and type")
         return out, B, Hq, dtype, pages
