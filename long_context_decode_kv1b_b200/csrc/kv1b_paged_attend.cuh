@@ -155,8 +155,8 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
   __shared__ Plan pl;
   {
     const Plan mine = make_plan<kThreads>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), p.ncta, cta == 0);
-    if (threadIdx.x == 0) pl = mine;
-    __syncthreads();
+    if (lane == 0) pl = mine;  // every warp writes the same
+    __syncwarp();
   }
 
   // sequences that see nothing: zeros
@@ -174,15 +174,17 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     return;
   }
 
-  const int64_t r0 = pl.begin(cta), r1 = pl.begin(cta + 1);
+  const int64_t border = pl.begin(cta + (lane & 1));  // both ends in one go
+  const int64_t r0 = __shfl_sync(kFull, border, 0);
+  __shared__ int64_t r1;  // every warp writes the same; kept out of the loop's registers
+  if (lane == 1) r1 = border;
+  __syncwarp();
   if (r0 == r1) {  // within what a segment counts besides its blocks
     if (threadIdx.x == 0 && !p.rows) p.spread[cta] = make_int2(0, 0);
     return;
   }
   const uint32_t ring = smem_u32(smem) + warp * kStages * kBlkBytes;
   const int max_segs = min(kMaxSegs, kQuerySlots / G);
-  const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
-  float* first = p.first + (static_cast<int64_t>(cta) * kWarps + warp) * G * kRow;
   if (threadIdx.x < 8) reinterpret_cast<uint32_t*>(smem + kOffRows)[threadIdx.x] = threadIdx.x < 4 ? 0x3C003C00u : 0u;
   const uint32_t side_row = smem_u32(smem) + kOffRows + (g == 4 ? 0 : 16);  // rows 4 and 5 .. 7 of the side product
   uint32_t phases = 0;  // bit s: parity of stage s's next completion
@@ -275,6 +277,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     }
 
     // ---- the round's queries
+    const float qs = __fmul_rn(__fmul_rn(p.scale, 1.4426950408889634f), 1.0f / kD);
     for (int r0 = warp; r0 < nrow; r0 += kWarps) {
       if (r0 >= 2 * kWarps) load_row(r0, q0);
       const QueryPrep qp = query_prep_values(q0, signs);
@@ -350,6 +353,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       side[0] = side[1] = side[2] = side[3] = 0.0f;
       m = 0.0f;
       bool fresh = true;   // no block has set m
+      float bar = kBase + kTau;  // an exponent past it raises the reference
       int top_scale = 0;   // weights are 2^-top_scale lower: no scale reaches 2^(1 + top_scale)
       const bool starts = cur.i == 0;
       const int count = min(cur.left, seg[cur.s].nb - cur.i);  // blocks of the segment in the warp's run
@@ -391,8 +395,6 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
           {
             uint32_t kw[4];
             ldsm_x4(kw, st + lane * 16);
-            lds128(ncr, st + kBlkOffNc + 32 * t);
-            lds128(ncr + 4, st + kBlkOffNc + 32 * t + 16);
             #pragma unroll
             for (int i = 0; i < 4; ++i) {
               // the sums start at the bits of 1.5 2^23: as a float, an entry is that plus its integer
@@ -410,6 +412,8 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
               }
             }
           }
+          lds128(ncr, st + kBlkOffNc + 32 * t);
+          lds128(ncr + 4, st + kBlkOffNc + 32 * t + 16);
           {
             // the block's 128 scales, four a lane: one of 2 or more has the top exponent bit
             uint32_t w0, w1;
@@ -422,6 +426,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
                 const float f = ex2(static_cast<float>(top_scale - k));
                 m += static_cast<float>(k - top_scale);
                 top_scale = k;
+                bar = kBase + kTau - static_cast<float>(k);
                 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   #pragma unroll
@@ -432,6 +437,8 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
               }
             }
           }
+          uint32_t mn[4];  // (where the loads stand matters: this one right before its products made 191 of 176 us for 1M tokens)
+          lds128(mn, g < 4 ? st + kBlkOffMin + g * 64 + 16 * t : side_row);
           // exponents of the weights: logit - m + kBase
           float y[8];
           {
@@ -445,7 +452,6 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
             for (int j = 0; j < 8; ++j) y[j] = (mine >> j) & 1u ? y[j] : -INFINITY;
           }
           float mx = fmaxf(max3(max3(y[0], y[1], y[2]), y[3], y[4]), max3(y[5], y[6], y[7]));
-          const float bar = kBase + kTau - static_cast<float>(top_scale);
           if (__any_sync(kFull, mx > bar) || fresh) {  // rare: raise references
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
@@ -470,8 +476,6 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
           #pragma unroll
           for (int i = 0; i < 4; ++i) pw[i] = pack_f16(ex2(y[2 * i]), ex2(y[2 * i + 1]));
           {
-            uint32_t mn[4];
-            lds128(mn, g < 4 ? st + kBlkOffMin + g * 64 + 16 * t : side_row);
             hmma(side, mn[0], 0u, mn[1], 0u, pw[0], pw[1]);
             hmma(side, mn[2], 0u, mn[3], 0u, pw[2], pw[3]);
           }
@@ -533,7 +537,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
           }
         }
       } else if (cur.left > 0) {  // its end: the run goes on with another segment
-        put_piece(first);
+        put_piece(p.first + (static_cast<int64_t>(cta) * kWarps + warp) * G * kRow);
       } else {
         last = true;
       }

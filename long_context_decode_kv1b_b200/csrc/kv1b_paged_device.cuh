@@ -209,65 +209,85 @@ struct Plan {
   }
 };
 
-// All threads of the CTA; lengths are limited to what the page table can hold.
+// A sequence's length, limited to what its page table can hold.
+__device__ __forceinline__ int plan_length(const PagedAttendParams& p, int b, bool* bad) {
+  const bool own = b >= p.packed;
+  const int64_t top = static_cast<int64_t>(own ? p.max_pages : p.max_prefix_pages) << (p.c.bpp_shift + 5);
+  const int n = own ? __ldg(p.lengths + b - p.packed) : __ldg(p.prefix_len);
+  *bad |= n < 0 || n > top;
+  return n < 0 ? 0 : static_cast<int>(n > top ? top : n);
+}
+
+// All threads of the CTA.  pre, len and some are in shared memory and, as the plan, the same for every warp: each
+// warp may use them at once.
 template <int THREADS>
 __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* pre, int* len, uint16_t* some, int ncta, bool report) {
-  __shared__ uint64_t s_tot[THREADS / 32];  // blocks, and sequences with some << 40
   const int nseq = p.packed + p.B;
-  const int per = (nseq + THREADS - 1) / THREADS;
-  const int page_shift = p.c.bpp_shift + 5;
-  const int64_t most = static_cast<int64_t>(p.max_pages) << page_shift;
-  Plan pl;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
-  const int b0 = threadIdx.x * per;
-  uint64_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = b0 + i;
-    if (b >= nseq) break;
-    const bool own = b >= p.packed;
-    const int64_t top = own ? most : static_cast<int64_t>(p.max_prefix_pages) << page_shift;
-    const int n = own ? __ldg(p.lengths + b - p.packed) : __ldg(p.prefix_len);
-    bad |= n < 0 || n > top;
-    const int nn = n < 0 ? 0 : static_cast<int>(n > top ? top : n);
-    len[b] = nn;
-    const int blocks = visible(nn, p.window, p.sinks).blocks;
-    mine += static_cast<uint64_t>(blocks) | (blocks > 0 ? 1ull << 40 : 0ull);
+  uint64_t total = 0;  // blocks, and sequences with some << 40
+  if (nseq <= 32) {  // by every warp for itself: a barrier less, and shorter chains
+    const int n = lane < nseq ? plan_length(p, lane, &bad) : 0;
+    const uint32_t blocks = visible(n, p.window, p.sinks).blocks;
+    const unsigned with = __ballot_sync(kFull, blocks > 0);
+    uint32_t x = blocks;
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane < nseq) {
+      len[lane] = n;
+      pre[lane + 1] = x;
+      if (blocks > 0) some[__popc(with & ((1u << lane) - 1u))] = static_cast<uint16_t>(lane);
+    }
+    if (lane == 0) pre[0] = 0;
+    total = __shfl_sync(kFull, x, 31) | static_cast<uint64_t>(__popc(with)) << 40;
+    __syncwarp();
+  } else {
+    __shared__ uint64_t s_tot[THREADS / 32];
+    const int per = (nseq + THREADS - 1) / THREADS;
+    const int b0 = threadIdx.x * per, b1 = min(b0 + per, nseq);
+    uint64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int n = plan_length(p, b, &bad);
+      len[b] = n;
+      const int blocks = visible(n, p.window, p.sinks).blocks;
+      mine += static_cast<uint64_t>(blocks) | (blocks > 0 ? 1ull << 40 : 0ull);
+    }
+    uint64_t x = mine;
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_tot[warp] = x;
+    __syncthreads();
+    uint64_t at = x - mine;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      at += w < warp ? s_tot[w] : 0ull;
+      total += s_tot[w];
+    }
+    for (int b = b0; b < b1; ++b) {
+      pre[b] = static_cast<uint32_t>(at);
+      const int blocks = visible(len[b], p.window, p.sinks).blocks;
+      if (blocks > 0) some[at >> 40] = static_cast<uint16_t>(b);
+      at += static_cast<uint64_t>(blocks) | (blocks > 0 ? 1ull << 40 : 0ull);
+    }
+    if (threadIdx.x == 0) pre[nseq] = static_cast<uint32_t>(total);
+    __syncthreads();
   }
   if (bad && report && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
-  uint64_t x = mine;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_tot[warp] = x;
-  __syncthreads();
-  uint64_t at = x - mine, total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    at += w < warp ? s_tot[w] : 0ull;
-    total += s_tot[w];
-  }
-  for (int i = 0; i < per; ++i) {
-    const int b = b0 + i;
-    if (b >= nseq) break;
-    pre[b] = static_cast<uint32_t>(at);
-    const int blocks = visible(len[b], p.window, p.sinks).blocks;
-    if (blocks > 0) some[at >> 40] = static_cast<uint16_t>(b);
-    at += static_cast<uint64_t>(blocks) | (blocks > 0 ? 1ull << 40 : 0ull);
-  }
-  const uint32_t total_blocks = static_cast<uint32_t>(total);
-  if (threadIdx.x == 0) pre[nseq] = total_blocks;
-  __syncthreads();
+  Plan pl;
   pl.pre = pre;
   pl.len = len;
   pl.some = some;
   pl.nsome = static_cast<int>(total >> 40);
   pl.B = nseq;
   pl.Hkv = p.c.Hkv;
-  pl.S = static_cast<int64_t>(total_blocks) * p.c.Hkv;
+  pl.S = static_cast<int64_t>(static_cast<uint32_t>(total)) * p.c.Hkv;
   const int64_t units = pl.S + static_cast<int64_t>(kSegUnits) * pl.nsome * pl.Hkv;
-  const int64_t want = (units + p.min_units - 1) / p.min_units;
+  const int64_t want = quotient(units + p.min_units - 1, p.min_units);
   pl.n = static_cast<int>(want < 1 ? 1 : (want < ncta ? want : ncta));
   pl.q = quotient(units, pl.n);
   pl.rem = static_cast<int>(units - pl.q * pl.n);
