@@ -104,6 +104,8 @@ struct PagedSharedParams {
 }  // namespace kv1b
 
 cudaError_t kv1b_launch_paged_append(const kv1b::PagedAppendParams& p, cudaStream_t stream);
+// The attend's kernel alone, and with the merge of what its ranges cut.
+cudaError_t kv1b_launch_paged_pieces(const kv1b::PagedAttendParams& p, int32_t G, cudaStream_t stream);
 cudaError_t kv1b_launch_paged_attend(const kv1b::PagedAttendParams& p, int32_t G, cudaStream_t stream);
 cudaError_t kv1b_launch_paged_shared(const kv1b::PagedAttendParams& p, const kv1b::PagedSharedParams& s, int32_t G,
                                      cudaStream_t stream);

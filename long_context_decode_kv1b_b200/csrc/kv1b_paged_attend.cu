@@ -32,14 +32,17 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedAttendParam
 
 using namespace kv1b;
 
-cudaError_t kv1b_launch_paged_attend(const PagedAttendParams& p, int32_t G, cudaStream_t stream) {
-  static std::atomic<unsigned long long> configured{0};
-  static std::atomic<unsigned long long> configured_fine{0};
+cudaError_t kv1b_launch_paged_pieces(const PagedAttendParams& p, int32_t G, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0}, configured_fine{0};
   const bool fine = p.q_dtype == KV1B_DTYPE_F16;
   const auto kernel = fine ? paged::paged_attend_kernel<true> : paged::paged_attend_kernel<false>;
   cudaError_t e = configure_smem(reinterpret_cast<const void*>(kernel), paged::kSmem, fine ? &configured_fine : &configured);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, dim3(p.ncta), dim3(paged::kThreads), paged::kSmem, stream, p, G);
+  return launch_pdl(kernel, dim3(p.ncta), dim3(paged::kThreads), paged::kSmem, stream, p, G);
+}
+
+cudaError_t kv1b_launch_paged_attend(const PagedAttendParams& p, int32_t G, cudaStream_t stream) {
+  const cudaError_t e = kv1b_launch_paged_pieces(p, G, stream);
   if (e != cudaSuccess || p.ncta < 2) return e;
   return launch_pdl(paged::paged_merge_kernel, dim3(p.ncta - 1, G), dim3(128), 0, stream, p, G);
 }

@@ -600,19 +600,21 @@ __global__ void __launch_bounds__(128) paged_shared_merge_kernel(const PagedAtte
 
 using namespace kv1b;
 
-cudaError_t kv1b_launch_paged_shared(const PagedAttendParams& p, const PagedSharedParams& s, int32_t G, cudaStream_t stream) {
+static cudaError_t launch_prefix(const PagedAttendParams& p, const PagedSharedParams& s, int32_t G, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0}, configured_fine{0};
   const bool fine = p.q_dtype == KV1B_DTYPE_F16;
   const auto kernel = fine ? paged::paged_shared_kernel<true> : paged::paged_shared_kernel<false>;
   cudaError_t e = configure_smem(reinterpret_cast<const void*>(kernel), paged::kShSmem, fine ? &configured_fine : &configured);
   if (e != cudaSuccess) return e;
-  const int units = p.packed ? 0 : p.c.Hkv * s.row_tiles * s.splits;
-  if (units) {
-    const int64_t rows = static_cast<int64_t>(p.B) * p.Hq;
-    e = launch_pdl(paged::paged_query_codes_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p, s, G);
-    if (e != cudaSuccess) return e;
-  }
-  e = launch_pdl(kernel, dim3(static_cast<unsigned>(units + p.ncta)), dim3(paged::kShThreads), paged::kShSmem, stream, p, s, G, units);
+  const int64_t rows = static_cast<int64_t>(p.B) * p.Hq;
+  e = launch_pdl(paged::paged_query_codes_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p, s, G);
+  if (e != cudaSuccess) return e;
+  const int units = p.c.Hkv * s.row_tiles * s.splits;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(units + p.ncta)), dim3(paged::kShThreads), paged::kShSmem, stream, p, s, G, units);
+}
+
+cudaError_t kv1b_launch_paged_shared(const PagedAttendParams& p, const PagedSharedParams& s, int32_t G, cudaStream_t stream) {
+  const cudaError_t e = p.packed ? kv1b_launch_paged_pieces(p, G, stream) : launch_prefix(p, s, G, stream);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged::paged_shared_merge_kernel, dim3(static_cast<unsigned>(p.B) * p.c.Hkv, G), dim3(128), 0, stream, p, s, G);
 }
