@@ -88,7 +88,6 @@ struct PagedAttendParams {
 };
 
 constexpr int kAttendWarps = 12;  // of a CTA of the attend's kernel
-constexpr int kPackedRows = 32;  // rows of a kv-head up to which the attend's kernel takes the prefix
 
 // The queries of a kv-head as the rows of one matrix: R = B G rows, row b G + g.
 struct PagedSharedParams {

@@ -196,13 +196,26 @@ kv1b::PagedSharedParams shared_plan(int32_t Hkv, int32_t G, int32_t num_seqs, in
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Few rows of a kv-head are served by the attend's kernel, eight at a time, the prefix once for each eight.
-int packed_groups(int32_t rows) { return rows <= kv1b::kPackedRows ? (rows + 7) / 8 : 0; }
+// Whether the attend's kernel takes the prefix, eight rows of a kv-head at a time and the prefix once for each
+// eight, and in how many groups (0: the matrix kernel does).  It starts sooner and costs rows x tiles; measured
+// over 8 kv-heads, it against the other, us:
+//   rows      8 tiles    64 tiles     504 tiles    1,880 tiles   6,256 tiles (of all kv-heads)
+//   16                                             29 against 38    60 against 78
+//   32                   15 against 28  24 against 28  37 against 39   105 against 80
+//   64                   18 against 28  28 against 31  63 against 48   195 against 100
+//   128                  21 against 30  41 against 51  119 against 69
+//   256                  30 against 30  74 against 55
+// The prefix's own length is the device's to know; its table's width stands for it.
+int packed_groups(int32_t rows, int32_t Hkv, int64_t max_tokens) {
+  const int64_t tiles = Hkv * ((max_tokens + 127) / 128);
+  return rows <= 16 || (rows <= 128 && rows * tiles <= 65536) ? (rows + 7) / 8 : 0;
+}
 
 // The buffers of a shared call in its workspace; bytes in all.
-size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int32_t Hkv, int32_t G, uint8_t* ws) {
+size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int32_t Hkv, int32_t G, int64_t max_tokens,
+                    uint8_t* ws) {
   const size_t rows = static_cast<size_t>(Hkv) * s->R, row = kv1b::kPartStride * 4;
-  const size_t packed = packed_groups(s->R), n = packed ? 8 : G;
+  const size_t packed = packed_groups(s->R, Hkv, max_tokens), n = packed ? 8 : G;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* const here = ws + at;
@@ -239,9 +252,9 @@ size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_
   if (num_seqs < 1 || num_seqs > KV1B_PAGED_MAX_SEQS || max_prefix_pages < 1) return 0;
   if (!paged_ok(cache) || heads_check(cache, num_q_heads) != KV1B_OK || table_check(cache, 1, 0, 1, max_prefix_pages) != KV1B_OK) return 0;
   const int32_t G = num_q_heads / cache->num_kv_heads;
-  kv1b::PagedSharedParams s =
-      shared_plan(cache->num_kv_heads, G, num_seqs, static_cast<int64_t>(max_prefix_pages) * cache->page_tokens);
-  return shared_carve(&s, nullptr, cache->num_kv_heads, G, nullptr);
+  const int64_t max_tokens = static_cast<int64_t>(max_prefix_pages) * cache->page_tokens;
+  kv1b::PagedSharedParams s = shared_plan(cache->num_kv_heads, G, num_seqs, max_tokens);
+  return shared_carve(&s, nullptr, cache->num_kv_heads, G, max_tokens, nullptr);
 }
 
 static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
@@ -286,9 +299,9 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   p.spread = reinterpret_cast<int2*>(p.first + static_cast<size_t>(p.ncta) * kv1b::kAttendWarps * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride);
   const int32_t G = num_q_heads / cache->num_kv_heads;
   if (!prefix_pages) return cuda_status(kv1b_launch_paged_attend(p, G, static_cast<cudaStream_t>(stream)));
-  kv1b::PagedSharedParams s =
-      shared_plan(cache->num_kv_heads, G, num_seqs, static_cast<int64_t>(max_prefix_pages) * cache->page_tokens);
-  shared_carve(&s, &p, cache->num_kv_heads, G, static_cast<uint8_t*>(ws));
+  const int64_t max_tokens = static_cast<int64_t>(max_prefix_pages) * cache->page_tokens;
+  kv1b::PagedSharedParams s = shared_plan(cache->num_kv_heads, G, num_seqs, max_tokens);
+  shared_carve(&s, &p, cache->num_kv_heads, G, max_tokens, static_cast<uint8_t*>(ws));
   return cuda_status(kv1b_launch_paged_shared(p, s, G, static_cast<cudaStream_t>(stream)));
 }
 

@@ -360,6 +360,28 @@ def test_attend_shared(case, dtype):
     check_attend(out, q, cache, signs, SCALE, table, lengths, prefix=(pre, prefix))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows", [17, 32, 33, 64, 128])
+@pytest.mark.parametrize("prefix", [0, 1, 100, 900])
+def test_attend_shared_wide_prefix_table(prefix, rows, dtype):
+    # the same prefix through a table of its own and through one that could hold a long prefix: which kernel
+    # takes it follows from the table's width
+    lengths, page, H = [29] * rows, 64, 2
+    lengths[3:5] = [0, 70]
+    cache, signs, table, pre = filled(lengths, page, H, 140 + rows, prefix=prefix)
+    if len(pre) == 0:
+        pre = np.array([-1], np.int32)
+    q = (2 * torch.randn((rows, H, 128), device="cuda")).to(dtype)
+    tab, n, plen = dev(table), dev(lengths, torch.int32), dev([prefix], torch.int32)
+    near = cache.attend_shared(q, SCALE, dev(pre), plen, tab, n)
+    wide = torch.full((70000 * 128 // (page * rows * H),), -1, dtype=torch.int32, device="cuda")
+    wide[:len(pre)] = dev(pre)
+    far = cache.attend_shared(q, SCALE, wide, plen, tab, n)
+    assert cache.status() == 0
+    check_attend(near, q, cache, signs, SCALE, table, lengths, prefix=(pre, prefix))
+    check_attend(far, q, cache, signs, SCALE, table, lengths, prefix=(pre, prefix))
+
+
 def test_attend_shared_bad_prefix():
     lengths, prefix = [40, 70, 1], 150
     cache, signs, table, pre = filled(lengths, 32, 2, 31, prefix=prefix)
