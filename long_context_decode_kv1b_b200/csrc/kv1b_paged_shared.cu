@@ -16,8 +16,8 @@
 // 131,072 tokens x 8 kv-heads.)
 //
 // Warps: 0 - 3 and 4 - 7 the lanes' softmax, 8 - 11 the values' expansion (codes to f16, one rounding), 12
-// and 13 issue a lane's products each, 14 and 15 expand the signs to f8, 14 also copies the packed blocks.  Each wait is bounded; one that
-// runs out ends the CTA with KV1B_STATUS_TIMEOUT.
+// and 13 issue a lane's products each, 14 and 15 expand the signs to f8, 14 also copies the blocks.  Each wait
+// is bounded; one that runs out ends the CTA with KV1B_STATUS_TIMEOUT.
 //
 // A tile of 128 tokens x 256 rows costs 512 + 1,024 clocks of products and 32,768 exponentials, 2,048
 // clocks at 16 a clock: the exponentials bound it.
@@ -35,7 +35,7 @@ constexpr float kMostSum = 32768.0f;       // 2^(kBase + kTau): a sum up to it h
 constexpr int kShThreads = 512;            // four warpgroups
 // 512 x 128 registers at launch; the softmax groups take what the others give back: 2 (168 + 88) = 4 x 128
 constexpr int kSoftRegs = 168, kOtherRegs = 88;
-constexpr int kRaw = 3;                    // tiles of packed blocks in flight
+constexpr int kRaw = 3;                    // tiles of blocks in flight
 constexpr int kBuf = 3;                    // expanded tiles
 constexpr int kQBytes = 128 * 128;         // one lane's codes
 constexpr int kKBytes = kTile * 128;       // signs as f8
@@ -413,7 +413,7 @@ __device__ __forceinline__ void prefix_cta(const PagedAttendParams& p, const Pag
     }
   } else if (warp >= kSignWarp) {
     // ------------------------------------------------------------------ signs as +-1 in f8 and the tokens' factors
-    // and, by the first of the two warps, the copies of the packed blocks (lane b < 4 block b of a tile)
+    // and, by the first of the two warps, the copies of the blocks (lane b < 4 block b of a tile)
     const int bit_row = 8 * ((lane >> 1) & 3) + 2 * (lane >> 3) + (lane & 1);
     const bool copies = warp == kSignWarp;
     const int nblk = (n + kBlkTok - 1) / kBlkTok;
