@@ -405,7 +405,7 @@ size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_
 
 /* Decode attention over a page table: one query token per sequence.
  * q: [num_seqs][num_q_heads][128] contiguous, KV1B_DTYPE_BF16 or _F16, 16-byte aligned; out: the same
- *   shape and type.  (An fp32 query is KV1B_ERR_UNSUPPORTED: weights and expanded values enter the
+ *   shape and type, q itself if the caller likes.  (An fp32 query is KV1B_ERR_UNSUPPORTED: weights and expanded values enter the
  *   tensor cores as binary16, which an fp32 output would promise too much for; kv1b_attend takes it.)
  * lengths: i32 [num_seqs], tokens each sequence holds (the query is the last of them); values below 0
  *   or past max_pages * page_tokens are limited to that range, with KV1B_STATUS_BAD_INDEX.
@@ -424,6 +424,8 @@ int kv1b_paged_attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype,
  * prefix (prefix_length[0] tokens, a device i32, in pages prefix_pages[0 .. max_prefix_pages)), then
  * its own lengths[b] tokens in its row of page_table, which starts a page of its own.  Equal to
  * kv1b_paged_attend over the concatenation, but the prefix is read once for the whole batch.
+ * max_prefix_pages stands for the prefix's length where the work is split before the device knows it: a
+ * table hardly wider than the prefix serves short ones faster.
  * Arguments otherwise as kv1b_paged_attend; either part may be empty. */
 int kv1b_paged_attend_shared(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
                              int32_t num_seqs, const int32_t* prefix_pages, int32_t max_prefix_pages,

@@ -237,7 +237,7 @@ __device__ __forceinline__ void query_rows(const PagedAppendParams& p, int64_t t
 __device__ __forceinline__ void query_row(const PagedAppendParams& p, int64_t t, int h) {
   const int lane = threadIdx.x & 31;
   float x[4];
-  load4(p.q, t * p.q_st + h * p.q_sh + 4 * lane, p.dtype, x);
+  load_query(p.q, t * p.q_st + h * p.q_sh + 4 * lane, p.dtype, x);
   if (p.cos_sin) {
     int ps[3];
     if (!positions(p, t, ps)) {

@@ -243,7 +243,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       const int s = slot_of(r);
       const Seg sg = seg[s / G];
       const int i = min(s % G, heads.count(sg.b) - 1);  // a row that is not there: the last one again, unused
-      load4(p.q, heads.query(sg.b, sg.h, i) * kD + 4 * lane, p.q_dtype, x);
+      load_query(p.q, heads.query(sg.b, sg.h, i) * kD + 4 * lane, p.q_dtype, x);
     };
     float q0[4], q1[4];
     if (warp < nrow) load_row(warp, q0);

@@ -140,6 +140,21 @@ __device__ __forceinline__ void expand_codes(uint32_t w, uint32_t (&c)[4]) {
   c[3] = hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
 }
 
+// A lane's four channels of a query row.  The append turns queries, in place if the caller likes, and a kernel
+// behind it may start before it ends: coherent loads, where load4's are for data that nothing writes meanwhile.
+__device__ __forceinline__ void load_query(const void* q, int64_t at, int dtype, float (&x)[4]) {
+  if (dtype == KV1B_DTYPE_F32) {
+    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(q) + at);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    return;
+  }
+  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at);
+  const uint32_t h[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
+  #pragma unroll
+  for (int r = 0; r < 4; ++r)
+    x[r] = dtype == KV1B_DTYPE_BF16 ? __uint_as_float(h[r] << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(h[r])));
+}
+
 __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float x) {
   if (dtype == KV1B_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
   else static_cast<__half*>(out)[i] = __float2half_rn(x);

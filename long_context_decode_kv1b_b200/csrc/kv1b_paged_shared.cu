@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(256) paged_query_codes_kernel(const PagedAtten
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // [sequence][q head]
   if (row >= static_cast<int64_t>(p.B) * p.Hq) return;
   float x[4];
-  load4(p.q, row * kD + 4 * lane, p.q_dtype, x);
+  load_query(p.q, row * kD + 4 * lane, p.q_dtype, x);
   int code[4];
   float vl, dl;
   query_quantise(x, p.c.signs, code, &vl, &dl);

@@ -228,7 +228,7 @@ class PagedCache:
                sinks: int = 0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Decode attention of q [seqs, q heads, 128] (bf16 / fp16) over each sequence's first lengths[b]
         tokens (int32, on the device); with window > 0 over the last `window` and the first `sinks` of them.
-        Returns q's shape and type."""
+        Returns q's shape and type (in ``out`` if given, q itself allowed)."""
         if self._away(stream):
             with self._on(stream):
                 return self.attend(q, scale, page_table, lengths, window, sinks, out)

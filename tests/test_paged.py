@@ -405,6 +405,83 @@ def test_attend_shared_bad_prefix():
 
 
 # -------------------------------------------------------------------------------------- together
+def test_attend_shared_bad_prefix_in_a_wide_table():
+    # the same refusals where the matrix kernel takes the prefix
+    lengths, prefix, page = [40, 0] * 20, 700, 32
+    cache, signs, table, pre = filled(lengths, page, 2, 33, prefix=prefix)
+    q = torch.randn((40, 4, 128), device="cuda", dtype=torch.float16)
+    args = (dev(table), dev(lengths, torch.int32))
+    wide = np.full((70000 * 128 // (page * 80 * 2),), -1, np.int32)
+    wide[:len(pre)] = pre
+    wide[[0, 3, 20]] = [cache.num_pages, -9, 2 ** 31 - 1]
+    out = cache.attend_shared(q, SCALE, dev(wide), dev([prefix], torch.int32), *args)
+    assert cache.status() == kv.STATUS_BAD_INDEX
+    pages, qn = cache.pages.cpu().numpy(), ref.to_np(q)
+    t = np.arange(prefix)
+    t = t[~np.isin(t // page, [0, 3, 20])]
+    for b in (0, 1, 39):
+        parts = [ref.gather(pages, wide, 1, t), ref.gather(pages, table[b], 1, np.arange(lengths[b]))]
+        row = ref.Row(qn[b, 3], signs, SCALE, parts)
+        assert (np.abs(ref.to_np(out)[b, 3] - row.out) <= row.tolerance(torch.finfo(q.dtype).eps)).all()
+    cache.status_word.zero_()
+    out = cache.attend_shared(q, SCALE, dev(wide), dev([-1], torch.int32), *args)
+    assert cache.status() == kv.STATUS_BAD_INDEX
+    check_attend(out, q, cache, signs, SCALE, table, lengths)
+    cache.status_word.zero_()
+    out = cache.attend_shared(q, SCALE, dev(np.full_like(wide, -1)), dev([2 ** 31 - 1], torch.int32), *args)
+    assert cache.status() == kv.STATUS_BAD_INDEX
+    check_attend(out, q, cache, signs, SCALE, table, lengths)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(bad):
+    lengths, prefix, page = [90, 5, 33, 64] * 6, 300, 64
+    cache, signs, table, pre = filled(lengths, page, 2, 34, prefix=prefix)
+    q = torch.randn((24, 4, 128), device="cuda", dtype=torch.bfloat16)
+    spoilt = q.clone()
+    spoilt[1, 2, 77] = bad
+    spoilt[13, 0, :] = bad
+    ok = torch.ones((24, 4, 1), dtype=torch.bool, device="cuda")
+    ok[1, 2] = ok[13, 0] = False
+    tab, n, plen = dev(table), dev(lengths, torch.int32), dev([prefix], torch.int32)
+    wide = torch.full((70000 * 128 // (page * 48 * 2),), -1, dtype=torch.int32, device="cuda")
+    wide[:len(pre)] = dev(pre)
+
+    def patched(out, clean):  # rows of the spoilt queries as those of the clean ones
+        assert torch.isfinite(out[ok.expand_as(out)]).all() and not torch.isfinite(out[~ok.expand_as(out)]).any()
+        return torch.where(ok, out, clean)
+
+    check_attend(patched(cache.attend(spoilt, SCALE, tab, n), cache.attend(q, SCALE, tab, n)), q, cache, signs, SCALE, table, lengths)
+    for pages in (dev(pre), wide):
+        out = patched(cache.attend_shared(spoilt, SCALE, pages, plen, tab, n), cache.attend_shared(q, SCALE, pages, plen, tab, n))
+        check_attend(out, q, cache, signs, SCALE, table, lengths, prefix=(pre, prefix))
+
+
+def test_results_over_the_queries():
+    # out may be q: one long sequence that every CTA reads, short ones, an empty one, both shared forms
+    lengths, prefix, page = [20000, 0, 70, 1] + [33] * 20, 500, 64
+    cache, signs, table, pre = filled(lengths, page, 2, 35, prefix=prefix)
+    q = torch.randn((24, 4, 128), device="cuda", dtype=torch.float16)
+    tab, n, plen = dev(table), dev(lengths, torch.int32), dev([prefix], torch.int32)
+    wide = torch.full((70000 * 128 // (page * 48 * 2),), -1, dtype=torch.int32, device="cuda")
+    wide[:len(pre)] = dev(pre)
+    for call in (lambda x, **kw: cache.attend(x, SCALE, tab, n, **kw),
+                 lambda x, **kw: cache.attend_shared(x, SCALE, dev(pre), plen, tab, n, **kw),
+                 lambda x, **kw: cache.attend_shared(x, SCALE, wide, plen, tab, n, **kw)):
+        apart, same = call(q), q.clone()
+        assert call(same, out=same) is same and torch.equal(apart, same)
+    k = torch.randn((24, 2, 128), device="cuda", dtype=torch.float16)
+    rope = kv.Rope(torch.randn((64, 128), device="cuda"))
+    at = torch.arange(24, dtype=torch.int32, device="cuda")
+    for _ in range(20):  # a step's append in place, and the attend behind it at once
+        same = q.clone()
+        turned = cache.append(k, k, tab, n - 1, torch.arange(25, dtype=torch.int32, device="cuda"), rope, at, q=q)
+        expect = cache.attend(turned, SCALE, tab, n)
+        torch.cuda.synchronize()
+        cache.append(k, k, tab, n - 1, torch.arange(25, dtype=torch.int32, device="cuda"), rope, at, q=same, q_out=same)
+        assert torch.equal(cache.attend(same, SCALE, tab, n, out=same), expect)
+
+
 def test_serving_loop_in_graphs():
     # a shared instruction, ragged prompts in chunks, then decode steps replayed from one captured
     # graph while lengths, positions and inputs change in place; a second graph of the same calls is
