@@ -1,5 +1,7 @@
 """The paged cache on the GPU: the append against the oracle's encoder byte for byte (untouched bytes
 included), attention against 64 bits, and the calls together as a serving loop makes them."""
+import concurrent.futures
+
 import numpy as np
 import pytest
 import torch
@@ -605,6 +607,61 @@ def test_another_stream_and_default_results():
     outs = [cache.attend(q, SCALE, tab, n, stream=s) for s in streams for _ in range(4)]
     torch.cuda.synchronize()
     assert all(torch.equal(first, o) for o in outs)
+
+
+def step_of(i, graphed):
+    """A decode step of its own cache: append, attend and both forms of the shared attend; run(stream) -> results."""
+    lengths, prefix, page = [150 + i, 1, 33, 64] * 6, 400, 64
+    cache, _, table, pre = filled(lengths, page, 2, 120 + i, prefix=prefix)
+    g = torch.Generator(device="cuda").manual_seed(i)
+    q = torch.randn((24, 4, 128), generator=g, device="cuda", dtype=torch.bfloat16)
+    k, v = torch.randn((2, 24, 2, 128), generator=g, device="cuda", dtype=torch.bfloat16)
+    tab, n, plen = dev(table), dev(lengths, torch.int32), dev([prefix], torch.int32)
+    cu = torch.arange(25, dtype=torch.int32, device="cuda")
+    rope, at = kv.Rope(dev(rope_table(300, 128))), cu[:24]
+    wide = torch.full((70000 * 128 // (page * 48 * 2),), -1, dtype=torch.int32, device="cuda")
+    wide[:len(pre)] = dev(pre)
+    start = n - 1
+
+    def run(stream):
+        turned = cache.append(k, v, tab, start, cu, rope, at, q=q, stream=stream)
+        return [turned, cache.attend(turned, SCALE, tab, n, window=40, sinks=3, stream=stream)] + \
+            [cache.attend_shared(turned, SCALE, pages, plen, tab, n, stream=stream) for pages in (dev_pre, wide)]
+
+    dev_pre = dev(pre)
+    torch.cuda.synchronize()
+    if not graphed:
+        return cache, run
+    run(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run(None)
+
+    def replay(stream, inputs=run):  # the graph reads the tensors that `run` holds
+        with torch.cuda.stream(stream):
+            graph.replay()
+            return [x.clone() for x in outs]
+
+    return cache, replay
+
+
+@pytest.mark.parametrize("graphed", [False, True])
+def test_two_threads_at_once(graphed):
+    # steps of two caches on two streams, launched by two host threads: as one after the other
+    steps = [step_of(i, graphed) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    alone = []
+    for (_, run), s in zip(steps, streams):
+        alone.append(run(s))
+        torch.cuda.synchronize()
+    with concurrent.futures.ThreadPoolExecutor(2) as pool:
+        both = list(pool.map(lambda x: [x[0][1](x[1]) for _ in range(20)], zip(steps, streams)))
+    torch.cuda.synchronize()
+    for one, many in zip(alone, both):
+        for outs in many:
+            assert all(torch.equal(a, b) for a, b in zip(one, outs))
+    assert all(cache.status() == 0 for cache, _ in steps)
 
 
 def test_offsets_past_32_bits():
