@@ -85,9 +85,15 @@ struct PagedAttendParams {
                            // rows [packed + B][Hkv] first CTA and pieces of each segment; pieces 0: none
   int32_t ncta;
   int32_t min_units;       // blocks and what segments count besides (kSegUnits each) that a CTA takes at least
+  int32_t beside;          // CTAs beside the matrix kernel's, if they end before it does (0: as min_units says)
+  int32_t splits, tile_ns; // the prefix's token ranges, and the time of a tile there
 };
 
 constexpr int kAttendWarps = 12;  // of a CTA of the attend's kernel
+constexpr int kSegUnits = 8;      // blocks that a segment counts for its start and end
+// Times that the split of a shared call goes by: of the sequences' own tokens a CTA's start and end and a unit of
+// its work; of the prefix a CTA's start and end and a 128-token tile for 256 rows and for 128.
+constexpr int kCtaNs = 10000, kUnitNs = 120, kPrefixNs = 18000, kTile256Ns = 2150, kTile128Ns = 1100;
 
 // The queries of a kv-head as the rows of one matrix: R = B G rows, row b G + g.
 struct PagedSharedParams {

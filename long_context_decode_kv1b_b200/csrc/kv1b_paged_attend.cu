@@ -8,7 +8,7 @@ namespace paged {
 template <bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(const PagedAttendParams p, const int G) {
   extern __shared__ __align__(128) uint8_t smem[];
-  attend_cta<kFine>(p, G, blockIdx.x, smem);
+  attend_cta<kFine, false>(p, G, blockIdx.x, smem);
 }
 
 // Segments cut by a range boundary: block (c, head) merges the one that starts in CTA c's range and goes

@@ -132,7 +132,7 @@ struct Heads {
 };
 
 // `cta` of p.ncta, kThreads threads, kSmem bytes at `smem` (128-byte aligned).
-template <bool kFine>
+template <bool kFine, bool kBeside>
 __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int G_, const int cta, uint8_t* smem) {
   const Heads heads = {p.packed, G_, p.Hq, p.B};
   const int G = p.packed ? 8 : G_;  // rows that a segment may have
@@ -155,7 +155,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
   for (int i = threadIdx.x; i < KV1B_MAX_ROUNDS * kD; i += kThreads) signs[i] = __ldg(p.c.signs + i);
   __shared__ Plan pl;
   {
-    const Plan mine = make_plan<kThreads>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), p.ncta, cta == 0);
+    const Plan mine = make_plan<kThreads, kBeside>(p, pre, slen, reinterpret_cast<uint16_t*>(smem + kOffSome), p.ncta, cta == 0);
     if (lane == 0) pl = mine;  // every warp writes the same
     __syncwarp();
   }

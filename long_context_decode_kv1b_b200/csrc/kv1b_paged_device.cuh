@@ -11,7 +11,6 @@ constexpr float kTau = 8.0f;    // a logit may pass the reference by 2^8 before 
 constexpr float kBase = 7.0f;   // weights are 2^7 at the reference: at most 2^15 < 65504
 constexpr float kNoRef = -1e30f;
 constexpr int kRow = 2 + kD;    // partial row: m (log2 units), l, o[128]
-constexpr int kSegUnits = 8;    // what a segment counts besides its blocks
 constexpr int kMaxSeqs = KV1B_PAGED_MAX_SEQS;
 constexpr int kWaitTries = 4096;
 
@@ -240,7 +239,8 @@ __device__ __forceinline__ int plan_length(const PagedAttendParams& p, int b, bo
 
 // All threads of the CTA.  pre, len and some are in shared memory and, as the plan, the same for every warp: each
 // warp may use them at once.
-template <int THREADS>
+// BESIDE: the plan of a shared call's own tokens beside the matrix kernel's CTAs.
+template <int THREADS, bool BESIDE>
 __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* pre, int* len, uint16_t* some, int ncta, bool report) {
   const int nseq = p.packed + p.B;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -309,6 +309,11 @@ __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* 
   const int64_t units = pl.S + static_cast<int64_t>(kSegUnits) * pl.nsome * pl.Hkv;
   const int64_t want = quotient(units + p.min_units - 1, p.min_units);
   pl.n = static_cast<int>(want < 1 ? 1 : (want < ncta ? want : ncta));
+  if (BESIDE && p.beside > 0) {
+    const int64_t tiles = (static_cast<int64_t>(max(__ldg(p.prefix_len), 0)) + 127) / 128;
+    const int64_t prefix_ns = kPrefixNs + quotient(tiles + p.splits - 1, p.splits) * p.tile_ns;
+    if (kCtaNs + quotient(units * kUnitNs, p.beside) <= prefix_ns) pl.n = p.beside;
+  }
   pl.q = quotient(units, pl.n);
   pl.rem = static_cast<int>(units - pl.q * pl.n);
   return pl;

@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kShThreads, 1) paged_shared_kernel(const Paged
   if (static_cast<int>(blockIdx.x) < units) prefix_cta(p, s, blockIdx.x, smem);
   else if (threadIdx.x < kThreads) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(160));  // 3 x 160 + 32 = 4 x 128
-    attend_cta<kFine>(p, G, blockIdx.x - units, smem);
+    attend_cta<kFine, true>(p, G, blockIdx.x - units, smem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(32));
   }

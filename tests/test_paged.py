@@ -384,6 +384,19 @@ def test_attend_shared_wide_prefix_table(prefix, rows, dtype):
     check_attend(far, q, cache, signs, SCALE, table, lengths, prefix=(pre, prefix))
 
 
+@pytest.mark.parametrize("prefix, own", [(20000, 200), (20000, 0), (20000, 3), (700, 200)])
+def test_attend_shared_own_tokens_beside_the_prefix(prefix, own):
+    # few CTAs for the sequences' own tokens while the prefix is worked on; with a short prefix in the same
+    # table, many behind it
+    lengths, page, H, G = [own - own * (b % 5) // 7 for b in range(40)], 64, 2, 4
+    cache, signs, table, pre = filled(lengths, page, H, 150, prefix=20000)
+    q = (2 * torch.randn((40, H * G, 128), device="cuda")).to(torch.bfloat16)
+    out = cache.attend_shared(q, SCALE, dev(pre), dev([prefix], torch.int32), dev(table), dev(lengths, torch.int32))
+    assert cache.status() == 0
+    some = [0, 1, 17, 39]
+    check_attend(out[some], q[some], cache, signs, SCALE, table[some], [lengths[b] for b in some], prefix=(pre, prefix))
+
+
 def test_attend_shared_bad_prefix():
     lengths, prefix = [40, 70, 1], 150
     cache, signs, table, pre = filled(lengths, 32, 2, 31, prefix=prefix)
