@@ -321,9 +321,15 @@ __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* 
 
 constexpr int kMaxPieces = 512;  // a row's pieces: CTAs of the split, and 148 token ranges of two lanes
 
-// Log-sum-exp merge of n <= kMaxPieces partial rows by a block of 128 threads, a channel each.
+// Log-sum-exp merge of n <= kMaxPieces partial rows by a block of 128 threads.  Warp w takes pieces w, w + 4, ..,
+// kAtOnce of them in flight, two pairs of channels a lane; then the four sums meet.  (A channel a thread and one piece
+// behind another took 23 us for 512 rows of 69 pieces, and 10 for 2,048 rows of 19.)
 template <typename Piece>
 __device__ __forceinline__ void merge_pieces(int n, Piece piece, float2* s_head, float* s_max, void* out, int dtype, int64_t at) {
+  constexpr int kAtOnce = 8;
+  __shared__ float2 s_num[4][kD / 2];
+  __shared__ float s_den[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float M = kNoRef;
   for (int i = threadIdx.x; i < n; i += 128) {
     const float2 h = *reinterpret_cast<const float2*>(piece(i));
@@ -332,17 +338,44 @@ __device__ __forceinline__ void merge_pieces(int n, Piece piece, float2* s_head,
   }
   #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = M;
+  if (lane == 0) s_max[warp] = M;
   __syncthreads();
   M = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-  float num = 0.0f, den = 0.0f;
-  #pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float o = piece(i)[2 + threadIdx.x];
-    const float2 h = s_head[i];
-    const float f = ex2(h.x - M);
-    num = __fmaf_rn(f, o, num);
-    den = __fmaf_rn(f, h.y, den);
+  float2 lo = make_float2(0.0f, 0.0f), hi = lo;
+  float den = 0.0f;
+  #pragma unroll 1
+  for (int i0 = warp; i0 < n; i0 += 4 * kAtOnce) {
+    float2 a[kAtOnce], b[kAtOnce];
+    #pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      a[u] = b[u] = make_float2(0.0f, 0.0f);
+      if (i0 + 4 * u < n) {
+        const float2* o = reinterpret_cast<const float2*>(piece(i0 + 4 * u) + 2);
+        a[u] = o[lane];
+        b[u] = o[32 + lane];
+      }
+    }
+    #pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (i0 + 4 * u < n) {
+        const float2 h = s_head[i0 + 4 * u];
+        const float f = ex2(h.x - M);
+        lo.x = __fmaf_rn(f, a[u].x, lo.x), lo.y = __fmaf_rn(f, a[u].y, lo.y);
+        hi.x = __fmaf_rn(f, b[u].x, hi.x), hi.y = __fmaf_rn(f, b[u].y, hi.y);
+        den = __fmaf_rn(f, h.y, den);
+      }
+    }
+  }
+  s_num[warp][lane] = lo;
+  s_num[warp][32 + lane] = hi;
+  if (lane == 0) s_den[warp] = den;
+  __syncthreads();
+  float num = 0.0f;
+  den = 0.0f;
+  #pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    num = __fadd_rn(num, reinterpret_cast<const float*>(s_num[w])[threadIdx.x]);
+    den = __fadd_rn(den, s_den[w]);
   }
   store_out(out, dtype, at + threadIdx.x, den != 0.0f ? __fdiv_rn(num, den) : 0.0f);
 }
