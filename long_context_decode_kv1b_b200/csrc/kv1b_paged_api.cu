@@ -195,8 +195,8 @@ kv1b::PagedSharedParams shared_plan(int32_t Hkv, int32_t G, int32_t num_seqs, in
 }
 
 // Fewer ranges where the SMs that they leave can do the sequences' own tokens meanwhile, as far as the tables'
-// widths tell (the lengths are the device's to know: it looks again): 171 against 179 us for 64 sequences of 512
-// tokens behind 131,072, 8 kv-heads, 4 heads each.
+// widths tell (the lengths are the device's to know: it looks again): 170 against 179 us for 64 sequences of 512
+// tokens behind 131,072 (8 kv-heads, 4 heads each), 65 against 77 for 100 tokens behind 30,000.
 void side_by_side(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int32_t Hkv, int64_t max_tokens, int64_t own_units) {
   const int64_t tiles = (max_tokens + 127) / 128, units = static_cast<int64_t>(Hkv) * s->row_tiles, sms = num_sms();
   p->tile_ns = s->two ? kv1b::kTile256Ns : kv1b::kTile128Ns;
@@ -222,16 +222,18 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // Whether the attend's kernel takes the prefix, eight rows of a kv-head at a time and the prefix once for each
 // eight, and in how many groups (0: the matrix kernel does).  It starts sooner and costs rows x tiles; measured
 // over 8 kv-heads, it against the other, us:
-//   rows      8 tiles    64 tiles     504 tiles    1,880 tiles   6,256 tiles (of all kv-heads)
-//   16                                             29 against 38    60 against 78
-//   32                   15 against 28  24 against 28  37 against 39   105 against 80
-//   64                   18 against 28  28 against 31  63 against 48   195 against 100
-//   128                  21 against 30  41 against 51  119 against 69
-//   256                  30 against 30  74 against 55
-// The prefix's own length is the device's to know; its table's width stands for it.
+//   rows   64 tiles       504            1,880          6,256 (of all kv-heads)
+//   16                                   26 against 35  57 against 73
+//   32     14 against 20  22 against 24  35 against 36  102 against 76
+//   64     17 against 22  27 against 27  62 against 41  194 against 83
+//   128    20 against 25  40 against 33  118 against 49
+//   256    30 against 30  74 against 39
+// and 47 against 60 for 32 rows of 32 kv-heads, 2,048 tiles, with 300 tokens of each sequence's own.  The prefix's
+// length is the device's to know; its table's width stands for it.
 int packed_groups(int32_t rows, int32_t Hkv, int64_t max_tokens) {
   const int64_t tiles = Hkv * ((max_tokens + 127) / 128);
-  return rows <= 16 || (rows <= 128 && rows * tiles <= 65536) ? (rows + 7) / 8 : 0;
+  const int64_t most = rows <= 16 ? INT64_MAX : (rows <= 32 ? 65536 : (rows <= 128 ? 32768 : 0));
+  return rows * tiles <= most ? (rows + 7) / 8 : 0;
 }
 
 // The buffers of a shared call in its workspace; bytes in all.
