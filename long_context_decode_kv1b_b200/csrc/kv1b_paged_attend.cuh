@@ -34,7 +34,7 @@
 // 12 warps: their 168 registers hold the loop's sums, operands and addresses, where 16 warps' 128 spilled; 8 warps
 // of 255 hid less of the products' latency (178, 190 and 222 us for 1M tokens x 8 heads).
 // 609 warp instructions a block (values expanded to binary16 by fma, a page entry and an address per
-// block) became 389: 243 us for 1M tokens x 8 heads became 176, the issue slots 55 % and the ALU 52 % busy;
+// block) became 389: 243 us for 1M tokens x 8 heads became 174, the issue slots 55 % and the ALU 52 % busy;
 // dependencies of fixed latency bound it.
 #pragma once
 #include "kv1b_paged_device.cuh"
