@@ -318,6 +318,8 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   p.max_prefix_pages = max_prefix_pages;
   p.out = out;
   p.ncta = num_sms();
+  // 12, 16, 24 units a CTA: 11.6, 12.2, 12.9 us for 397 tokens of 8 kv-heads; 13.4, 14.0, 16.4 for 16 rows and 15.6,
+  // 14.2, 16.7 for 32 rows of each behind a prefix of 1,000.  Where there is more work every SM has a CTA anyway.
   p.min_units = 16;
   p.part = static_cast<float*>(ws);
   p.first = p.part + static_cast<size_t>(p.ncta) * 2 * (num_q_heads / cache->num_kv_heads) * kv1b::kPartStride;
