@@ -508,6 +508,8 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
               }
             }
           }
+        } else if (x == edge_at) {  // a block that is not there: the edges behind it still count
+          edge_at = next_edge(seg[cur.s], x + 1);
         }
         __syncwarp();
         // ---- the stage's next block
