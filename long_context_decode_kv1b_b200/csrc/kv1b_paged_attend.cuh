@@ -28,8 +28,15 @@
 // (exact: the product of two 11-bit numbers has 22) goes through a second set of products.  What is left is
 // the subnormal codes' own loss: the tensor cores line a product up by its operands' exponents, so the sums
 // of scale code keep some ten bits fewer than fp32's 24 (2^-14.6 of them seen).
-// Range: p = 2^(x - m + kBase) <= 2^15 and scale < 2 keep p scale finite; a block with a larger scale lowers
-// the weights by its power of two.  A weight keeps 11 bits down to 2^-21 of the reference.
+// Range: p = 2^(x - m + kBase) <= 2^15 and scale < 2 keep p scale finite.  The sums of scale code have a unit, a
+// power of two: 1 for ordinary blocks, whose largest scale is in [2^-7, 2), and else such that a block's scales, as
+// multiples of it, are below 2 and reach 2^-3.  Those blocks' scales are divided by it in place, and the sums are
+// rescaled where a block needs another unit, up or down (exactly: fp32 by a power of two).  Small values held to
+// unit 1 lost their codes where p scale is below 2^-25: errors of 5.6e-7 for 4,096 tokens of 1e-5 behind one 6 nats
+// above them, a result of 1e-6.  The second test costs 1 % (190.6 and 193.1 us for 1M tokens x 8 heads).
+// p keeps 11 bits down to 2^-21 of the reference (2^7), 2^-17 for the weights that are 2^-4 lower; p scale keeps 11
+// down to 2^-21 of reference times unit; below, both lose at most 2^-25, so a token's code part loses at most 2^-24 of
+// its unit, relative to a reference of weight 1.
 //
 // 12 warps: their 168 registers hold the loop's sums, operands and addresses, where 16 warps' 128 spilled; 8 warps
 // of 255 hid less of the products' latency (178, 190 and 222 us for 1M tokens x 8 heads).
@@ -113,7 +120,8 @@ __device__ __forceinline__ int next_edge(const Seg& g, int i) {
   return i < g.skip_from ? g.skip_from - 1 : (i == g.skip_from ? i : g.nb - 1);
 }
 
-constexpr float kCodeUnit = 16777216.0f;  // codes enter the products as binary16 subnormals, units of 2^-24
+constexpr int kCodeBits = 24;  // codes enter the products as binary16 subnormals, units of 2^-24
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
 
 // kFine: the weights of the codes in two binary16 parts (fp16 results); one part is enough for bf16.
 // The query heads of kv-head h that sequence b of the plan serves: G, or up to 8 rows b G' + g of the batch.
@@ -301,9 +309,10 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
     #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
     float m = kNoRef;  // reference of head g
+    int unit = 0;      // acc is in units of 2^(unit - 24)
     // element (i, e, hi) of the weighted value sum of head 2 t + e, channel 16 i + g + 8 hi
     auto value = [&](int i, int e, int hi) {
-      return __fmaf_rn(acc[i][2 * hi + e], kCodeUnit, __shfl_sync(kFull, side[e], 4 * (i >> 1) + t));
+      return __fmaf_rn(acc[i][2 * hi + e], power_of_two(kCodeBits + unit), __shfl_sync(kFull, side[e], 4 * (i >> 1) + t));
     };
     // the warp's sums of a segment to a piece [head][kRow]
     auto put_piece = [&](float* w) {
@@ -354,8 +363,8 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
       side[0] = side[1] = side[2] = side[3] = 0.0f;
       m = 0.0f;
       bool fresh = true;   // no block has set m
-      float bar = kBase + kTau;  // an exponent past it raises the reference
-      int top_scale = 0;   // weights are 2^-top_scale lower: no scale reaches 2^(1 + top_scale)
+      unit = 0;
+      uint32_t ordinary = 0x20002000u;  // the bit that a scale of [2^-7, 2) has; none where every block is looked at
       const bool starts = cur.i == 0;
       const int count = min(cur.left, seg[cur.s].nb - cur.i);  // blocks of the segment in the warp's run
       const bool ends = cur.i + count == seg[cur.s].nb;
@@ -419,25 +428,35 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
           }
           lds128(mn, g < 4 ? st + kBlkOffMin + g * 64 + 16 * t : side_row);
           {
-            // the block's 128 scales, four a lane: one of 2 or more has the top exponent bit
+            // the block's 128 scales, four a lane: whether one is 2 or more, or a lane has none of 2^-7
+            const uint32_t at = st + kBlkOffScale + 8 * lane;
             uint32_t w0, w1;
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(st + kBlkOffScale + 8 * lane) : "memory");
-            if (__any_sync(kFull, ((w0 | w1) & 0x40004000u) != 0)) {  // rare: large values
-              int k = max(max(static_cast<int>(w0 & 0x7C00u), static_cast<int>((w0 >> 16) & 0x7C00u)),
-                          max(static_cast<int>(w1 & 0x7C00u), static_cast<int>((w1 >> 16) & 0x7C00u)));
-              k = __reduce_max_sync(kFull, (k >> 10) - 15);  // all scales are below 2^(1 + k)
-              if (k > top_scale) {
-                const float f = ex2(static_cast<float>(top_scale - k));
-                m += static_cast<float>(k - top_scale);
-                top_scale = k;
-                bar = kBase + kTau - static_cast<float>(k);
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
+            if (__any_sync(kFull, ((w0 | w1) & 0x40004000u) != 0 || ((w0 | w1) & ordinary) == 0)) {
+              uint32_t top = max(max(w0 & 0xFFFFu, w0 >> 16), max(w1 & 0xFFFFu, w1 >> 16));
+              top = __reduce_max_sync(kFull, top);  // the largest, as its bits
+              if (top != 0) {
+                const int k = top >= 0x400u ? static_cast<int>(top >> 10) - 15 : 7 - __clz(top);  // 2^k <= it < 2^(k + 1)
+                if (k > unit || k < unit - (unit == 0 ? 7 : 3)) {
+                  const int to = k <= 0 && k >= -7 ? 0 : k;
+                  const float f = power_of_two(unit - to);
+                  unit = to;
+                  ordinary = to == 0 ? 0x20002000u : 0u;
                   #pragma unroll
-                  for (int e = 0; e < 4; ++e) acc[i][e] = __fmul_rn(acc[i][e], f);
+                  for (int i = 0; i < 8; ++i) {
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][e] = __fmul_rn(acc[i][e], f);
+                  }
                 }
-                #pragma unroll
-                for (int e = 0; e < 4; ++e) side[e] = __fmul_rn(side[e], f);
+                if (unit != 0) {  // by 2^-unit, in two factors: neither 2^24 nor 2^-15 is a normal binary16
+                  const int up = max(min(-unit, 12), -14);
+                  const uint32_t f0 = static_cast<uint32_t>(15 + up) * 0x04000400u, f1 = static_cast<uint32_t>(15 - unit - up) * 0x04000400u;
+                  w0 = hmul2(hmul2(w0, f0), f1);
+                  w1 = hmul2(hmul2(w1, f0), f1);
+                  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(w0), "r"(w1) : "memory");
+                  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy to the stage
+                  __syncwarp();
+                }
               }
             }
           }
@@ -454,10 +473,10 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
             for (int j = 0; j < 8; ++j) y[j] = (mine >> j) & 1u ? y[j] : -INFINITY;
           }
           float mx = fmaxf(max3(max3(y[0], y[1], y[2]), y[3], y[4]), max3(y[5], y[6], y[7]));
-          if (__any_sync(kFull, mx > bar) || fresh) {  // rare: raise references
+          if (__any_sync(kFull, mx > kBase + kTau) || fresh) {  // rare: raise references
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-            const float rise = fresh || mx > bar ? mx - (bar - kTau) : 0.0f;
+            const float rise = fresh || mx > kBase + kTau ? mx - kBase : 0.0f;
             const float alpha = fresh ? 0.0f : ex2(-rise);
             m += rise;
             #pragma unroll

@@ -86,3 +86,97 @@ def test_attend_shared_missing_first_page_before_a_partial_last_block():
     assert cache.status() == kv.STATUS_BAD_INDEX and torch.isfinite(out).all()
     check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(32, lengths[b]), some_rows(rng, 16, 64, 60),
                prefix=(pre, np.arange(32, prefix)))
+
+
+# ------------------------------------------------------------------------------------- values of every size
+def unit_tolerance(row, eps):
+    """As Row.tolerance, but what small weights may lose goes with the values' size: a block's scales enter the products
+    as their multiple of a power of two whose largest is below 2 and at least 2^-7 where they are ordinary (unit 1),
+    else at least 2^-3 (unit at most 8 of the largest scale).  A token's weight scale may lose 2^-25 of the unit, 2^4 more
+    where its code sits four bits higher, times a code of 15, behind a reference of 2^7: 2^-24 of the unit.  Its weight
+    as a subnormal loses 2^-25, 2^-21 where it is lowered, behind 2^7: 2^-32 of the largest |value|, twice for the
+    normaliser, and 2^-28 of 15 scales.  Scales of 2 or more come down by their power of two and may lose 2^-25 of
+    15 units each time their weight counts.  Minima that are subnormal operands: a product of theirs keeps 2^-38 of
+    its largest weight, 17 terms."""
+    if row.tokens == 0:
+        return np.full(ref.D, 1e-30)
+    unit = 8 * row.step if row.step < 2.0 ** -7 else max(1.0, 8 * row.step if row.step >= 2 else 1.0)
+    rel = 3 * 2.0 ** -11 + 2 * (16 * 2.0 ** -24 * row.mag + 2.0 ** -21) + 2.0 ** -18
+    tail = row.tokens * (2.0 ** -24 * unit + 2.0 ** -31 * row.largest + 2.0 ** -24 * row.step)
+    tail += 2.0 ** -21 * unit * (row.step >= 2) + 17 * 2.0 ** -38
+    part = 2.0 ** -11 if eps > 2.0 ** -9 else 2.0 ** -13
+    return (1 + eps) * (rel * row.spread + part * row.reach + tail) + eps / 2 * np.abs(row.out) + 2.0 ** -25
+
+
+def sized_cache(n, H, size, lead, growing=False, page=64):
+    """A cache of one list of pages with n tokens of normal values of a size (growing: from a 1024th of it on), the logits
+    of one token `lead` above the others' for queries near `q`; (cache, signs, pages, q of a kv-head)."""
+    g = torch.Generator(device="cuda").manual_seed(46)
+    num = (n + page - 1) // page
+    cache, signs = new_cache(num + 1, H, page)
+    k, v = torch.randn((2, n, H, 128), generator=g, device="cuda")
+    q = torch.randn((H, 128), generator=g, device="cuda")
+    k *= 0.05
+    # the 1-bit key of 0.05 z + a q reads q at about its norm: logit |q|^2 a / sqrt(128) over the others'
+    k[n // 3] = q * (lead / (q.square().sum(1, keepdim=True) * SCALE))
+    v *= size
+    if growing:
+        v *= torch.logspace(-10, 0, n, base=2.0, device="cuda")[:, None, None]
+    v.clamp_(-65504, 65504)
+    pages = np.random.default_rng(46).permutation(num).astype(np.int32)
+    cache.append(k, v, dev(pages[None]), dev([0], torch.int32), dev([0, n], torch.int32))
+    return cache, signs, pages, q
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n, lead", [(860, 8.0), (4096, 0.0), (4096, 6.0)])
+@pytest.mark.parametrize("size", [3e-6, 1e-5, 1e-4, 1e-3, 0.03, 1.0, 40.0, 30000.0])
+def test_attend_values_of_every_size(size, n, lead, dtype):
+    # one run of tokens a warp, so that the leading token is the reference of the others: 148 x 12 segments at least
+    H, G = 2, 4
+    cache, signs, pages, q1 = sized_cache(n, H, size, lead)
+    B = 148 * 12 // H // 2
+    q = (q1[:, None].expand(H, G, 128).reshape(1, H * G, 128) + 0.02 * torch.randn((B, H * G, 128), device="cuda")).to(dtype)
+    table = np.tile(pages, (B, 1))
+    out = cache.attend(q, SCALE, dev(table), dev([n] * B, torch.int32))
+    assert cache.status() & ~kv.STATUS_FP16_SATURATED == 0
+    rows = some_rows(np.random.default_rng(6), B, H * G, 12)
+    check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(n), rows, tolerance=unit_tolerance)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("turned", [False, True])
+@pytest.mark.parametrize("size", [1e-2, 8.0, 60000.0])
+def test_attend_values_that_grow_or_fall(size, turned, dtype):
+    # sizes that change by 2^10 along a warp's run, up or down, with a flat softmax
+    n, H, G = 1500, 2, 2
+    cache, signs, pages, q1 = sized_cache(n, H, size, 0.0, growing=True)
+    if turned:  # whole pages back to front
+        n = n // 64 * 64
+        pages = pages[:n // 64][::-1].copy()
+    B = 500
+    q = (q1[:, None].expand(H, G, 128).reshape(1, H * G, 128) + torch.randn((B, H * G, 128), device="cuda")).to(dtype)
+    table = np.tile(pages, (B, 1))
+    out = cache.attend(q, SCALE, dev(table), dev([n] * B, torch.int32))
+    rows = some_rows(np.random.default_rng(7), B, H * G, 12)
+    check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(n), rows, tolerance=unit_tolerance)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("growing", [False, True])
+@pytest.mark.parametrize("rows", [32, 160])
+@pytest.mark.parametrize("size", [1e-5, 1e-3, 40.0, 60000.0])
+def test_matrix_prefix_values_of_every_size(size, rows, growing, dtype):
+    # a prefix that the matrix kernel takes, values small, large or growing along it, one token ahead
+    n, H, G = 9000, 8, 4
+    cache, signs, pages, q1 = sized_cache(n, H, size, 5.0, growing=growing)
+    B = rows // G
+    q = (q1[:, None].expand(H, G, 128).reshape(1, H * G, 128) + 0.1 * torch.randn((B, H * G, 128), device="cuda")).to(dtype)
+    wide = np.full((40000 // 64,), -1, np.int32)
+    wide[:len(pages)] = pages
+    own = np.tile(pages[5:6], (B, 1))  # and own tokens of the same sizes
+    lengths = [int(x) for x in np.arange(B) % 60]
+    out = cache.attend_shared(q, SCALE, dev(wide), dev([n], torch.int32), dev(own), dev(lengths, torch.int32))
+    assert cache.status() & ~kv.STATUS_FP16_SATURATED == 0
+    check_rows(out, q, cache, signs, SCALE, own, lambda b: np.arange(lengths[b]), some_rows(np.random.default_rng(8), B, H * G, 6),
+               prefix=(pages, np.arange(n)), tolerance=unit_tolerance)
