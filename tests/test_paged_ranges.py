@@ -180,3 +180,75 @@ def test_matrix_prefix_values_of_every_size(size, rows, growing, dtype):
     assert cache.status() & ~kv.STATUS_FP16_SATURATED == 0
     check_rows(out, q, cache, signs, SCALE, own, lambda b: np.arange(lengths[b]), some_rows(np.random.default_rng(8), B, H * G, 6),
                prefix=(pages, np.arange(n)), tolerance=unit_tolerance)
+
+
+# ------------------------------------------------------------------- references that rise in the matrix kernel
+def rising(kind, n):
+    """Factors of the query along the tokens: its share of each key, so logits of about 11 times it."""
+    x = np.linspace(0, 1, n)
+    return {"rising": 8 * x, "falling": 8 - 8 * x, "steps": np.floor(6 * x) * 1.3, "late": np.where(x > 0.9, 5.0, 0.1),
+            "low first": np.where(np.arange(n) % 1200 < 64, 0.0, 0.35)}[kind]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows", [32, 132, 160])
+@pytest.mark.parametrize("kind", ["rising", "falling", "steps", "late", "low first"])
+def test_matrix_prefix_references_that_rise(kind, rows, dtype):
+    # every row, a few rows of a warp or none have logits that pass what the first tokens set
+    n, H, G, page = 20000, 8, 4, 64
+    g = torch.Generator(device="cuda").manual_seed(47)
+    num = (n + page - 1) // page
+    cache, signs = new_cache(num + 1, H, page)
+    k = 0.3 * torch.randn((n, H, 128), generator=g, device="cuda")
+    v = torch.randn((n, H, 128), generator=g, device="cuda")
+    q1 = torch.randn((H, 128), generator=g, device="cuda")
+    k += dev(rising(kind, n), torch.float32)[:, None, None] * q1
+    B = rows // G
+    share = torch.ones((B, 1, G, 1), device="cuda")
+    if B % 2 == 0:
+        share[1::3] = 0.1      # rows that hardly rise among those that do
+        share[2::5] = -1.0     # and rows whose logits fall
+    q = (share * q1[None, :, None] + 0.1 * torch.randn((B, H, G, 128), generator=g, device="cuda")).reshape(B, H * G, 128).to(dtype)
+    pages = np.random.default_rng(47).permutation(num).astype(np.int32)
+    cache.append(k, v, dev(pages[None]), dev([0], torch.int32), dev([0, n], torch.int32))
+    wide = np.full((40000 // page,), -1, np.int32)
+    wide[:num] = pages
+    own = np.tile(pages[:1], (B, 1))
+    lengths = [int(x) for x in np.arange(B) % 50]
+    args = (q, SCALE, dev(wide), dev([n], torch.int32), dev(own), dev(lengths, torch.int32))
+    out = cache.attend_shared(*args)
+    assert cache.status() == 0 and torch.equal(out, cache.attend_shared(*args))
+    picks = some_rows(np.random.default_rng(9), B, H * G, 6) + [(1, 3), (2, 3)]
+    check_rows(out, q, cache, signs, SCALE, own, lambda b: np.arange(lengths[b]), picks, prefix=(pages, np.arange(n)))
+
+
+def test_matrix_prefix_low_first_tokens_take_no_longer():
+    # 64 first tokens that score low, then all higher than them by some 2^5: the reference rises once, where rows that
+    # kept the first one sent their warps through each job three times (1.8 times as long).  148 heads: one token range
+    n, H, G, B, page = 4096, 148, 4, 33, 128
+    g = torch.Generator(device="cuda").manual_seed(48)
+    q1 = torch.randn((H, 128), generator=g, device="cuda")
+    q = (q1[None, :, None] + 0.1 * torch.randn((B, H, G, 128), generator=g, device="cuda")).reshape(B, H * G, 128).to(torch.bfloat16)
+    share = torch.full((n, 1, 1), 0.3, device="cuda")
+    calls = []
+    for low in (False, True):
+        cache, _ = new_cache(n // page, H, page)
+        if low:
+            share[:64] = 0.0
+        k = (0.3 * torch.randn((n, H, 128), generator=g, device="cuda") + share * q1).to(torch.bfloat16)
+        pages = torch.arange(n // page, dtype=torch.int32, device="cuda")
+        cache.append(k, k, pages[None], dev([0], torch.int32), dev([0, n], torch.int32))
+        calls.append(lambda c=cache, args=(q, SCALE, pages, dev([n], torch.int32), pages[:1].repeat(B)[:, None],
+                                           dev([0] * B, torch.int32)): c.attend_shared(*args))
+    best = [1e9, 1e9]
+    for _ in range(6):
+        for i, call in enumerate(calls):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda.synchronize()
+            a.record()
+            for _ in range(10):
+                call()
+            b.record()
+            torch.cuda.synchronize()
+            best[i] = min(best[i], a.elapsed_time(b))
+    assert best[1] < 1.5 * best[0], best
