@@ -252,3 +252,38 @@ def test_matrix_prefix_low_first_tokens_take_no_longer():
             torch.cuda.synchronize()
             best[i] = min(best[i], a.elapsed_time(b))
     assert best[1] < 1.5 * best[0], best
+
+
+# --------------------------------------------------------------------- more segments than a CTA takes at once
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heads, group", [(8, 8), (16, 2)])
+def test_attend_more_segments_than_a_round(heads, group, dtype):
+    # 1,024 sequences x heads over 148 CTAs: more than the 256 / group, at most 64, segments that a CTA holds
+    rng = np.random.default_rng(4)
+    lengths = [int(x) for x in rng.integers(0, 71, 1024)]
+    lengths[5] = lengths[1023] = 0
+    lengths[700] = 900
+    cache, signs, table, _ = filled(lengths, 32, heads, 44)
+    q = (2 * torch.randn((1024, heads * group, 128), device="cuda")).to(dtype)
+    args = (q, SCALE, dev(table), dev(lengths, torch.int32))
+    out = cache.attend(*args)
+    assert cache.status() == 0 and torch.equal(out, cache.attend(*args))
+    assert (out[5] == 0).all() and (out[1023] == 0).all()
+    rows = some_rows(rng, 1024, heads * group, 300) + [(700, h) for h in range(heads * group)]
+    check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(lengths[b]), rows)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("group", [4, 8])
+def test_attend_shared_more_own_segments_than_a_round(group, dtype):
+    # 2,048 segments of one block on the 20 CTAs that the prefix's token ranges leave to them
+    rng = np.random.default_rng(5)
+    lengths, prefix = [int(x) for x in rng.integers(0, 33, 256)], 30000
+    lengths[9] = 0
+    cache, signs, table, pre = filled(lengths, 32, 8, 45, prefix=prefix, width=1)
+    q = (2 * torch.randn((256, 8 * group, 128), device="cuda")).to(dtype)
+    args = (q, SCALE, dev(pre), dev([prefix], torch.int32), dev(table), dev(lengths, torch.int32))
+    out = cache.attend_shared(*args)
+    assert cache.status() == 0 and torch.equal(out, cache.attend_shared(*args))
+    check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(lengths[b]), some_rows(rng, 256, 8 * group, 40) + [(9, 3)],
+               prefix=(pre, np.arange(prefix)))
