@@ -287,3 +287,68 @@ def test_attend_shared_more_own_segments_than_a_round(group, dtype):
     assert cache.status() == 0 and torch.equal(out, cache.attend_shared(*args))
     check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(lengths[b]), some_rows(rng, 256, 8 * group, 40) + [(9, 3)],
                prefix=(pre, np.arange(prefix)))
+
+
+# ----------------------------------------------------------------------- the prompt encoder with several heads a warp
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("heads, tokens, q_heads, rot, sections, interleaved", [
+    (32, 2200, 40, 128, [64], False),             # two heads a warp, query rows in two parts a token
+    (33, 4500, 33, 64, [32], True),               # four and a last one
+    (3, 51000, 3, 128, [16, 24, 24], False),      # four, of which there are three
+    (10, 10500, 80, 80, [40], False),             # three, a last one; rotary widths that are read again
+    (8, 16600, 8, 0, [], False),
+])
+def test_append_of_several_heads_a_warp(heads, tokens, q_heads, rot, sections, interleaved, dtype):
+    # byte for byte what short calls store, in which a warp takes one head; some tokens against the oracle's encoder
+    page, rng = 64, np.random.default_rng(10)
+    n = np.diff(np.sort(np.concatenate([[0, tokens], rng.integers(0, tokens, 4)])))
+    n = np.append(n, 0)
+    start = rng.integers(0, 100, len(n)).astype(np.int32)
+    counts = [(int(s + x) + page - 1) // page for s, x in zip(start, n)]
+    cache, signs = new_cache(sum(counts) + 1, heads, page, fill=11)
+    same = kv.PagedCache.wrap(cache.pages.clone(), cache.signs)
+    before = cache.pages.clone()
+    table, _ = table_for(counts, sum(counts) + 1, rng)
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    assert (tokens // 8 + 2 * len(n)) * heads >= 2 * 148 * 28
+    g = torch.Generator(device="cuda").manual_seed(12)
+    qkv = torch.randn((tokens, q_heads + 2 * heads, 128), generator=g, device="cuda").to(dtype)
+    q, k, v = qkv[:, :q_heads], qkv[:, q_heads:q_heads + heads], qkv[:, q_heads + heads:]
+    kw, rope_np, pos = {}, None, None
+    if rot:
+        cs = rope_table(500, rot)
+        pos = rng.integers(0, 500, (len(sections), tokens)).astype(np.int32)
+        kw = dict(rope=kv.Rope(dev(cs), sections=sections, interleaved=interleaved))
+        rope_np = (cs, sections, interleaved)
+    tab = dev(table)
+    got = cache.append(k, v, tab, dev(start), dev(cu), q=q, positions=dev(pos) if rot else None, **kw)
+    part = 8288 // heads * 4      # tokens of a call that gives a warp one head
+    want = torch.empty_like(got)
+    for b in range(len(n)):
+        for t0 in range(cu[b], cu[b + 1], part):
+            t1 = min(t0 + part, cu[b + 1])
+            assert (-(-(t1 - t0) // 8) + 2) * heads < 2 * 148 * 28
+            at = dict(positions=dev(pos[:, t0:t1])) if rot else {}
+            want[t0:t1] = same.append(k[t0:t1], v[t0:t1], tab[b:b + 1], dev([start[b] + t0 - cu[b]], torch.int32),
+                                      dev([0, t1 - t0], torch.int32), q=q[t0:t1], **at, **kw)
+    assert cache.status() == 0 and same.status() == 0
+    assert torch.equal(cache.pages, same.pages) and torch.equal(got, want)
+    # single tokens: the first and last of a sequence, some between
+    after, before = cache.pages.cpu().numpy(), before.cpu().numpy()
+    for b in range(len(n)):
+        for t in {int(cu[b]), int(cu[b + 1]) - 1, int(cu[b] + n[b] // 2)} if n[b] else ():
+            p = int(start[b]) + t - int(cu[b])
+            page_no, off = table[b, p // page], p % page
+            one = ref.append(before, ref.to_np(k[t:t + 1]), ref.to_np(v[t:t + 1]), table[b:b + 1], [p], [0, 1], signs, rope_np,
+                             pos[:, t:t + 1] if rot else None)
+            blk, tok = off // 32, off % 32
+            for h in {0, heads // 2, heads - 1}:
+                a, w = ref.fields(after[page_no, h, blk]), ref.fields(one[page_no, h, blk])
+                assert (a[0][ref.bit_row(tok)] == w[0][ref.bit_row(tok)]).all() and a[1][tok] == w[1][tok]
+                assert (a[2][:, tok] == w[2][:, tok]).all() and (a[3][:, tok] == w[3][:, tok]).all()
+                mask = np.uint32(15) << np.uint32(4 * ref.nibble(tok))
+                assert ((a[4][:, tok // 8] & mask) == (w[4][:, tok // 8] & mask)).all()
+            for hq in {0, q_heads - 1}:
+                row = ref.to_np(q[t, hq])[None]
+                row = ref.turn(row, rope_np[0], [pos[a][t] for a in range(len(sections))], sections, interleaved) if rot else row
+                assert torch.equal(got[t, hq].cpu(), torch.from_numpy(row[0]).to(dtype))
