@@ -383,8 +383,11 @@ int kv1b_paged_signs(float* signs, uint64_t seed, int32_t rounds, int32_t* d_sta
  *   page_table[b*table_stride + i], i < max_pages.
  * rope: NULL for none; positions: i32, token row t on axis a at positions[a*pos_stride + t].
  * q, q_out: NULL, or the queries (element (t, h, c) at q[t*q_stride_t + h*q_stride_h + c], h <
- *   num_q_heads) and where their turned rows go, in `dtype` (copied when rope is NULL; q_out may be q
- *   with the same strides; its rows may not overlap).
+ *   num_q_heads) and where their turned rows go, in `dtype` (copied when rope is NULL).  q_out may be q
+ *   with the same strides.  Otherwise no row of it may share an element with another of its rows or with
+ *   a row of q, k or v, else KV1B_ERR_INVALID_ARG: told apart exactly where one stride of q_out steps over
+ *   all rows along the other and the two tensors' token strides (or head strides) agree, as slices of one
+ *   buffer have them; taken to meet where their address ranges do and the strides are of another kind.
  * Encoded as kv1b_encode_append, except that values are first limited to +-65504 (NaN to 0) and a
  * group's scale is one binary16 step lower where min + 15 scale would pass 65504.
  * Skipped, with KV1B_STATUS_BAD_INDEX: tokens whose page is outside [0, num_pages) or past max_pages,

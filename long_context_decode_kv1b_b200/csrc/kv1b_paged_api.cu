@@ -72,6 +72,57 @@ int table_check(const kv1b_paged_t* c, int32_t num_seqs, int64_t table_stride, i
   return KV1B_OK;
 }
 
+// The rows of a tensor [T][H][128]: element strides of a token and a head.
+struct Rows {
+  uintptr_t base;
+  int64_t T, st, H, sh;
+};
+typedef __int128 Wide;
+constexpr Wide kRowElems = KV1B_HEAD_DIM;
+
+Wide span(int64_t n, int64_t stride) { return Wide(n - 1) * stride + kRowElems; }  // of n rows
+
+// No two rows share an element: one stride steps over all rows along the other.
+bool rows_apart(const Rows& r) {
+  if ((r.T > 1 && r.st < kRowElems) || (r.H > 1 && r.sh < kRowElems)) return false;
+  return r.T == 1 || r.H == 1 || r.st >= span(r.H, r.sh) || r.sh >= span(r.T, r.st);
+}
+
+// About the d of lo .. hi for which x + d step is nearest to 0 (one of its neighbours may be nearer).
+Wide nearest(Wide x, Wide step, Wide lo, Wide hi) {
+  const Wide d = -x / step;
+  return d < lo ? lo : (d > hi ? hi : d);
+}
+
+// Whether rows 0, a, 2 a, .. (na of them) and x, x + b, .. (nb) share an element; true also where they only may.
+bool lines_meet(int64_t na, int64_t a, Wide x, int64_t nb, int64_t b) {
+  if (x >= span(na, a) || x + span(nb, b) <= 0) return false;
+  if (na > 1 && nb > 1 && a != b) return true;
+  const Wide step = na > 1 ? a : b, lo = -Wide(na - 1), hi = nb - 1;  // x + d step for d = lo .. hi against one row at 0
+  if (step == 0) return true;
+  const Wide at = nearest(x, step, lo, hi);
+  for (Wide d = at - 1; d <= at + 1; ++d)
+    if (d >= lo && d <= hi && x + d * step > -kRowElems && x + d * step < kRowElems) return true;
+  return false;
+}
+
+// Whether rows that are apart and those of another tensor of as many tokens share an element: exactly where their
+// strides of tokens, or of heads, agree and step over the other dimension; else where their ranges meet.
+bool rows_meet(const Rows& o, const Rows& r, int64_t es) {
+  if (o.base == r.base) return true;
+  const Wide delta = r.base > o.base ? Wide((r.base - o.base) / es) : -Wide((o.base - r.base) / es);
+  if (delta >= Wide(o.T - 1) * o.st + span(o.H, o.sh) || delta + Wide(r.T - 1) * r.st + span(r.H, r.sh) <= 0) return false;
+  auto outer = [&](int64_t no, int64_t nr, int64_t so, int64_t sr, int64_t mo, int64_t a, int64_t mr, int64_t b) {
+    if (no == 1 && nr == 1) return lines_meet(mo, a, delta, mr, b);
+    if (so != sr || so < span(mo, a) || so < span(mr, b)) return true;
+    const Wide lo = -Wide(no - 1), hi = nr - 1, at = nearest(delta, so, lo, hi);
+    for (Wide d = at - 1; d <= at + 1; ++d)  // so steps over both: no other d comes near
+      if (d >= lo && d <= hi && lines_meet(mo, a, delta + d * so, mr, b)) return true;
+    return false;
+  };
+  return outer(o.T, r.T, o.st, r.st, o.H, o.sh, r.H, r.sh) && outer(o.H, r.H, o.sh, r.sh, o.T, o.st, r.T, r.st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -132,9 +183,21 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
   if (q || q_out) {
     if (!q || !q_out || q_stride_t < 0 || q_stride_h < 0 || qo_stride_t < 0 || qo_stride_h < 0) return KV1B_ERR_INVALID_ARG;
     if (num_q_heads < 1 || num_q_heads > KV1B_PAGED_MAX_HEADS) return KV1B_ERR_INVALID_ARG;
-    if ((num_tokens > 1 && qo_stride_t < KV1B_HEAD_DIM) || (num_q_heads > 1 && qo_stride_h < KV1B_HEAD_DIM)) return KV1B_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(q_out, 16) || q_stride_t % 4 || q_stride_h % 4 || qo_stride_t % 4 || qo_stride_h % 4)
       return KV1B_ERR_MISALIGNED;
+    if (num_tokens > 0) {
+      // rows are written while others are read: a result row is no other's, nor an input's but its own
+      auto rows = [&](const void* ptr, int64_t st, int64_t H, int64_t sh) {
+        return Rows{reinterpret_cast<uintptr_t>(ptr), num_tokens, st, H, sh};
+      };
+      const Rows out = rows(q_out, qo_stride_t, num_q_heads, qo_stride_h);
+      const bool in_place = q == q_out && (num_tokens == 1 || q_stride_t == qo_stride_t) && (num_q_heads == 1 || q_stride_h == qo_stride_h);
+      const int64_t es = dtype == KV1B_DTYPE_F32 ? 4 : 2;
+      if (!rows_apart(out) || (!in_place && rows_meet(out, rows(q, q_stride_t, num_q_heads, q_stride_h), es)) ||
+          rows_meet(out, rows(k, k_stride_t, cache->num_kv_heads, k_stride_h), es) ||
+          rows_meet(out, rows(v, v_stride_t, cache->num_kv_heads, v_stride_h), es))
+        return KV1B_ERR_INVALID_ARG;
+    }
     p.q = q;
     p.q_out = q_out;
     p.Hq = num_q_heads;

@@ -132,6 +132,19 @@ def test_shared_prefix_refusals(lib):
         assert lib.kv1b_paged_attend_shared(ctypes.addressof(d), P, 1, 8, 0.1, 2, *pre, *tail) == code
 
 
+@pytest.mark.parametrize("change", [
+    dict(qs0=1024, qs1=128, os0=128, os1=128), dict(qs0=1024, qs1=128, os0=1024, os1=256),       # rows over one another
+    dict(q=P + 256, qs0=1024, qs1=128, os0=1024, os1=128), dict(q=P, qs0=2048, qs1=128, os0=1024, os1=128),
+    dict(q=P + 64, qs0=1024, qs1=128, os0=1024, os1=128), dict(q=P, qs0=0, qs1=0, os0=1024, os1=128),
+    dict(k=P + 2 * 1024, kst=2048, qs0=1024, qs1=128, q=2 * P, os0=1024, os1=128),
+    dict(v=P + 2 * 896, vst=1024, qs0=1024, qs1=128, q=2 * P, os0=1024, os1=128)])
+def test_append_refuses_rows_that_meet(lib, change):
+    d = desc()
+    a = dict(APPEND, cache=ctypes.addressof(d), k=3 * P, v=4 * P, q=P, qo=P, hq=8)
+    a.update(change)
+    assert lib.kv1b_paged_append(*a.values()) == -1
+
+
 # ---- the plain forms themselves
 def test_reference_turn_is_a_rotation_by_the_positions_angle():
     rng = np.random.default_rng(0)

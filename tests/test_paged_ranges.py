@@ -352,3 +352,75 @@ def test_append_of_several_heads_a_warp(heads, tokens, q_heads, rot, sections, i
                 row = ref.to_np(q[t, hq])[None]
                 row = ref.turn(row, rope_np[0], [pos[a][t] for a in range(len(sections))], sections, interleaved) if rot else row
                 assert torch.equal(got[t, hq].cpu(), torch.from_numpy(row[0]).to(dtype))
+
+
+# ------------------------------------------------------------------------- results beside and over their inputs
+def row_elements(offset, T, st, H, sh):
+    return (offset + np.arange(T)[:, None, None] * st + np.arange(H)[None, :, None] * sh + np.arange(128)).ravel()
+
+
+def test_append_refuses_query_rows_that_meet():
+    # layouts drawn at random inside one buffer, with what shares an element counted out element by element
+    rng = np.random.default_rng(13)
+    buf = torch.randn((1 << 16,), device="cuda", dtype=torch.float16)
+    cache, _ = new_cache(4, 2, 32)
+    seen = {True: 0, False: 0}
+    for trial in range(600):
+        T, H = int(rng.integers(1, 5)), int(rng.integers(1, 5))
+        near = lambda x: int(x + 8 * rng.choice([0, 0, 0, -1, 1, -8, 8]))  # noqa: E731
+        if rng.random() < 0.6:
+            sh = max(0, near(128 * rng.integers(1, 3)))
+            st = max(0, near(sh * int(rng.choice([H, 2 * H, 3 * H]))))
+        else:
+            st = max(0, near(128 * rng.integers(1, 3)))
+            sh = max(0, near(st * int(rng.choice([T, 2 * T]))))
+        o0 = 8 * int(rng.integers(0, 1024))
+        how = rng.random()
+        q0, qst, qsh = o0 + int(rng.choice([0, 128, -128, sh, st, H * sh, 8, 64, 2 * st + sh, 4096])), st, sh
+        if how < 0.2:
+            qst, qsh = int(rng.choice([0, 128, 256, 512])), int(rng.choice([0, 128, 384]))
+        kv0 = o0 + int(rng.choice([8192, 8192, 8192, H * sh, -2 * sh, 64]))
+        if min(q0, kv0) < 0:
+            continue
+        view = lambda at, t, n, h: buf.as_strided((T, n, 128), (t, h, 1), at)  # noqa: E731
+        out, q, k = view(o0, st, H, sh), view(q0, qst, H, qsh), view(kv0, st, 2, sh)
+        mine = row_elements(o0, T, st, H, sh)
+        others = row_elements(kv0, T, st, 2, sh)
+        same = q0 == o0 and (T == 1 or qst == st) and (H == 1 or qsh == sh)
+        if not same:
+            others = np.concatenate([others, row_elements(q0, T, qst, H, qsh)])
+        meet = len(np.unique(mine)) < len(mine) or len(np.intersect1d(mine, others)) > 0
+        nested = T == 1 or H == 1 or st >= (H - 1) * sh + 128 or sh >= (T - 1) * st + 128
+        agree = nested and (same or T == 1 or H == 1 or (qst, qsh) == (st, sh)) and \
+            (T == 1 or st >= max((H - 1) * sh, sh) + 128 or H == 2) and how >= 0.2
+        call = lambda: cache.append(k, k, dev([[0]], torch.int32), dev([0], torch.int32), dev([0, T], torch.int32), q=q, q_out=out)  # noqa: E731
+        expect, before = q.clone(), buf.clone()
+        try:
+            call()
+        except kv.Kv1bError as e:
+            assert e.code == -1 and torch.equal(buf, before)
+            assert meet or not agree, (T, H, st, sh, o0, q0, qst, qsh, kv0)
+            seen[True] += 1
+        else:
+            assert not meet, (T, H, st, sh, o0, q0, qst, qsh, kv0)
+            assert torch.equal(out, expect)
+            rest = torch.ones_like(buf, dtype=torch.bool)
+            rest[dev(mine)] = False
+            assert torch.equal(buf[rest], before[rest])
+            seen[False] += 1
+    assert min(seen.values()) > 100, seen
+    # what serving code does: a slice turned in place, into a neighbouring slice, and transposed
+    qkv = torch.randn((6, 12, 128), device="cuda", dtype=torch.float16)
+    args = (qkv[:, 8:10], qkv[:, 10:], dev([[0]], torch.int32), dev([0], torch.int32), dev([0, 6], torch.int32))
+    rope = dict(rope=kv.Rope(dev(rope_table(64, 128))), positions=torch.arange(6, dtype=torch.int32, device="cuda"))
+    want = cache.append(*args, q=qkv[:, :4], **rope)
+    cache.append(*args, q=qkv[:, :4], q_out=qkv[:, 4:8], **rope)
+    assert torch.equal(qkv[:, 4:8], want)
+    turned = torch.empty((4, 6, 128), device="cuda", dtype=torch.float16).transpose(0, 1)
+    assert torch.equal(cache.append(*args, q=qkv[:, :4], q_out=turned, **rope), want)
+    cache.append(*args, q=qkv[:, :4], q_out=qkv[:, :4], **rope)
+    assert torch.equal(qkv[:, :4], want)
+    for bad in (qkv[:, 1:5], qkv[:, 5:9], qkv[:, 7:11]):
+        with pytest.raises(kv.Kv1bError):
+            cache.append(*args, q=qkv[:, :4], q_out=bad, **rope)
+    assert cache.status() == 0
