@@ -408,7 +408,7 @@ size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_
 
 /* Decode attention over a page table: one query token per sequence.
  * q: [num_seqs][num_q_heads][128] contiguous, KV1B_DTYPE_BF16 or _F16, 16-byte aligned; out: the same
- *   shape and type, q itself if the caller likes.  (An fp32 query is KV1B_ERR_UNSUPPORTED: weights and expanded values enter the
+ *   shape and type, q itself if the caller likes or clear of it.  (An fp32 query is KV1B_ERR_UNSUPPORTED: weights and expanded values enter the
  *   tensor cores as binary16, which an fp32 output would promise too much for; kv1b_attend takes it.)
  * lengths: i32 [num_seqs], tokens each sequence holds (the query is the last of them); values below 0
  *   or past max_pages * page_tokens are limited to that range, with KV1B_STATUS_BAD_INDEX.

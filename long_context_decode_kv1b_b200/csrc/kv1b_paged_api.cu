@@ -359,6 +359,10 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(page_table, 4) || !aligned(lengths, 4) ||
       !aligned(prefix_pages, 4) || !aligned(prefix_length, 4))
     return KV1B_ERR_MISALIGNED;
+  // results over the queries, or clear of them: rows are written while others' queries are still read
+  const Wide rows = Wide(num_seqs) * num_q_heads * KV1B_HEAD_DIM * 2;
+  const Wide apart = Wide(reinterpret_cast<uintptr_t>(out)) - Wide(reinterpret_cast<uintptr_t>(q));
+  if (apart != 0 && apart < rows && -apart < rows) return KV1B_ERR_INVALID_ARG;
   if (ws_bytes < (prefix_pages ? kv1b_paged_shared_workspace_bytes(cache, num_seqs, num_q_heads, max_prefix_pages)
                                : kv1b_paged_attend_workspace_bytes(cache, num_q_heads)))
     return KV1B_ERR_WORKSPACE;

@@ -145,6 +145,18 @@ def test_append_refuses_rows_that_meet(lib, change):
     assert lib.kv1b_paged_append(*a.values()) == -1
 
 
+@pytest.mark.parametrize("out", [P + 128 * 2, P + 2 * 8 * 256 - 16, P - 16, P - 2 * 8 * 256 + 16])
+def test_attend_refuses_results_over_a_part_of_the_queries(lib, out):
+    d = desc()
+    a = dict(ATTEND, out=out, ws=2 * P)
+    assert lib.kv1b_paged_attend(ctypes.addressof(d), *a.values()) == -1
+    args = [a[x] for x in ("q", "dtype", "hq", "scale", "seqs")] + [P, 4, P] + \
+           [a[x] for x in ("table", "tstride", "max_pages", "lengths", "out", "ws", "wsb", "stream")]
+    assert lib.kv1b_paged_attend_shared(ctypes.addressof(d), *args) == -1
+    for clear in (P + 2 * 8 * 256, P - 2 * 8 * 256, P):  # these pass on to the workspace's check
+        assert lib.kv1b_paged_attend(ctypes.addressof(d), *dict(ATTEND, out=clear, wsb=64).values()) == -5
+
+
 # ---- the plain forms themselves
 def test_reference_turn_is_a_rotation_by_the_positions_angle():
     rng = np.random.default_rng(0)
