@@ -381,7 +381,8 @@ int kv1b_paged_signs(float* signs, uint64_t seed, int32_t rounds, int32_t* d_sta
  *   Rows past cu_new[num_seqs] (padding) are not touched.
  * page_table: i32, sequence b's page of positions [i page_tokens, (i+1) page_tokens) at
  *   page_table[b*table_stride + i], i < max_pages.
- * rope: NULL for none; positions: i32, token row t on axis a at positions[a*pos_stride + t].
+ * rope: NULL for none; positions: i32, token row t on axis a at positions[a*pos_stride + t] (pos_stride 0:
+ *   the same on every axis, as text's tokens have it).
  * q, q_out: NULL, or the queries (element (t, h, c) at q[t*q_stride_t + h*q_stride_h + c], h <
  *   num_q_heads) and where their turned rows go, in `dtype` (copied when rope is NULL).  q_out may be q
  *   with the same strides.  Otherwise no row of it may share an element with another of its rows or with
@@ -408,8 +409,10 @@ size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_
 
 /* Decode attention over a page table: one query token per sequence.
  * q: [num_seqs][num_q_heads][128] contiguous, KV1B_DTYPE_BF16 or _F16, 16-byte aligned; out: the same
- *   shape and type, q itself if the caller likes or clear of it.  (An fp32 query is KV1B_ERR_UNSUPPORTED: weights and expanded values enter the
- *   tensor cores as binary16, which an fp32 output would promise too much for; kv1b_attend takes it.)
+ *   shape and type, q itself if the caller likes or clear of it.  (An fp32 query is
+ *   KV1B_ERR_UNSUPPORTED: weights and expanded values enter the tensor cores as binary16, which an fp32
+ *   output would promise too much for; kv1b_attend takes it.)
+ * page_table: as kv1b_paged_append; table_stride 0: the same pages for every sequence.
  * lengths: i32 [num_seqs], tokens each sequence holds (the query is the last of them); values below 0
  *   or past max_pages * page_tokens are limited to that range, with KV1B_STATUS_BAD_INDEX.
  * window, sinks: window = 0 sees every token; window > 0 sees token t iff t >= length - window or

@@ -60,9 +60,11 @@ int heads_check(const kv1b_paged_t* c, int32_t num_q_heads) {
   return KV1B_OK;
 }
 
-int table_check(const kv1b_paged_t* c, int32_t num_seqs, int64_t table_stride, int32_t max_pages, int32_t prefix_pages) {
+// `one_for_all`: whether every sequence may have the same pages (a stride of 0).
+int table_check(const kv1b_paged_t* c, int32_t num_seqs, int64_t table_stride, int32_t max_pages, int32_t prefix_pages,
+                bool one_for_all) {
   if (num_seqs < 1 || max_pages < 1 || table_stride < 0 || prefix_pages < 0) return KV1B_ERR_INVALID_ARG;
-  if (num_seqs > 1 && table_stride < max_pages) return KV1B_ERR_INVALID_ARG;
+  if (num_seqs > 1 && table_stride < max_pages && !(one_for_all && table_stride == 0)) return KV1B_ERR_INVALID_ARG;
   if (num_seqs > KV1B_PAGED_MAX_SEQS) return KV1B_ERR_UNSUPPORTED;
   const int64_t bpp = c->page_tokens / KV1B_PAGED_BLOCK_TOKENS;
   const int64_t blocks = num_seqs * bpp * (static_cast<int64_t>(max_pages) + prefix_pages);
@@ -148,7 +150,7 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
                       int64_t qo_stride_t, int64_t qo_stride_h, void* stream) {
   if (!paged_ok(cache) || !k || !v || !dtype_ok(dtype) || num_tokens < 0 || !cu_new || !start || !page_table)
     return KV1B_ERR_INVALID_ARG;
-  const int tc = table_check(cache, num_seqs, table_stride, max_pages, 0);
+  const int tc = table_check(cache, num_seqs, table_stride, max_pages, 0, false);
   if (tc != KV1B_OK) return tc;
   if (k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0) return KV1B_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || k_stride_t % 4 || k_stride_h % 4 || v_stride_t % 4 || v_stride_h % 4)
@@ -161,7 +163,7 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
   memset(&p, 0, sizeof(p));
   if (rope) {
     if (!rope->cos_sin || !positions || rope->num_positions < 1 || rope->rot_dim < 8 || rope->rot_dim > KV1B_HEAD_DIM ||
-        rope->axes < 1 || rope->axes > KV1B_ROPE_MAX_AXES || pos_stride < 0 || (rope->axes > 1 && pos_stride < num_tokens))
+        rope->axes < 1 || rope->axes > KV1B_ROPE_MAX_AXES || pos_stride < 0 || (rope->axes > 1 && pos_stride > 0 && pos_stride < num_tokens))
       return KV1B_ERR_INVALID_ARG;
     if (rope->rot_dim % 8) return KV1B_ERR_UNSUPPORTED;
     int sum = 0;
@@ -338,7 +340,7 @@ size_t shared_carve(kv1b::PagedSharedParams* s, kv1b::PagedAttendParams* p, int3
 size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_seqs, int32_t num_q_heads,
                                          int32_t max_prefix_pages) {
   if (num_seqs < 1 || num_seqs > KV1B_PAGED_MAX_SEQS || max_prefix_pages < 1) return 0;
-  if (!paged_ok(cache) || heads_check(cache, num_q_heads) != KV1B_OK || table_check(cache, 1, 0, 1, max_prefix_pages) != KV1B_OK) return 0;
+  if (!paged_ok(cache) || heads_check(cache, num_q_heads) != KV1B_OK || table_check(cache, 1, 0, 1, max_prefix_pages, true) != KV1B_OK) return 0;
   const int32_t G = num_q_heads / cache->num_kv_heads;
   const int64_t max_tokens = static_cast<int64_t>(max_prefix_pages) * cache->page_tokens;
   kv1b::PagedSharedParams s = shared_plan(cache->num_kv_heads, G, num_seqs, max_tokens);
@@ -353,7 +355,7 @@ static int attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int
   if (q_dtype == KV1B_DTYPE_F32) return KV1B_ERR_UNSUPPORTED;
   const int hc = heads_check(cache, num_q_heads);
   if (hc != KV1B_OK) return hc;
-  const int tc = table_check(cache, num_seqs, table_stride, max_pages, max_prefix_pages);
+  const int tc = table_check(cache, num_seqs, table_stride, max_pages, max_prefix_pages, true);
   if (tc != KV1B_OK) return tc;
   if (!(scale == scale) || window < 0 || sinks < 0) return KV1B_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(page_table, 4) || !aligned(lengths, 4) ||

@@ -157,6 +157,18 @@ def test_attend_refuses_results_over_a_part_of_the_queries(lib, out):
         assert lib.kv1b_paged_attend(ctypes.addressof(d), *dict(ATTEND, out=clear, wsb=64).values()) == -5
 
 
+def test_one_row_for_all(lib):
+    # positions of a stride of 0 and, where it is only read, a page table of one: taken, up to the next check
+    d, r = desc(), rope(axes=3, sections=(ctypes.c_int32 * 3)(32, 16, 16))
+    at, ro = ctypes.addressof(d), ctypes.addressof(r)
+    assert lib.kv1b_paged_append(*dict(APPEND, cache=at, rope=ro, pos=P, pstride=0, num_tokens=0).values()) == 0
+    assert lib.kv1b_paged_append(*dict(APPEND, cache=at, rope=ro, pos=P, pstride=0, q=P).values()) == -1
+    assert lib.kv1b_paged_append(*dict(APPEND, cache=at, rope=ro, pos=P + 2, pstride=0).values()) == -4
+    assert lib.kv1b_paged_append(*dict(APPEND, cache=at, tstride=0).values()) == -1  # two sequences in one page
+    assert lib.kv1b_paged_attend(at, *dict(ATTEND, tstride=0, wsb=64).values()) == -5
+    assert lib.kv1b_paged_attend_shared(at, P, 1, 8, 0.1, 2, P, 4, P, P, 0, 4, P, P, P, 64, None) == -5
+
+
 # ---- the plain forms themselves
 def test_reference_turn_is_a_rotation_by_the_positions_angle():
     rng = np.random.default_rng(0)

@@ -424,3 +424,35 @@ def test_append_refuses_query_rows_that_meet():
         with pytest.raises(kv.Kv1bError):
             cache.append(*args, q=qkv[:, :4], q_out=bad, **rope)
     assert cache.status() == 0
+
+
+def test_one_row_for_all():
+    # text through a three-axis model: positions.expand; samples of one sequence: one page list for all
+    lengths = [200] * 9
+    cache, signs, table, _ = filled([200], 64, 2, 49)
+    one = dev(table)
+    q = torch.randn((9, 4, 128), device="cuda", dtype=torch.float16)
+    n = dev(lengths, torch.int32)
+    out = cache.attend(q, SCALE, one.expand(9, -1), n)
+    assert torch.equal(out, cache.attend(q, SCALE, one.repeat(9, 1), n))
+    check_attend(out, q, cache, signs, SCALE, np.tile(table, (9, 1)), lengths)
+    args = (one[0, :1], dev([30], torch.int32))
+    shared = cache.attend_shared(q, SCALE, *args, one.expand(9, -1), n)
+    assert torch.equal(shared, cache.attend_shared(q, SCALE, *args, one.repeat(9, 1), n))
+    rope = kv.Rope(dev(rope_table(300, 96)), sections=[16, 16, 16])
+    for tokens in (1, 40):
+        k, v, x = torch.randn((3, tokens, 2, 128), device="cuda", dtype=torch.float16)
+        pos = torch.randint(0, 300, (tokens,), dtype=torch.int32, device="cuda")
+        place = (one, dev([0], torch.int32), dev([0, tokens], torch.int32))
+        a = cache.append(k, v, *place, rope=rope, positions=pos.expand(3, tokens), q=x)
+        first = cache.pages.clone()
+        cache.pages.view(torch.int32).random_()
+        cache.pages[table[0]] = 0
+        b = cache.append(k, v, *place, rope=rope, positions=pos.repeat(3, 1), q=x)
+        assert torch.equal(a, b)
+        got, want = ref.fields(cache.pages.cpu().numpy()), ref.fields(first.cpu().numpy())
+        rows = [ref.bit_row(t) for t in range(min(tokens, 32))]
+        assert (got[0][table[0, 0], :, 0][:, rows] == want[0][table[0, 0], :, 0][:, rows]).all()
+    with pytest.raises(kv.Kv1bError):
+        cache.append(k[:9], v[:9], one.expand(9, -1), n, dev(range(10), torch.int32))
+    assert cache.status() == 0
