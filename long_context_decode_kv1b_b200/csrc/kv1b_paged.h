@@ -58,6 +58,7 @@ struct PagedAppendParams {
   int64_t q_st, q_sh, qo_st, qo_sh;
   int32_t Hq;
   int32_t groups;          // bound of the 8-token groups of all sequences
+  int32_t sms;
 };
 
 struct PagedAttendParams {
@@ -89,6 +90,8 @@ struct PagedAttendParams {
   int32_t splits, tile_ns; // the prefix's token ranges, and the time of a tile there
 };
 
+constexpr int kMaxCtas = 192;     // of the attend's kernel: one an SM
+constexpr int kMaxSplits = 148;   // token ranges of a shared prefix
 constexpr int kAttendWarps = 12;  // of a CTA of the attend's kernel
 constexpr int kSegUnits = 8;      // blocks that a segment counts for its start and end
 // Times that the split of a shared call goes by: of the sequences' own tokens a CTA's start and end and a unit of

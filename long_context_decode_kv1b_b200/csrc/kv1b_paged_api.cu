@@ -49,7 +49,7 @@ int num_sms() {
   if (cached[dev] == 0) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    cached[dev] = n;
+    cached[dev] = n < kv1b::kMaxCtas ? n : kv1b::kMaxCtas;
   }
   return cached[dev];
 }
@@ -225,6 +225,7 @@ int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, i
   p.table_stride = table_stride;
   p.max_pages = max_pages;
   p.groups = num_tokens / 8 + 2 * num_seqs;
+  p.sms = num_sms();
   return cuda_status(kv1b_launch_paged_append(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -249,7 +250,7 @@ kv1b::PagedSharedParams shared_plan(int32_t Hkv, int32_t G, int32_t num_seqs, in
   s.row_tiles = (s.R + rows - 1) / rows;
   const int64_t tiles = (max_tokens + 127) / 128, units = static_cast<int64_t>(Hkv) * s.row_tiles, sms = num_sms();
   int64_t best = -1;
-  for (int64_t n = 1; n <= tiles && n <= 148; ++n) {
+  for (int64_t n = 1; n <= tiles && n <= kv1b::kMaxSplits; ++n) {
     const int64_t cost = (units * n + sms - 1) / sms * ((tiles + n - 1) / n + kFixed);
     if (best < 0 || cost < best) {
       best = cost;

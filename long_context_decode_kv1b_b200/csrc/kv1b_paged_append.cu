@@ -795,8 +795,11 @@ static cudaError_t launch_prefill(const PagedAppendParams& p, int heads, cudaStr
 }
 
 cudaError_t kv1b_launch_paged_append(const PagedAppendParams& p, cudaStream_t stream) {
-  // The decode form where hardly a sequence brings a second token: 3.9 against 7.0 us for one token, 5.5 against 7.9
-  // for one of each of 64 sequences, but 15.4 against 8.0 for two of each (8 kv-heads, 32 query heads).
+  // The decode form where hardly a sequence can bring a second token: 3.7 against 6.8 us for one token of each of 4
+  // sequences, 5.4 against 7.6 for 64, 8.5 against 15.4 for 256, but 15.4 against 8.0 for two of each of 64 (8 kv-heads,
+  // 32 query heads).  Which sequences bring them is the device's to know: where one of many slots brings all, its warps
+  // take eight in turn, and the prompts' form would do better: 14.1 against 7.1 us for 64 tokens of one of 64 slots, 15.9
+  // against 8.6 for 256, 30.1 against 21.5 for 1,023.
   if (p.T <= p.B + 1) {
     const int64_t units = 2LL * p.groups * p.c.Hkv + (p.q ? static_cast<int64_t>(p.T) * p.Hq : 0);
     return launch_pdl(paged::paged_append_token_kernel, dim3(static_cast<unsigned>((units + 3) / 4)), dim3(128), 0, stream, p);
@@ -804,7 +807,7 @@ cudaError_t kv1b_launch_paged_append(const PagedAppendParams& p, cudaStream_t st
   // Heads a warp takes in turn, so that their rows can be copied ahead, while every SM still gets its 20 warps more
   // than once: 1, 2, 4 heads take 13.1, 15.1, 21.2 us for 2,048 tokens x 8 heads, 47.1, 45.2, 47.5 for 8,192 and
   // 175.9, 163.4, 156.8 for 32,768.
-  const int64_t share = static_cast<int64_t>(p.groups) * p.c.Hkv / (148 * 28);
+  const int64_t share = static_cast<int64_t>(p.groups) * p.c.Hkv / (p.sms * 28);
   const int heads = share < 1 ? 1 : (share > 4 ? 4 : static_cast<int>(share));
   switch (p.dtype) {
     case KV1B_DTYPE_F32: return launch_prefill<KV1B_DTYPE_F32>(p, heads, stream);

@@ -319,7 +319,8 @@ __device__ __forceinline__ Plan make_plan(const PagedAttendParams& p, uint32_t* 
   return pl;
 }
 
-constexpr int kMaxPieces = 512;  // a row's pieces: CTAs of the split, and 148 token ranges of two lanes
+constexpr int kMaxPieces = 512;  // a row's pieces: CTAs of the split, and the token ranges of two lanes or the CTAs once more
+static_assert(kMaxCtas + 2 * kMaxSplits <= kMaxPieces && 2 * kMaxCtas <= kMaxPieces, "pieces of a merge");
 
 // Log-sum-exp merge of n <= kMaxPieces partial rows by a block of 128 threads.  Warp w takes pieces w, w + 4, ..,
 // kAtOnce of them in flight, two pairs of channels a lane; then the four sums meet.  (A channel a thread and one piece
