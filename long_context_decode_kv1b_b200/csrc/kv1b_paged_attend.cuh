@@ -554,7 +554,7 @@ __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float lo = __fmul_rn(value(i, e, 0), r), hi = __fmul_rn(value(i, e, 1), r);
-              const uint32_t w = kFine ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+              const uint32_t w = kFine ? pack_result_f16(lo, hi) : pack_bf16(lo, hi);
               if (hd < G) {
                 row[16 * i] = static_cast<uint16_t>(w);
                 row[16 * i + 8] = static_cast<uint16_t>(w >> 16);

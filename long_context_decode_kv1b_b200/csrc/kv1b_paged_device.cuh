@@ -159,9 +159,16 @@ __device__ __forceinline__ void load_query(const void* q, int64_t at, int dtype,
     x[r] = dtype == KV1B_DTYPE_BF16 ? __uint_as_float(h[r] << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(h[r])));
 }
 
+// Results as binary16.  They are means of values within +-65504, whose roundings (a weight's 2^-11 against the
+// unrounded normaliser in the shared prefix) may pass that by more than half a step: limited to it.  NaN stays.
+__device__ __forceinline__ uint32_t pack_result_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float x) {
   if (dtype == KV1B_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
-  else static_cast<__half*>(out)[i] = __float2half_rn(x);
+  else static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(pack_result_f16(x, 0.0f));
 }
 
 // ---------------------------------------------------------------------------------------------

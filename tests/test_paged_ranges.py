@@ -456,3 +456,35 @@ def test_one_row_for_all():
     with pytest.raises(kv.Kv1bError):
         cache.append(k[:9], v[:9], one.expand(9, -1), n, dev(range(10), torch.int32))
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("low_halves", [False, True])
+def test_results_at_the_end_of_binary16_stay_finite(low_halves, dtype):
+    # values at both ends of binary16, and equal weights that are rounded all one way against the sum they are divided by:
+    # with low_halves a reference set by 64 lower tokens and 64 higher ones after them in each tile
+    n, H, G, B = 9000, 8, 4, 40
+    cache, signs, pages, q1 = sized_cache(n, H, 1.0, 0.0)
+    share = torch.full((n, 1, 1), 0.2, device="cuda")
+    v = torch.full((n, H, 128), 65504.0, device="cuda")
+    if low_halves:
+        share[torch.arange(n, device="cuda") % 128 < 64] = 0.05
+        v[:, :, 32:64] = v[:, :, 96:] = -65504.0
+    else:
+        share[:64] *= 2
+        v[:, :, 1::2] = -65504.0
+    cache.append(share * q1, v, dev(pages[None]), dev([0], torch.int32), dev([0, n], torch.int32))
+    stored = ref.gather(cache.pages.cpu().numpy(), pages, 0, np.arange(n))[1]
+    assert (stored == stored[:1]).all()  # 65504, or 65416 where a group has both ends: min + 15 steps of 8728
+    q = (torch.linspace(0.1, 0.75 if low_halves else 2, B, device="cuda")[:, None, None, None] * q1[None, :, None].expand(B, H, G, 128)).reshape(B, H * G, 128)
+    wide = np.full((40000 // 64,), -1, np.int32)
+    wide[:len(pages)] = pages
+    tab, none, full, x = dev(np.tile(pages, (B, 1))), dev([0] * B, torch.int32), dev([n] * B, torch.int32), q.to(dtype)
+    for out in (cache.attend_shared(x, SCALE, dev(wide), dev([n], torch.int32), tab, none), cache.attend(x, SCALE, tab, full),
+                cache.attend_shared(x, SCALE, dev(wide[:2]), dev([128], torch.int32), tab[:, 2:].contiguous(), full - 128)):
+        assert torch.isfinite(out).all()
+        # a rounding of the weights against their sum, one of weight scale (a group's values span twice its result at
+        # most), fp32 sums, and the result's type
+        tol = 2.0 ** -11 + 2 * 2.0 ** -11 + 2.0 ** -18 + torch.finfo(dtype).eps / 2
+        assert np.abs(out.double().cpu().numpy() / stored[0] - 1).max() <= tol
+    assert cache.status() == 0
