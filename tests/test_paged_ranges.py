@@ -488,3 +488,65 @@ def test_results_at_the_end_of_binary16_stay_finite(low_halves, dtype):
         tol = 2.0 ** -11 + 2 * 2.0 ** -11 + 2.0 ** -18 + torch.finfo(dtype).eps / 2
         assert np.abs(out.double().cpu().numpy() / stored[0] - 1).max() <= tol
     assert cache.status() == 0
+
+
+# ------------------------------------------------------------------------------------------- wide batches
+@pytest.mark.parametrize("tokens", [1000, 3000])
+def test_append_to_a_thousand_sequences(tokens):
+    # both forms find a token's sequence among 1,000, many of which bring none; query rows turned along
+    rng = np.random.default_rng(14)
+    n = rng.multinomial(tokens, rng.dirichlet(np.full(1000, 0.3)))
+    n[[0, 999]] = 0
+    T = int(n.sum())
+    start = rng.integers(0, 40, 1000).astype(np.int32)
+    counts = [(int(s + x) + 31) // 32 for s, x in zip(start, n)]
+    cache, signs = new_cache(sum(counts) + 1, 1, 32, fill=15)
+    table, _ = table_for(counts, sum(counts) + 1, rng)
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    k, v, q = torch.randn((3, T, 1, 128), device="cuda", dtype=torch.bfloat16)
+    cs, pos = rope_table(200, 128), rng.integers(0, 200, (1, T)).astype(np.int32)
+    before = cache.pages.cpu().numpy()
+    got = cache.append(k, v, dev(table), dev(start), dev(cu), rope=kv.Rope(dev(cs)), positions=dev(pos), q=q)
+    want = ref.append(before, ref.to_np(k), ref.to_np(v), table, start, cu, signs, (cs, [64], False), pos)
+    same_bytes(cache.pages.cpu().numpy(), want)
+    for t in rng.integers(0, T, 50):
+        row = ref.turn(ref.to_np(q[t]), cs, [pos[0, t]], [64], False)
+        assert torch.equal(got[t].cpu(), torch.from_numpy(row).to(q.dtype))
+    assert cache.status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens", [2, 61])
+def test_append_sections_of_any_size(tokens, interleaved, dtype):
+    # axes that change inside four pairs, an axis without pairs, keys and values spread over heads or tokens by strides
+    rng = np.random.default_rng(16)
+    for sections in ([11, 27, 26], [1, 0, 63], [0, 63, 1], [5, 8, 7], [0, 0, 4]):
+        rot = 2 * sum(sections)
+        cache, signs = new_cache(4, 3, 64, fill=17)
+        cs, pos = rope_table(90, rot), rng.integers(0, 90, (3, tokens)).astype(np.int32)
+        k = torch.randn((3, tokens, 128), device="cuda").to(dtype).transpose(0, 1)
+        v = torch.randn((tokens, 1, 128), device="cuda").to(dtype).expand(tokens, 3, 128)
+        q = torch.randn((5, tokens, 132), device="cuda").to(dtype)[:, :, :128].transpose(0, 1)
+        table = np.array([[2, 1]], np.int32)
+        before = cache.pages.cpu().numpy()
+        rope = kv.Rope(dev(cs), sections=sections, interleaved=interleaved)
+        got = cache.append(k, v, dev(table), dev([50], torch.int32), dev([0, tokens], torch.int32), rope=rope, positions=dev(pos), q=q)
+        want = ref.append(before, ref.to_np(k), ref.to_np(v), table, [50], [0, tokens], signs, (cs, sections, interleaved), pos)
+        same_bytes(cache.pages.cpu().numpy(), want, f"sections {sections}")
+        for t in range(tokens):
+            row = ref.turn(ref.to_np(q[t]), cs, pos[:, t], sections, interleaved)
+            assert torch.equal(got[t].cpu(), torch.from_numpy(row).to(dtype)), (sections, t)
+
+
+def test_attend_shared_a_thousand_sequences():
+    # 2,048 rows of a kv-head: eight row tiles, each over the whole prefix
+    rng = np.random.default_rng(18)
+    lengths, prefix = [int(x) for x in rng.integers(0, 33, 1024)], 333
+    cache, signs, table, pre = filled(lengths, 32, 2, 50, prefix=prefix, width=1)
+    q = (2 * torch.randn((1024, 4, 128), device="cuda")).to(torch.bfloat16)
+    args = (q, SCALE, dev(pre), dev([prefix], torch.int32), dev(table), dev(lengths, torch.int32))
+    out = cache.attend_shared(*args)
+    assert cache.status() == 0 and torch.equal(out, cache.attend_shared(*args))
+    check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(lengths[b]), some_rows(rng, 1024, 4, 200),
+               prefix=(pre, np.arange(prefix)))
