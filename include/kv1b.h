@@ -393,7 +393,8 @@ int kv1b_paged_signs(float* signs, uint64_t seed, int32_t rounds, int32_t* d_sta
  * group's scale is one binary16 step lower where min + 15 scale would pass 65504.
  * Skipped, with KV1B_STATUS_BAD_INDEX: tokens whose page is outside [0, num_pages) or past max_pages,
  * tokens with a position outside the rotary table, and all new tokens of a sequence whose cu_new or
- * start entries are not valid.  KV1B_STATUS_NONFINITE / _FP16_SATURATED as kv1b_encode_append.
+ * start entries are not valid (where cu_new does not ascend, tokens of the sequences around it too).
+ * KV1B_STATUS_NONFINITE / _FP16_SATURATED as kv1b_encode_append.
  * Two sequences of one call must not write the same page. */
 int kv1b_paged_append(const kv1b_paged_t* cache, const void* k, const void* v, int32_t dtype, int32_t num_tokens,
                       int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h, int32_t num_seqs,

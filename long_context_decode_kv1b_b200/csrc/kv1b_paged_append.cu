@@ -65,6 +65,18 @@ __device__ __forceinline__ Group find_group(const PagedAppendParams& p, int gi) 
   return g;
 }
 
+// Whether the sequences' rows ascend, by a warp that has nothing else to do.  Where they do not, find_group may pass by a
+// sequence, the one at fault among them, so nobody else would report it.
+__device__ __forceinline__ void check_rows(const PagedAppendParams& p) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  for (int b = lane; b < p.B; b += 32) {
+    const int row0 = __ldg(p.cu + b), row1 = __ldg(p.cu + b + 1);
+    bad |= row0 < 0 || row1 < row0 || row1 > p.T;
+  }
+  if (__any_sync(kFull, bad) && lane == 0 && p.c.status) atomicOr(p.c.status, KV1B_STATUS_BAD_INDEX);
+}
+
 // The block of position `pos` of sequence b and kv-head h, or null (flagged) if its page is not there.
 __device__ __forceinline__ uint8_t* block_of(const PagedAppendParams& p, int b, int h, int64_t pos) {
   const int64_t blk = pos >> 5;
@@ -262,7 +274,7 @@ __device__ __forceinline__ void group_scale(float mn, float mx, uint32_t* scale_
 
 // ---------------------------------------------------------------------------------------------
 // Decode form: one warp per (group, kv-head) and half (key or value), 32 lanes x 4 channels, the
-// group's new tokens one after another (one, in a decode step); then one warp per query row.  The
+// group's new tokens one after another (one, in a decode step); then one warp per query row, and one more.  The
 // chain of dependent loads (cu, start, page, old words) is what a step waits for.
 __global__ void __launch_bounds__(128) paged_append_token_kernel(const PagedAppendParams p) {
   pdl_wait();
@@ -271,8 +283,9 @@ __global__ void __launch_bounds__(128) paged_append_token_kernel(const PagedAppe
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int64_t kv_units = 2LL * p.groups * p.c.Hkv;
   if (unit >= kv_units) {
-    const int64_t r = unit - kv_units;
-    if (!p.q || r >= static_cast<int64_t>(p.T) * p.Hq) return;
+    const int64_t r = unit - kv_units, query_rows = p.q ? static_cast<int64_t>(p.T) * p.Hq : 0;
+    if (r == query_rows) check_rows(p);
+    if (r >= query_rows) return;
     const int64_t t = r / p.Hq;
     if (t >= __ldg(p.cu + p.B)) return;  // rows behind the last sequence
     query_row(p, t, static_cast<int>(r - t * p.Hq));
@@ -516,6 +529,12 @@ __global__ void __launch_bounds__(32 * Prefill<DT>::kWarps, 20 / Prefill<DT>::kW
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tau = lane >> 2, j = lane & 3;
+  // A block behind the others, which costs 32,768 tokens 155.2 against 154.5 us.  (The check by a warp behind the groups
+  // took 159.4 against 150.6, as a call 181.7 against 154.4.)
+  if (blockIdx.x == gridDim.x - 1) {
+    if (warp == 0) check_rows(p);
+    return;
+  }
   // Blocks of keys and values, which are bound by their instructions, and blocks of queries, by memory,
   // are spread evenly among one another: both kinds run on every SM at all times.  kv_share is the keys' share
   // of the blocks in units of 2^-32, rounded up (0: all), and block u theirs where its multiple passes a whole.
@@ -791,7 +810,7 @@ static cudaError_t launch_prefill(const PagedAppendParams& p, int heads, cudaStr
   const int64_t rows = p.q ? static_cast<int64_t>(p.T) * ((p.Hq + paged::kQueryHeads - 1) / paged::kQueryHeads) : 0;
   const int64_t blocks = kv_blocks + (rows + kWarps - 1) / kWarps;  // below 2^30: the API limits the rows
   const uint32_t kv_share = blocks == kv_blocks ? 0u : static_cast<uint32_t>(((kv_blocks << 32) + blocks - 1) / blocks);
-  return launch_pdl(paged::paged_append_prefill_kernel<DT>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), 0, stream, p, kv_share, heads);
+  return launch_pdl(paged::paged_append_prefill_kernel<DT>, dim3(static_cast<unsigned>(blocks + 1)), dim3(32 * kWarps), 0, stream, p, kv_share, heads);
 }
 
 cudaError_t kv1b_launch_paged_append(const PagedAppendParams& p, cudaStream_t stream) {
@@ -802,7 +821,7 @@ cudaError_t kv1b_launch_paged_append(const PagedAppendParams& p, cudaStream_t st
   // against 8.6 for 256, 30.1 against 21.5 for 1,023.
   if (p.T <= p.B + 1) {
     const int64_t units = 2LL * p.groups * p.c.Hkv + (p.q ? static_cast<int64_t>(p.T) * p.Hq : 0);
-    return launch_pdl(paged::paged_append_token_kernel, dim3(static_cast<unsigned>((units + 3) / 4)), dim3(128), 0, stream, p);
+    return launch_pdl(paged::paged_append_token_kernel, dim3(static_cast<unsigned>(units / 4 + 1)), dim3(128), 0, stream, p);
   }
   // Heads a warp takes in turn, so that their rows can be copied ahead, while every SM still gets its 20 warps more
   // than once: 1, 2, 4 heads take 13.1, 15.1, 21.2 us for 2,048 tokens x 8 heads, 47.1, 45.2, 47.5 for 8,192 and

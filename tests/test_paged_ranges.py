@@ -550,3 +550,22 @@ def test_attend_shared_a_thousand_sequences():
     assert cache.status() == 0 and torch.equal(out, cache.attend_shared(*args))
     check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(lengths[b]), some_rows(rng, 1024, 4, 200),
                prefix=(pre, np.arange(prefix)))
+
+
+@pytest.mark.parametrize("cu", [[0, 100, 3, 8], [0, 9, 9, 200], [-1, 3, 5, 9], [0, 60, 59, 120]])
+@pytest.mark.parametrize("copies", [1, 20])
+def test_append_reports_rows_that_do_not_ascend(cu, copies):
+    # wherever the fault is, also at a sequence that no row leads to; both forms, few and many sequences; nothing is
+    # written outside the sequences' places
+    cu = np.concatenate([np.array(cu)] + [np.array(cu[-1:] * 3)] * (copies - 1))
+    B, T = len(cu) - 1, 120
+    for tokens in (T, B + 1):
+        cache, _ = new_cache(5 * B + 2, 1, 32, fill=19)
+        table, spare = table_for([5] * B, 5 * B + 2, np.random.default_rng(20))
+        k = torch.randn((tokens, 1, 128), device="cuda", dtype=torch.float16)
+        before = cache.pages.cpu().numpy()
+        cache.append(k, k, dev(table), dev([0] * B, torch.int32), dev(cu, torch.int32))
+        assert cache.status() == kv.STATUS_BAD_INDEX
+        after = cache.pages.cpu().numpy()
+        same_bytes(after[spare], before[spare])
+        same_bytes(after[table[:, 4]], before[table[:, 4]])
