@@ -569,3 +569,28 @@ def test_append_reports_rows_that_do_not_ascend(cu, copies):
         after = cache.pages.cpu().numpy()
         same_bytes(after[spare], before[spare])
         same_bytes(after[table[:, 4]], before[table[:, 4]])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rounds", [1, 2, 3])
+@pytest.mark.parametrize("group, page", [(3, 32), (7, 256), (8, 4096)])
+def test_attend_after_several_rotation_rounds(rounds, group, page, dtype):
+    # the queries' side of every kernel with 1 to 3 rounds, odd groups, the smallest and the largest page
+    n, H, B = 700, 2, 50
+    num = (n + page - 1) // page
+    cache, signs = new_cache(num + 1, H, page, rounds=rounds, seed=21)
+    k, v = torch.randn((2, n, H, 128), device="cuda")
+    pages = np.random.default_rng(21).permutation(num).astype(np.int32)
+    cache.append(k, v, dev(pages[None]), dev([0], torch.int32), dev([0, n], torch.int32))
+    q = (2 * torch.randn((B, H * group, 128), device="cuda")).to(dtype)
+    table, lengths = np.tile(pages, (B, 1)), [int(x) for x in np.linspace(0, n, B)]
+    rows = some_rows(np.random.default_rng(22), B, H * group, 20)
+    tab, count = dev(table), dev(lengths, torch.int32)
+    out = cache.attend(q, SCALE, tab, count)
+    check_rows(out, q, cache, signs, SCALE, table, lambda b: np.arange(lengths[b]), rows)
+    # 4 rows a kv-head and fewer in the attend's kernel, 150 and more in the matrix kernel
+    for some in (slice(0, 1), slice(0, B)):
+        out = cache.attend_shared(q[some], SCALE, dev(pages), dev([n], torch.int32), tab[some], count[some])
+        check_rows(out, q[some], cache, signs, SCALE, table, lambda b: np.arange(lengths[b]),
+                   [r for r in rows if r[0] < len(out)] + [(0, 1)], prefix=(pages, np.arange(n)))
+    assert cache.status() == 0
