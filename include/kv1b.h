@@ -420,6 +420,9 @@ size_t kv1b_paged_shared_workspace_bytes(const kv1b_paged_t* cache, int32_t num_
  *   t < sinks.
  * Logits and softmax as kv1b_attend.  Zeros for a sequence of length 0.  Blocks whose page is outside
  *   [0, num_pages) count as unseen, with KV1B_STATUS_BAD_INDEX.
+ * Accuracy, of the logits' softmax over the stored values: weights enter the products as binary16 (11 bits
+ *   down to 2^-21 of the row's largest, about), weight x scale as one binary16 for bf16 results and two for
+ *   fp16, at the values' own size, whatever it is; sums are fp32.  fp16 results are limited to +-65504.
  * ws: 256-byte aligned, kv1b_paged_attend_workspace_bytes; written and read within the call only.
  *   Calls that may overlap on the GPU need workspaces of their own. */
 int kv1b_paged_attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
@@ -433,7 +436,9 @@ int kv1b_paged_attend(const kv1b_paged_t* cache, const void* q, int32_t q_dtype,
  * kv1b_paged_attend over the concatenation, but the prefix is read once for the whole batch.
  * max_prefix_pages stands for the prefix's length where the work is split before the device knows it: a
  * table hardly wider than the prefix serves short ones faster.
- * Arguments otherwise as kv1b_paged_attend; either part may be empty. */
+ * Arguments otherwise as kv1b_paged_attend; either part may be empty.  For many rows the prefix's values
+ * are rounded to binary16 once, and its binary16 weights meet a normaliser of unrounded ones: up to 2^-11
+ * of the result more than there. */
 int kv1b_paged_attend_shared(const kv1b_paged_t* cache, const void* q, int32_t q_dtype, int32_t num_q_heads, float scale,
                              int32_t num_seqs, const int32_t* prefix_pages, int32_t max_prefix_pages,
                              const int32_t* prefix_length, const int32_t* page_table, int64_t table_stride,

@@ -2,7 +2,7 @@
 // and launchers.
 //
 // A block holds 32 tokens of one kv-head in 3,200 contiguous bytes, so that one untiled bulk copy
-// brings everything a warp needs for its tokens and a page of any multiple of 32 tokens is a row of
+// brings everything a warp needs for its tokens and a page, a power of two of tokens from 32 on, is a row of
 // blocks.  Inside a block the planes are laid out for the attend's tensor-core fragments:
 //   sign bits  row 8 i + 2 t + e is token 8 t + 2 i + e, so that the eight rows of score product i are
 //              128 contiguous bytes (one ldmatrix) and lane t of a quad receives the logits of tokens

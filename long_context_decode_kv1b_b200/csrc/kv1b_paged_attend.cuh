@@ -33,16 +33,18 @@
 // multiples of it, are below 2 and reach 2^-3.  Those blocks' scales are divided by it in place, and the sums are
 // rescaled where a block needs another unit, up or down (exactly: fp32 by a power of two).  Small values held to
 // unit 1 lost their codes where p scale is below 2^-25: errors of 5.6e-7 for 4,096 tokens of 1e-5 behind one 6 nats
-// above them, a result of 1e-6.  The second test costs 1 % (190.6 and 193.1 us for 1M tokens x 8 heads).
-// p keeps 11 bits down to 2^-21 of the reference (2^7), 2^-17 for the weights that are 2^-4 lower; p scale keeps 11
-// down to 2^-21 of reference times unit; below, both lose at most 2^-25, so a token's code part loses at most 2^-24 of
-// its unit, relative to a reference of weight 1.
+// above them, a result of 1e-6.  The test for them costs 1 to 3 % (1M tokens x 8 heads: 190.6 and 193.1 us over other
+// pages each time, 174 and 179 over the same); where every block is divided, 212 us instead of 180.
+// p keeps 11 bits down to 2^-21 of the reference (2^7), and to 2^-17 for the weights that are 2^-4 lower; p scale, in
+// units, keeps 11 bits while it is 2^-14 or more.  Below, each loses 2^-25 at most: of a token's code part no more than
+// 2^-24 units, relative to a reference of weight 1.
 //
-// 12 warps: their 168 registers hold the loop's sums, operands and addresses, where 16 warps' 128 spilled; 8 warps
-// of 255 hid less of the products' latency (178, 190 and 222 us for 1M tokens x 8 heads).
+// 12 warps: their 168 registers hold the loop's sums, operands and addresses (the fp16 instance, which keeps the
+// weights' remainders too, spills 32 bytes), where 16 warps' 128 spilled; 8 warps of 255 hid less of the products'
+// latency (178, 190 and 222 us for 1M tokens x 8 heads).
 // 609 warp instructions a block (values expanded to binary16 by fma, a page entry and an address per
-// block) became 389: 243 us for 1M tokens x 8 heads became 174, the issue slots 55 % and the ALU 52 % busy;
-// dependencies of fixed latency bound it.
+// block) became 389 and 243 us for 1M tokens x 8 heads 174; with the units 395 and 179, the issue slots 55 % and the ALU
+// 53 % busy: dependencies of fixed latency bound it.
 #pragma once
 #include "kv1b_paged_device.cuh"
 
@@ -123,7 +125,6 @@ __device__ __forceinline__ int next_edge(const Seg& g, int i) {
 constexpr int kCodeBits = 24;  // codes enter the products as binary16 subnormals, units of 2^-24
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
 
-// kFine: the weights of the codes in two binary16 parts (fp16 results); one part is enough for bf16.
 // The query heads of kv-head h that sequence b of the plan serves: G, or up to 8 rows b G' + g of the batch.
 struct Heads {
   int V, G, Hq, B;
@@ -139,6 +140,7 @@ struct Heads {
   }
 };
 
+// kFine: the weights of the codes in two binary16 parts (fp16 results); one part is enough for bf16.
 // `cta` of p.ncta, kThreads threads, kSmem bytes at `smem` (128-byte aligned).
 template <bool kFine, bool kBeside>
 __device__ __forceinline__ void attend_cta(const PagedAttendParams& p, const int G_, const int cta, uint8_t* smem) {
