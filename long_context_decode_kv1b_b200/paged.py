@@ -138,8 +138,9 @@ class PagedCache:
         k, v: [tokens, num_kv_heads, 128] rows of all sequences behind one another (any token and head
         strides that are multiples of 4); cu_new int32 [seqs + 1] says which rows are whose, start int32
         [seqs] how many tokens each sequence holds (not advanced here), page_table int32 [seqs, pages].
-        positions: int32 [tokens], or [axes, tokens] (positions.expand(axes, tokens) where all axes agree).  q [tokens, q heads, 128]: turned alike into q_out
-        (a new contiguous tensor by default; q itself allowed), which is returned."""
+        positions: int32 [tokens], or [axes, tokens] (positions.expand(axes, tokens) where all axes agree).
+        q [tokens, q heads, 128]: turned alike into q_out (a new contiguous tensor by default; q itself
+        allowed, otherwise clear of q, k and v), which is returned."""
         if self._away(stream):
             with self._on(stream):
                 return self.append(k, v, page_table, start, cu_new, rope, positions, q, q_out)

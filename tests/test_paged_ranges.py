@@ -594,3 +594,21 @@ def test_attend_after_several_rotation_rounds(rounds, group, page, dtype):
         check_rows(out, q[some], cache, signs, SCALE, table, lambda b: np.arange(lengths[b]),
                    [r for r in rows if r[0] < len(out)] + [(0, 1)], prefix=(pages, np.arange(n)))
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_fp16_rows_that_are_not_finite_stay_so(bad):
+    # the limit of fp16 results hides no NaN: spoilt queries' rows, all of them and no others, in the three kernels
+    lengths, prefix, page = [90, 5, 33, 700] * 12, 300, 64
+    cache, signs, table, pre = filled(lengths, page, 2, 51, prefix=prefix)
+    q = torch.randn((48, 8, 128), device="cuda", dtype=torch.float16)
+    q[1, 2, 77] = bad
+    q[3, 5] = bad
+    q[13, 0, :] = bad
+    spoilt = torch.zeros((48, 8), dtype=torch.bool, device="cuda")
+    spoilt[1, 2] = spoilt[3, 5] = spoilt[13, 0] = True
+    tab, n, plen = dev(table), dev(lengths, torch.int32), dev([prefix], torch.int32)
+    for out in (cache.attend(q, SCALE, tab, n), cache.attend_shared(q, SCALE, dev(pre), plen, tab, n),
+                cache.attend_shared(q[:4], SCALE, dev(pre), plen, tab[:4], n[:4])):
+        assert torch.equal(torch.isfinite(out).all(-1), ~spoilt[:len(out)])
+        assert torch.equal(torch.isfinite(out).any(-1), ~spoilt[:len(out)])
